@@ -42,7 +42,6 @@ swa_status_t fail(swa_status_t st, const char* fmt, ...) {
   return st;
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 20;  // T (TND) or S (BNSD) limit: 1M rows
 constexpr double kLog2e = 1.4426950408889634;
 
 struct Seq {
@@ -58,9 +57,11 @@ struct Plan {
   int64_t mask_bits = 0;
 };
 
+}  // namespace
+
 // Sequence spans from cumulative ends; a drop (trailing zeros) marks skipped
 // batches (aclnnFlashAttentionUnpaddingScoreGradV2 article §6.4).
-swa_status_t parse_cumulative(const int64_t* cu, int64_t B, int64_t T, const char* name, std::vector<int64_t>& start,
+swa_status_t swa::parse_cumulative(const int64_t* cu, int64_t B, int64_t T, const char* name, std::vector<int64_t>& start,
                               std::vector<int64_t>& len) {
   start.assign(B, 0);
   len.assign(B, 0);
@@ -90,6 +91,11 @@ swa_status_t parse_cumulative(const int64_t* cu, int64_t B, int64_t T, const cha
     return fail(SWA_ERR_PARAM_INVALID, "%s ends at %lld but T = %lld", name, (long long)prev, (long long)T);
   return SWA_OK;
 }
+
+int32_t swa::debug_stall_bits() { return g_stall.load(std::memory_order_relaxed); }
+int64_t swa::debug_extent_slack() { return g_extent_slack.load(std::memory_order_relaxed); }
+
+namespace {
 
 swa_status_t make_plan(const swa_params_t* p, Plan& plan) {
   if (!p) return fail(SWA_ERR_PARAM_NULLPTR, "params is NULL");
@@ -299,8 +305,10 @@ cudaError_t run_tables(const std::vector<SeqDesc>& descs, FS&& small, FL&& large
   return for_each_table<kLargeTable>(descs, 0, descs.size(), large);
 }
 
+}  // namespace
+
 // ------------------------------------------------------------ TMA maps --
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 swa::encode_fn() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   std::call_once(once, [] {
@@ -313,6 +321,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // 128 rows x 64 columns per box, 128-byte swizzle.  BNSD: (d, s, n, b);
 // TND: (d, n, t, 1).

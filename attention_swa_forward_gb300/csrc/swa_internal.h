@@ -6,11 +6,15 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <vector>
 
 #include "swa.h"
 
 namespace swa {
 
+constexpr int64_t kMaxRows = int64_t(1) << 20;  // T (TND) or S (BNSD) limit: 1M rows
 constexpr int kTileM = 128;  // query rows per tile (tcgen05 M)
 constexpr int kTileN = 128;  // key rows per tile
 
@@ -167,6 +171,15 @@ __host__ __device__ constexpr int drop_mode_of(int has_mask, int gen) { return h
 
 // Record `fmt` as the text of swa_last_error() on this thread; returns st.
 swa_status_t set_error(swa_status_t st, const char* fmt, ...);
+
+// Sequence spans from cumulative ends (swa_api.cpp).
+swa_status_t parse_cumulative(const int64_t* cu, int64_t B, int64_t T, const char* name, std::vector<int64_t>& start,
+                              std::vector<int64_t>& len);
+// The driver's tensor map encoder, or NULL.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+// What swa_debug_stall / swa_debug_extent_slack last set.
+int32_t debug_stall_bits();
+int64_t debug_extent_slack();
 
 // Kernel launchers (defined in the .cu files).  Each returns the launch's
 // cudaError_t.

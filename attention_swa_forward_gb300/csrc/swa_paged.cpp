@@ -1,0 +1,693 @@
+// swa_paged.cpp — host side of the rotary and paged-cache operators
+// (include/swa.h): argument checks, split of the work, launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <memory>
+
+#include "swa_paged.h"
+
+using namespace swa;
+
+namespace {
+
+constexpr int64_t kSms = 152;  // SMs of the part this library is built for; sizes grids only
+constexpr int64_t kMaxKv = int64_t(1) << 28;
+constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is below 2^40 bytes
+constexpr double kLog2e = 1.4426950408889634;
+constexpr double kTwoPi = 6.283185307179586;
+
+template <typename... A>
+swa_status_t fail(swa_status_t st, const char* fmt, A... a) {
+  return set_error(st, fmt, a...);
+}
+swa_status_t cuda_fail(cudaError_t e, const char* what) {
+  return set_error(SWA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t less_slack(int64_t extent) { return std::max<int64_t>(extent - debug_extent_slack(), 0); }
+
+// Largest divisor of n that is at most `most`.
+int64_t divisor_up_to(int64_t n, int64_t most) {
+  for (int64_t d = std::min(n, most); d > 1; --d)
+    if (n % d == 0) return d;
+  return 1;
+}
+
+swa_status_t check_heads(int64_t N, int64_t* N_kv, int64_t D) {
+  if (N < 1 || N > 256) return fail(SWA_ERR_PARAM_INVALID, "N must be in [1, 256], got %lld", (long long)N);
+  if (*N_kv == 0) *N_kv = N;
+  if (*N_kv < 1 || *N_kv > 256) return fail(SWA_ERR_PARAM_INVALID, "N_kv must be in [1, 256], got %lld", (long long)*N_kv);
+  if (D < 1 || D > 768) return fail(SWA_ERR_PARAM_INVALID, "D must be in [1, 768], got %lld", (long long)D);
+  if (D % 8 != 0 || D > 128)
+    return fail(SWA_ERR_UNSUPPORTED, "D = %lld is not built (a multiple of 8 up to 128)", (long long)D);
+  return SWA_OK;
+}
+
+swa_status_t check_pointer(const void* p, const char* name) {
+  if (!p) return fail(SWA_ERR_PARAM_NULLPTR, "%s is NULL", name);
+  if (!aligned16(p)) return fail(SWA_ERR_PARAM_INVALID, "%s must be 16-byte aligned", name);
+  return SWA_OK;
+}
+
+// One stride of a dimension of `n` entries: a multiple of 8 elements; `least`
+// apart where the entries must not overlap (0: they may coincide).
+swa_status_t check_stride(int64_t* stride, int64_t n, int64_t least, const char* name, const char* dim) {
+  if (n <= 1) {
+    *stride = 0;  // never used
+    return SWA_OK;
+  }
+  if (*stride < least || *stride > kMaxStride || *stride % 8 != 0)
+    return fail(SWA_ERR_PARAM_INVALID, "%s: %s stride %lld is not a multiple of 8 in [%lld, 2^38]", name, dim,
+                (long long)*stride, (long long)least);
+  return SWA_OK;
+}
+
+// Strides of a [B,N,S,D] / [B*S,N,D] tensor; `extent` its elements from first to last.
+swa_status_t tensor_strides(const swa_strides_t* given, int32_t layout, int64_t B, int64_t S, int64_t N, int64_t D,
+                            bool output, const char* name, swa_strides_t* s, int64_t* extent) {
+  if (layout == SWA_LAYOUT_BNSD) *s = swa_strides_t{N * S * D, D, S * D};
+  else *s = swa_strides_t{S * N * D, N * D, D};
+  if (given) {
+    s->row = given->row;
+    s->head = given->head;
+    if (layout == SWA_LAYOUT_BNSD) s->batch = given->batch;
+  }
+  if (layout == SWA_LAYOUT_TND) {
+    S *= B;
+    B = 1;
+  }
+  const int64_t least = output ? D : 0;
+  swa_status_t st = check_stride(&s->batch, B, least, name, "batch");
+  if (st == SWA_OK) st = check_stride(&s->row, S, least, name, "row");
+  if (st == SWA_OK) st = check_stride(&s->head, N, least, name, "head");
+  if (st != SWA_OK) return st;
+  const long double last = (long double)(B - 1) * s->batch + (long double)(S - 1) * s->row + (long double)(N - 1) * s->head;
+  if (last > (long double)(int64_t(1) << 60)) return fail(SWA_ERR_PARAM_INVALID, "%s: strides too large", name);
+  *extent = (B - 1) * s->batch + (S - 1) * s->row + (N - 1) * s->head + D;
+  return SWA_OK;
+}
+
+// ----------------------------------------------------------------- rotary --
+swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
+  if (!p) return fail(SWA_ERR_PARAM_NULLPTR, "params is NULL");
+  if (p->layout != SWA_LAYOUT_BNSD && p->layout != SWA_LAYOUT_TND)
+    return fail(SWA_ERR_PARAM_INVALID, "layout %d is neither BNSD (0) nor TND (1)", p->layout);
+  *n_kv = p->N_kv;
+  swa_status_t st = check_heads(p->N, n_kv, p->D);
+  if (st != SWA_OK) return st;
+  if (p->B < 1 || p->S < 1 || p->B > (int64_t(1) << 31) || p->S > (int64_t(1) << 31) ||
+      p->B * p->S >= (int64_t(1) << 31))
+    return fail(SWA_ERR_PARAM_INVALID, "B and S must be >= 1 with B * S below 2^31");
+  if (p->dtype != SWA_DTYPE_BF16 && p->dtype != SWA_DTYPE_FP16 && p->dtype != SWA_DTYPE_FP32)
+    return fail(SWA_ERR_PARAM_INVALID, "dtype should be 0 (bf16), 1 (fp16) or 2 (fp32), got %d", p->dtype);
+  if (p->interleaved != 0 && p->interleaved != 1)
+    return fail(SWA_ERR_PARAM_INVALID, "interleaved should be 0 or 1, got %d", p->interleaved);
+  const int64_t R = p->rotary_dim == 0 ? p->D : p->rotary_dim;
+  if (R < 1 || R > p->D) return fail(SWA_ERR_PARAM_INVALID, "rotary_dim must be in [1, D], got %lld", (long long)R);
+  if (R % 8 != 0) return fail(SWA_ERR_UNSUPPORTED, "rotary_dim = %lld is not built (a multiple of 8)", (long long)R);
+  if (p->n_axes < 1 || p->n_axes > 4)
+    return fail(SWA_ERR_PARAM_INVALID, "n_axes must be in [1, 4], got %d", p->n_axes);
+  if (!p->inv_freq && !(p->base > 0.0 && std::isfinite(p->base)))
+    return fail(SWA_ERR_PARAM_INVALID, "base must be positive and finite, got %g", p->base);
+  a = RopeArgs{};
+  a.D = static_cast<int32_t>(p->D);
+  a.R = static_cast<int32_t>(R);
+  a.n_axes = p->n_axes;
+  for (int64_t i = 0; i < R / 2; ++i) {
+    const double f = p->inv_freq ? p->inv_freq[i] : std::pow(p->base, -2.0 * static_cast<double>(i) / static_cast<double>(R));
+    if (!std::isfinite(f) || std::fabs(f) > 1048576.0)
+      return fail(SWA_ERR_PARAM_INVALID, "inv_freq[%lld] = %g is not within 2^20", (long long)i, f);
+    const int32_t ax = p->pair_axis ? p->pair_axis[i] : 0;
+    if (ax < 0 || ax >= p->n_axes)
+      return fail(SWA_ERR_PARAM_INVALID, "pair_axis[%lld] = %d is outside [0, n_axes)", (long long)i, ax);
+    const double turns = f / kTwoPi;
+    double frac = turns - std::floor(turns);
+    if (frac >= 1.0) frac = 0.0;  // a tiny negative angle rounds up to a whole turn
+    a.freq[i] = static_cast<uint64_t>(std::ldexp(frac, 64));
+    a.axis[i] = static_cast<uint8_t>(ax);
+  }
+  return SWA_OK;
+}
+
+// Thread split of the heads named in a.heads: units of 2 * VEC elements.
+void rope_split(RopeArgs& a, int dtype, int64_t rows) {
+  const int vec = rope_vec(dtype, a.R);
+  a.H = a.heads[0] + a.heads[1] + a.heads[2];
+  a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.H - 1) / a.H);
+  a.units = static_cast<int32_t>(ceil_div(a.D, 2 * vec));
+  a.row_lanes = kRopeThreads / a.units;
+  // few tokens: one per CTA, so that every SM has some; many: 16, whose
+  // angles one pass of the CTA's threads computes
+  a.tok = static_cast<int32_t>(std::min<int64_t>(kRopeMaxTok, std::max<int64_t>(1, rows / (4 * kSms))));
+}
+
+swa_status_t rope_call(const swa_rope_params_t* p, const void* q, const swa_strides_t* q_s, const void* k,
+                       const swa_strides_t* k_s, const int32_t* positions, void* q_out, const swa_strides_t* qo_s,
+                       void* k_out, const swa_strides_t* ko_s, int inverse, swa_stream_t stream) {
+  RopeArgs a;
+  int64_t n_kv;
+  swa_status_t st = rope_plan(p, a, &n_kv);
+  if (st != SWA_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (!q && !k) || !positions)
+    return fail(SWA_ERR_PARAM_NULLPTR, "q and q_out, or k and k_out, or both, and positions are required");
+  const bool bnsd = p->layout == SWA_LAYOUT_BNSD;
+  if (reinterpret_cast<uintptr_t>(positions) & 3u)
+    return fail(SWA_ERR_PARAM_INVALID, "positions must be 4-byte aligned");
+  const void* src[2] = {q, k};
+  void* dst[2] = {q_out, k_out};
+  const swa_strides_t* ss[2] = {q_s, k_s};
+  const swa_strides_t* ds[2] = {qo_s, ko_s};
+  const int64_t heads[2] = {p->N, n_kv};
+  const char* names[4] = {"q", "k", "q_out", "k_out"};
+  for (int x = 0; x < 2; ++x) {
+    if (!src[x]) continue;
+    if ((st = check_pointer(src[x], names[x])) != SWA_OK || (st = check_pointer(dst[x], names[2 + x])) != SWA_OK)
+      return st;
+    swa_strides_t s;
+    int64_t n;
+    st = tensor_strides(ss[x], p->layout, p->B, p->S, heads[x], p->D, false, names[x], &s, &n);
+    if (st != SWA_OK) return st;
+    a.src[x] = src[x];
+    a.src_b[x] = s.batch;
+    a.src_r[x] = s.row;
+    a.src_h[x] = s.head;
+    a.n_src[x] = less_slack(n);
+    st = tensor_strides(ds[x], p->layout, p->B, p->S, heads[x], p->D, true, names[2 + x], &s, &n);
+    if (st != SWA_OK) return st;
+    a.dst[x] = dst[x];
+    a.dst_b[x] = s.batch;
+    a.dst_r[x] = s.row;
+    a.dst_h[x] = s.head;
+    a.n_dst[x] = less_slack(n);
+    a.heads[x] = static_cast<int32_t>(heads[x]);
+  }
+  a.inverse = inverse;
+  a.rows = p->B * p->S;
+  a.n_pos = a.rows;
+  a.S = static_cast<int32_t>(bnsd ? p->S : a.rows);
+  a.positions = positions;
+  rope_split(a, p->dtype, a.rows);
+  const cudaError_t e = launch_rope(a, p->dtype, p->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : cuda_fail(e, "rotary launch");
+}
+
+// ------------------------------------------------------------------ paged --
+struct PagedPlan {
+  int64_t N_kv = 0;
+  int64_t max_kv = 0;
+  std::vector<int64_t> start, len;  // per sequence
+  int64_t uniform = 0;              // > 0: the first `n_uniform` sequences have this chunk length, the others none
+  int64_t n_uniform = 0;
+};
+
+swa_status_t paged_plan(const swa_paged_params_t* p, PagedPlan& plan) {
+  if (!p) return fail(SWA_ERR_PARAM_NULLPTR, "params is NULL");
+  plan.N_kv = p->N_kv;
+  swa_status_t st = check_heads(p->N, &plan.N_kv, p->D);
+  if (st != SWA_OK) return st;
+  if (p->N % plan.N_kv != 0)
+    return fail(SWA_ERR_PARAM_INVALID, "N = %lld must be a multiple of N_kv = %lld", (long long)p->N,
+                (long long)plan.N_kv);
+  if (p->dtype == SWA_DTYPE_FP32) return fail(SWA_ERR_UNSUPPORTED, "a paged cache of fp32 is not built");
+  if (p->dtype != SWA_DTYPE_BF16 && p->dtype != SWA_DTYPE_FP16)
+    return fail(SWA_ERR_PARAM_INVALID, "dtype should be 0 (bf16) or 1 (fp16), got %d", p->dtype);
+  if (p->sparse_mode != 0 && p->sparse_mode != 4)
+    return fail(SWA_ERR_PARAM_INVALID, "sparse_mode should be 0 or 4, got %d", p->sparse_mode);
+  if (p->sparse_mode == 4 && (long double)p->pre_tokens + (long double)p->next_tokens < 0)
+    return fail(SWA_ERR_PARAM_INVALID, "pre_tokens + next_tokens < 0: every row would be empty");
+  if (!std::isfinite(p->scale)) return fail(SWA_ERR_PARAM_INVALID, "scale is not finite");
+  if (p->cache_layout != SWA_LAYOUT_BNSD && p->cache_layout != SWA_LAYOUT_TND)
+    return fail(SWA_ERR_PARAM_INVALID, "cache_layout %d is neither BNSD (0) nor TND (1)", p->cache_layout);
+  if (p->num_pages < 1 || p->num_pages > 2147483647)
+    return fail(SWA_ERR_PARAM_INVALID, "num_pages must be in [1, 2^31), got %lld", (long long)p->num_pages);
+  if (p->page_size < 1 || p->page_size > 65536)
+    return fail(SWA_ERR_PARAM_INVALID, "page_size must be in [1, 65536], got %lld", (long long)p->page_size);
+  if (p->page_size % 16 != 0)
+    return fail(SWA_ERR_UNSUPPORTED, "page_size = %lld is not built (a multiple of 16)", (long long)p->page_size);
+  if (p->max_pages < 1 || p->max_pages > (int64_t(1) << 24))
+    return fail(SWA_ERR_PARAM_INVALID, "max_pages must be in [1, 2^24], got %lld", (long long)p->max_pages);
+  if (p->max_kv_len < 0 || p->max_kv_len > kMaxKv)
+    return fail(SWA_ERR_PARAM_INVALID, "max_kv_len must be in [0, 2^28], got %lld", (long long)p->max_kv_len);
+  const int64_t held = std::min(p->max_pages * p->page_size, kMaxKv);
+  plan.max_kv = p->max_kv_len == 0 ? held : std::min(p->max_kv_len, held);
+  if (p->B < 1 || p->B > (int64_t(1) << 20)) return fail(SWA_ERR_PARAM_INVALID, "B must be in [1, 2^20]");
+  if (p->T_q < 1 || p->T_q > kMaxRows)
+    return fail(SWA_ERR_PARAM_INVALID, "T_q must be in [1, %lld]", (long long)kMaxRows);
+  if (!p->cu_seqlens_q) return fail(SWA_ERR_PARAM_NULLPTR, "cu_seqlens_q is NULL");
+  st = parse_cumulative(p->cu_seqlens_q, p->B, p->T_q, "cu_seqlens_q", plan.start, plan.len);
+  if (st != SWA_OK) return st;
+  int64_t n = 0;
+  while (n < p->B && plan.len[n] > 0 && plan.len[n] == plan.len[0]) ++n;
+  if (n > 0 && n * plan.len[0] == p->T_q) {
+    plan.uniform = plan.len[0];
+    plan.n_uniform = n;
+  }
+  return SWA_OK;
+}
+
+swa_status_t page_strides(const swa_page_strides_t* given, const swa_paged_params_t* p, int64_t N_kv, const char* name,
+                          swa_page_strides_t* s, int64_t* extent) {
+  const int64_t P = p->page_size, D = p->D;
+  if (p->cache_layout == SWA_LAYOUT_BNSD) *s = swa_page_strides_t{N_kv * P * D, P * D, D};
+  else *s = swa_page_strides_t{P * N_kv * D, D, N_kv * D};
+  if (given) *s = *given;
+  swa_status_t st = check_stride(&s->page, p->num_pages, D, name, "page");
+  if (st == SWA_OK) st = check_stride(&s->head, N_kv, D, name, "head");
+  if (st == SWA_OK) st = check_stride(&s->slot, P, D, name, "slot");
+  if (st != SWA_OK) return st;
+  const long double last =
+      (long double)(p->num_pages - 1) * s->page + (long double)(N_kv - 1) * s->head + (long double)(P - 1) * s->slot;
+  if (last > (long double)(int64_t(1) << 60)) return fail(SWA_ERR_PARAM_INVALID, "%s: strides too large", name);
+  *extent = (p->num_pages - 1) * s->page + (N_kv - 1) * s->head + (P - 1) * s->slot + D;
+  return SWA_OK;
+}
+
+swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, const void* k_pages,
+                        const swa_page_strides_t* k_s, const void* v_pages, const swa_page_strides_t* v_s,
+                        const int32_t* table, int64_t table_stride, const int32_t* kv_lens, PagedGeom& g) {
+  swa_status_t st;
+  if ((st = check_pointer(k_pages, "k_pages")) != SWA_OK || (st = check_pointer(v_pages, "v_pages")) != SWA_OK)
+    return st;
+  if (!table || !kv_lens) return fail(SWA_ERR_PARAM_NULLPTR, "block_table or kv_lens is NULL");
+  if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u)
+    return fail(SWA_ERR_PARAM_INVALID, "block_table and kv_lens must be 4-byte aligned");
+  if (table_stride == 0) table_stride = p->max_pages;
+  if (table_stride < p->max_pages || table_stride > (int64_t(1) << 40))
+    return fail(SWA_ERR_PARAM_INVALID, "table_stride %lld is below max_pages", (long long)table_stride);
+  g = PagedGeom{};
+  g.N = static_cast<int32_t>(p->N);
+  g.N_kv = static_cast<int32_t>(plan.N_kv);
+  g.D = static_cast<int32_t>(p->D);
+  g.page_size = static_cast<int32_t>(p->page_size);
+  g.num_pages = static_cast<int32_t>(p->num_pages);
+  g.max_pages = static_cast<int32_t>(p->max_pages);
+  g.kv_limit = static_cast<int32_t>(plan.max_kv);
+  g.table_stride = table_stride;
+  g.table = table;
+  g.kv_lens = kv_lens;
+  swa_page_strides_t s;
+  if ((st = page_strides(k_s, p, plan.N_kv, "k_pages", &s, &g.n_k)) != SWA_OK) return st;
+  g.k_page = s.page;
+  g.k_head = s.head;
+  g.k_slot = s.slot;
+  if ((st = page_strides(v_s, p, plan.N_kv, "v_pages", &s, &g.n_v)) != SWA_OK) return st;
+  g.v_page = s.page;
+  g.v_head = s.head;
+  g.v_slot = s.slot;
+  g.n_k = less_slack(g.n_k);
+  g.n_v = less_slack(g.n_v);
+  g.n_table = (p->B - 1) * table_stride + p->max_pages;
+  g.n_lens = p->B;
+  return SWA_OK;
+}
+
+swa_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(SWA_ERR_WORKSPACE, "workspace must be >= %zu bytes and 256-byte aligned (got %zu)", need, bytes);
+  return SWA_OK;
+}
+
+// Launch on the sequences that `take` fills an entry for, at most CAP of them per table.
+template <int CAP, typename Take, typename Launch>
+cudaError_t each_table(const PagedPlan& plan, Take&& take, Launch&& launch) {
+  static thread_local std::unique_ptr<PagedTable<CAP>> storage;
+  if (!storage) storage.reset(new PagedTable<CAP>());
+  PagedTable<CAP>& tab = *storage;
+  std::memset(&tab, 0, sizeof tab);
+  auto flush = [&]() -> cudaError_t {
+    if (tab.count == 0) return cudaSuccess;
+    const cudaError_t e = launch(tab);
+    std::memset(&tab, 0, sizeof tab);
+    return e;
+  };
+  for (size_t b = 0; b < plan.len.size(); ++b) {
+    PagedDesc d{};
+    if (plan.len[b] == 0 || !take(static_cast<int>(b), d, tab)) continue;
+    tab.d[tab.count++] = d;
+    if (tab.count == CAP) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return flush();
+}
+
+int64_t live_sequences(const PagedPlan& plan) {
+  int64_t n = 0;
+  for (int64_t x : plan.len) n += x > 0;
+  return n;
+}
+
+// ----------------------------------------------------------------- append --
+int64_t append_tok(const swa_paged_params_t* p) {
+  return std::min<int64_t>(kRopeMaxTok, std::max<int64_t>(1, p->T_q / (4 * kSms)));
+}
+// CTAs of an append call: each launch covers the tokens of its table's sequences.
+int64_t append_ctas(const swa_paged_params_t* p, const PagedPlan& plan) {
+  const int64_t tok = append_tok(p);
+  if (plan.uniform > 0) return ceil_div(p->T_q, tok);
+  int64_t ctas = 0, count = 0, rows = 0;
+  for (int64_t n : plan.len) {
+    if (n == 0) continue;
+    rows += n;
+    if (++count == kPagedLargeTable) {
+      ctas += ceil_div(rows, tok);
+      count = rows = 0;
+    }
+  }
+  return ctas + ceil_div(rows, tok);
+}
+
+// -------------------------------------------------------------- attention --
+// The row tiles and splits of one kernel over the sequences it takes.
+struct Part {
+  int64_t gs = 1, tok = 1, rows = 0;  // heads and tokens of a tile, rows of a partial
+  int64_t items = 0, splits = 1, min_steps = 1, step = 1;
+  size_t status_at = 0, ml_at = 0, o_at = 0;  // workspace offsets
+};
+struct ForwardPlan {
+  PagedPlan seq;
+  Part rows;
+  size_t total = 0;
+};
+
+swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
+  swa_status_t st = paged_plan(p, f.seq);
+  if (st != SWA_OK) return st;
+  const int64_t G = p->N / f.seq.N_kv, DP = p->D <= 64 ? 64 : 128;
+  f.total = kHeaderBytes;
+  auto lay_out = [&](Part& part, int64_t most_rows, int64_t step, int64_t resident, int64_t min_steps) {
+    part.gs = divisor_up_to(G, most_rows);
+    part.tok = most_rows / part.gs;
+    part.rows = most_rows;
+    part.step = step;
+    part.min_steps = min_steps;
+    part.items = 0;
+    for (int64_t n : f.seq.len) part.items += ceil_div(n, part.tok) * (p->N / part.gs);
+    // keys a tile can see, in steps (one more: a run may begin inside a step)
+    int64_t keys = f.seq.max_kv;
+    if (p->sparse_mode == 4) {
+      const long double w = (long double)p->pre_tokens + (long double)p->next_tokens + (long double)part.tok;
+      if (w < (long double)keys) keys = std::max<int64_t>(1, static_cast<int64_t>(w));
+    }
+    const int64_t steps = ceil_div(keys, step) + 1;
+    part.splits = part.items == 0 ? 1 : std::max<int64_t>(1, std::min(ceil_div(steps, min_steps), ceil_div(resident, part.items)));
+    part.splits = std::min<int64_t>(part.splits, 65535);
+    part.status_at = f.total;
+    f.total += round256(part.items * part.splits * 4);
+    if (part.splits > 1) {
+      const size_t rows = static_cast<size_t>(part.items) * part.splits * part.rows;
+      part.ml_at = f.total;
+      part.o_at = part.ml_at + round256(rows * 8);
+      f.total = part.o_at + round256(rows * DP * 4);
+    }
+  };
+  lay_out(f.rows, kRowsTile, kRowsStep, 4 * 2 * kSms, 2);
+  if (f.rows.items > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many query rows for one call");
+  return SWA_OK;
+}
+
+template <int CAP>
+cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
+                     cudaStream_t s) {
+  a.gs = static_cast<int32_t>(part.gs);
+  a.tok = static_cast<int32_t>(part.tok);
+  a.groups = static_cast<int32_t>(p->N / part.gs);
+  a.splits = static_cast<int32_t>(part.splits);
+  a.min_steps = static_cast<int32_t>(part.min_steps);
+  a.rows_pad = static_cast<int32_t>(part.rows);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
+  a.page_err = reinterpret_cast<int32_t*>(ws + part.status_at);
+  a.part_ml = reinterpret_cast<float2*>(ws + part.ml_at);
+  a.part_o = reinterpret_cast<float*>(ws + part.o_at);
+  auto go = [&](PagedTable<CAP>& tab) {
+    cudaError_t e = launch_paged_rows(a, tab, s);
+    if (e == cudaSuccess && a.splits > 1) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
+    a.item_base += tab.n_items;
+    a.clear_err = 0;
+    return e;
+  };
+  if (f.seq.uniform > 0) {
+    PagedTable<CAP> tab{};
+    tab.count = 1;
+    tab.d[0].q_len = static_cast<int32_t>(f.seq.uniform);
+    tab.d[0].b = -1;
+    tab.d[0].tiles = static_cast<int32_t>(ceil_div(f.seq.uniform, part.tok));
+    tab.n_items = static_cast<int32_t>(part.items);
+    return go(tab);
+  }
+  auto take = [&](int b, PagedDesc& d, PagedTable<CAP>& tab) {
+    d.q_start = static_cast<int32_t>(f.seq.start[b]);
+    d.q_len = static_cast<int32_t>(f.seq.len[b]);
+    d.b = b;
+    d.tiles = static_cast<int32_t>(ceil_div(d.q_len, part.tok));
+    d.item_begin = tab.n_items;
+    tab.n_items += d.tiles * a.groups;
+    return true;
+  };
+  return each_table<CAP>(f.seq, take, go);
+}
+
+swa_status_t read_status(size_t n, const void* workspace, size_t at, swa_stream_t stream) {
+  if (!workspace) return fail(SWA_ERR_PARAM_NULLPTR, "workspace is NULL");
+  swa_status_t st = swa_workspace_status(workspace, stream);
+  if (st != SWA_OK) return st;
+  std::vector<int32_t> host(n);
+  const cudaError_t e =
+      cudaMemcpy(host.data(), static_cast<const uint8_t*>(workspace) + at, n * 4, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the page status");
+  for (int32_t w : host) {
+    if (w == kPageErrLength) return fail(SWA_ERR_PAGE, "an entry of kv_lens is outside [0, max_kv_len]");
+    if (w != 0) return fail(SWA_ERR_PAGE, "an entry of block_table is outside [0, num_pages)");
+  }
+  return SWA_OK;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ ABI --
+extern "C" {
+
+void swa_rope_params_default(swa_rope_params_t* p) {
+  if (!p) return;
+  std::memset(p, 0, sizeof *p);
+  p->n_axes = 1;
+  p->base = 10000.0;
+}
+
+swa_status_t swa_rope_forward(const swa_rope_params_t* p, const void* q, const swa_strides_t* q_strides, const void* k,
+                              const swa_strides_t* k_strides, const int32_t* positions, void* q_out,
+                              const swa_strides_t* q_out_strides, void* k_out, const swa_strides_t* k_out_strides,
+                              swa_stream_t stream) {
+  return rope_call(p, q, q_strides, k, k_strides, positions, q_out, q_out_strides, k_out, k_out_strides, 0, stream);
+}
+
+swa_status_t swa_rope_backward(const swa_rope_params_t* p, const void* dq_out, const swa_strides_t* dq_out_strides,
+                               const void* dk_out, const swa_strides_t* dk_out_strides, const int32_t* positions,
+                               void* dq, const swa_strides_t* dq_strides, void* dk, const swa_strides_t* dk_strides,
+                               swa_stream_t stream) {
+  return rope_call(p, dq_out, dq_out_strides, dk_out, dk_out_strides, positions, dq, dq_strides, dk, dk_strides, 1,
+                   stream);
+}
+
+void swa_paged_params_default(swa_paged_params_t* p) {
+  if (!p) return;
+  std::memset(p, 0, sizeof *p);
+  p->scale = 1.0;
+  p->pre_tokens = 2147483647;
+  p->next_tokens = 2147483647;
+}
+
+swa_status_t swa_paged_append_workspace_size(const swa_paged_params_t* p, size_t* bytes) {
+  if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
+  PagedPlan plan;
+  const swa_status_t st = paged_plan(p, plan);
+  if (st != SWA_OK) return st;
+  *bytes = kHeaderBytes + round256(append_ctas(p, plan) * 4);
+  return SWA_OK;
+}
+
+swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const swa_strides_t* k_strides,
+                              const void* v, const swa_strides_t* v_strides, void* k_pages,
+                              const swa_page_strides_t* k_page_strides, void* v_pages,
+                              const swa_page_strides_t* v_page_strides, const int32_t* block_table,
+                              int64_t table_stride, const int32_t* kv_lens, const swa_rope_params_t* rope,
+                              const int32_t* positions, const void* q, const swa_strides_t* q_strides, void* q_out,
+                              const swa_strides_t* q_out_strides, void* workspace, size_t workspace_bytes,
+                              swa_stream_t stream) {
+  PagedPlan plan;
+  swa_status_t st = paged_plan(p, plan);
+  if (st != SWA_OK) return st;
+  RopeArgs a{};
+  if (rope) {
+    int64_t rope_kv;
+    if ((st = rope_plan(rope, a, &rope_kv)) != SWA_OK) return st;
+    if (rope->layout != SWA_LAYOUT_TND || rope->B * rope->S != p->T_q || rope->N != p->N || rope_kv != plan.N_kv ||
+        rope->D != p->D || rope->dtype != p->dtype)
+      return fail(SWA_ERR_PARAM_INVALID, "rope must be TND with B * S = T_q and the cache's N, N_kv, D and dtype");
+    if (reinterpret_cast<uintptr_t>(positions) & 3u)
+      return fail(SWA_ERR_PARAM_INVALID, "positions must be 4-byte aligned");
+  } else if (positions || q || q_out) {
+    return fail(SWA_ERR_PARAM_INVALID, "positions, q and q_out are taken with rope only");
+  }
+  if ((q == nullptr) != (q_out == nullptr)) return fail(SWA_ERR_PARAM_NULLPTR, "q and q_out come together");
+  if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
+  if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
+  st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.pg);
+  if (st != SWA_OK) return st;
+  const size_t need = kHeaderBytes + round256(append_ctas(p, plan) * 4);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
+
+  a.D = static_cast<int32_t>(p->D);
+  const void* src[3] = {q, k, v};
+  const swa_strides_t* ss[3] = {q_strides, k_strides, v_strides};
+  const int64_t heads[3] = {q ? p->N : 0, plan.N_kv, plan.N_kv};
+  const char* names[3] = {"q", "k", "v"};
+  for (int x = 0; x < 3; ++x) {
+    if (!src[x]) continue;
+    swa_strides_t s;
+    int64_t n;
+    st = tensor_strides(ss[x], SWA_LAYOUT_TND, 1, p->T_q, heads[x], p->D, false, names[x], &s, &n);
+    if (st != SWA_OK) return st;
+    a.src[x] = src[x];
+    a.src_r[x] = s.row;
+    a.src_h[x] = s.head;
+    a.n_src[x] = less_slack(n);
+    a.heads[x] = static_cast<int32_t>(heads[x]);
+  }
+  if (q) {
+    swa_strides_t s;
+    int64_t n;
+    st = tensor_strides(q_out_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q_out", &s, &n);
+    if (st != SWA_OK) return st;
+    a.dst_r[0] = s.row;
+    a.dst_h[0] = s.head;
+    a.n_dst[0] = less_slack(n);
+  }
+  a.dst[0] = q_out;
+  a.dst[1] = k_pages;
+  a.dst[2] = v_pages;
+  a.dst_h[1] = a.pg.k_head;
+  a.dst_h[2] = a.pg.v_head;
+  a.n_dst[1] = a.pg.n_k;
+  a.n_dst[2] = a.pg.n_v;
+  a.S = static_cast<int32_t>(p->T_q);
+  a.n_pos = p->T_q;
+  a.positions = positions;
+  rope_split(a, p->dtype, p->T_q);
+  a.err = static_cast<int32_t*>(workspace);
+  a.page_err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  a.clear_err = SWA_CHECKS ? 0 : 1;
+  if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+  const bool il = rope && rope->interleaved != 0;
+  if (plan.uniform > 0) {
+    PagedTable<kPagedSmallTable> tab{};
+    tab.count = 1;
+    tab.d[0].b = -1;
+    tab.d[0].q_len = static_cast<int32_t>(plan.uniform);
+    a.rows = p->T_q;
+    e = launch_append(a, tab, p->dtype, il, static_cast<int>(ceil_div(p->T_q, a.tok)), s);
+  } else {
+    auto take = [&](int b, PagedDesc& d, auto&) {
+      d.q_start = static_cast<int32_t>(plan.start[b]);
+      d.q_len = static_cast<int32_t>(plan.len[b]);
+      d.b = b;
+      return true;
+    };
+    auto go = [&](auto& tab) {
+      const PagedDesc& last = tab.d[tab.count - 1];
+      a.tok_begin = tab.d[0].q_start;
+      a.rows = last.q_start + last.q_len;
+      const int n = static_cast<int>(ceil_div(a.rows - a.tok_begin, a.tok));
+      const cudaError_t le = launch_append(a, tab, p->dtype, il, n, s);
+      a.page_err += n;
+      a.clear_err = 0;
+      return le;
+    };
+    e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, take, go)
+                                                 : each_table<kPagedLargeTable>(plan, take, go);
+  }
+  return e == cudaSuccess ? SWA_OK : cuda_fail(e, "append launch");
+}
+
+swa_status_t swa_paged_forward_workspace_size(const swa_paged_params_t* p, size_t* bytes) {
+  if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
+  ForwardPlan f;
+  const swa_status_t st = forward_plan(p, f);
+  if (st != SWA_OK) return st;
+  *bytes = f.total;
+  return SWA_OK;
+}
+
+swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const swa_strides_t* q_strides,
+                               const void* k_pages, const swa_page_strides_t* k_page_strides, const void* v_pages,
+                               const swa_page_strides_t* v_page_strides, const int32_t* block_table,
+                               int64_t table_stride, const int32_t* kv_lens, void* out, float* softmax_max,
+                               float* softmax_sum, void* workspace, size_t workspace_bytes, swa_stream_t stream) {
+  ForwardPlan f;
+  swa_status_t st = forward_plan(p, f);
+  if (st != SWA_OK) return st;
+  if ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(out, "out")) != SWA_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(softmax_max) | reinterpret_cast<uintptr_t>(softmax_sum)) & 3u)
+    return fail(SWA_ERR_PARAM_INVALID, "softmax_max and softmax_sum must be 4-byte aligned");
+  PagedArgs a{};
+  st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.g);
+  if (st != SWA_OK) return st;
+  swa_strides_t qs;
+  // the row stride may not fold rows onto each other: tensor maps want it
+  st = tensor_strides(q_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q", &qs, &a.n_q);
+  if (st != SWA_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, f.total)) != SWA_OK) return st;
+  a.n_q = less_slack(a.n_q);
+  a.group = static_cast<int32_t>(p->N / f.seq.N_kv);
+  a.f16 = p->dtype == SWA_DTYPE_FP16 ? 1 : 0;
+  a.sparse_mode = p->sparse_mode;
+  const int64_t lim = int64_t(1) << 29;  // positions stay within +-2^28: no sum passes int32
+  a.pre = static_cast<int32_t>(std::min(std::max(p->pre_tokens, -lim), lim));
+  a.next = static_cast<int32_t>(std::min(std::max(p->next_tokens, -lim), lim));
+  a.scale_log2 = static_cast<float>(p->scale * kLog2e);
+  a.stall = debug_stall_bits();
+  a.q_row = qs.row;
+  a.q_head = qs.head;
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.out = out;
+  a.smax = softmax_max;
+  a.ssum = softmax_sum;
+  a.err = static_cast<int32_t*>(workspace);
+  a.clear_err = SWA_CHECKS ? 0 : 1;
+  a.n_out = less_slack(p->T_q * p->N * p->D);
+  a.n_stats = less_slack(p->T_q * p->N);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+  if (f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable)
+    e = run_part<kPagedSmallTable>(p, f, f.rows, a, s);
+  else
+    e = run_part<kPagedLargeTable>(p, f, f.rows, a, s);
+  return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
+}
+
+swa_status_t swa_paged_append_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
+  PagedPlan plan;
+  const swa_status_t st = paged_plan(p, plan);
+  if (st != SWA_OK) return st;
+  return read_status(append_ctas(p, plan), workspace, kHeaderBytes, stream);
+}
+
+swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
+  ForwardPlan f;
+  const swa_status_t st = forward_plan(p, f);
+  if (st != SWA_OK) return st;
+  return read_status(f.rows.items * f.rows.splits, workspace, f.rows.status_at, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,186 @@
+// swa_paged.h — shapes shared by the host side and the kernels of the rotary
+// and paged-cache operators (include/swa.h, "Rotary positions, a paged
+// key/value cache, and attention over it").
+#pragma once
+#include "swa_internal.h"
+
+#if defined(__CUDACC__)
+#define SWA_PAGED_HD __host__ __device__ __forceinline__
+#else
+#define SWA_PAGED_HD inline
+#endif
+
+namespace swa {
+
+// Sequences of one launch, passed as a kernel parameter.  b < 0: one entry
+// stands for `tiles`-many equal sequences (b = q_start = 0, 1, ... times
+// q_len), which is what a decoding step of any batch size is.
+struct PagedDesc {
+  int32_t q_start, q_len, b;
+  int32_t tiles;       // row tiles per head group (attention)
+  int32_t item_begin;  // first work item of this entry (attention)
+};
+template <int CAP>
+struct PagedTable {
+  int32_t count;    // entries used
+  int32_t n_items;  // work items of this launch (attention)
+  PagedDesc d[CAP];
+};
+
+// The cache and the chunk as a kernel sees them.
+struct PagedGeom {
+  int32_t N, N_kv, D;
+  int32_t page_size, num_pages, max_pages;
+  int32_t kv_limit;  // largest valid kv_lens[b]
+  int64_t table_stride;
+  int64_t k_page, k_head, k_slot;  // strides in elements
+  int64_t v_page, v_head, v_slot;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  // extents of the caller's tensors in elements, for the bounds-checked build
+  int64_t n_k, n_v, n_table, n_lens;
+};
+
+// ------------------------------------------------------- rotary / append --
+constexpr int kRopeMaxTok = 16;  // rows (tokens) per CTA at most
+constexpr int kRopeThreads = 256;
+
+struct RopeArgs {
+  // segments: 0 q, 1 k, 2 v (append only).  heads[s] = 0: absent
+  const void* src[3];
+  void* dst[3];
+  int64_t src_b[3], src_r[3], src_h[3];  // strides: batch, row, head
+  int64_t dst_b[3], dst_r[3], dst_h[3];  // (pages: dst_b / dst_r unused)
+  int64_t n_src[3], n_dst[3];            // extents, for the bounds-checked build
+  int32_t heads[3];
+  int32_t H;          // heads[0] + heads[1] + heads[2]
+  uint32_t h_magic;   // ceil(2^32 / H)
+  int32_t D, R;
+  int32_t units;      // 2 * VEC-element units of a head row
+  int32_t row_lanes;  // rows a CTA takes at a time: threads / units
+  int32_t tok;        // tokens per CTA
+  int32_t n_axes, inverse;
+  int32_t S;          // rows per batch
+  int64_t rows;       // tokens in all
+  int64_t n_pos;      // positions per axis
+  const int32_t* positions;  // NULL (append): the token's position in its sequence
+  PagedGeom pg;       // append only
+  int32_t* err;       // append: status word; else NULL
+  int32_t clear_err;  // append: 1 in the first launch of a call
+  int32_t* page_err;  // append: this launch's per-CTA page status
+  int32_t tok_begin;  // append: first token of this launch
+  uint64_t freq[64];  // angle per position as a fraction of a turn, 2^64 = one turn
+  uint8_t axis[64];
+};
+
+template <int CAP>
+cudaError_t launch_append(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype, bool interleaved, int n_ctas,
+                          cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, cudaStream_t stream);
+// Elements per load: 8 where R is a multiple of 16 (16-byte loads of 16-bit
+// types), else 4; always 4 for fp32.
+inline int rope_vec(int dtype, int64_t R) { return dtype == SWA_DTYPE_FP32 || R % 16 != 0 ? 4 : 8; }
+
+// -------------------------------------------------------------- attention --
+// Row tile: `tok` tokens x `gs` query heads that share one key/value head,
+// row r = token r / gs, head r mod gs of head group vh (heads vh*gs ...).
+struct PagedArgs {
+  PagedGeom g;
+  int32_t gs, tok, groups;  // groups = N / gs head groups
+  int32_t group;            // N / N_kv: head group vh reads key/value head vh * gs / group
+  int32_t f16;
+  int32_t sparse_mode;
+  int32_t pre, next;  // clamped so that position sums stay inside int32
+  float scale_log2;
+  int32_t splits;     // CTAs per item along the keys, at most
+  int32_t min_steps;  // key steps a split takes at least
+  int32_t rows_pad;   // rows of a partial tile
+  int32_t stall;      // test hook (kStallPaged)
+  int64_t q_row, q_head;
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  void* out;
+  float* smax;        // may be NULL
+  float* ssum;        // may be NULL
+  float* part_o;      // [items][splits][rows_pad][DP] (splits > 1)
+  float2* part_ml;    // [items][splits][rows_pad]: maximum (log2 units), sum
+  int32_t item_base;  // items of earlier launches of the call
+  int32_t* err;
+  int32_t clear_err;
+  int32_t* page_err;  // per CTA of the call, [items][splits]
+  int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build
+};
+
+// A resolved work item.
+struct PagedItem {
+  int32_t b, vh, tile, q_start, q_len;
+};
+template <int CAP>
+SWA_PAGED_HD PagedItem resolve_paged(const PagedTable<CAP>& tab, int groups, int k) {
+  int lo = 0, hi = tab.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.d[mid].item_begin <= k) lo = mid; else hi = mid - 1;
+  }
+  const PagedDesc& d = tab.d[lo];
+  const int local = k - d.item_begin;
+  PagedItem it;
+  // sequence, then head group, then tile: the CTAs in flight share a
+  // sequence's pages (its head groups) and a head group's keys (its tiles)
+  const int hg = local / d.tiles;
+  it.tile = local - hg * d.tiles;
+  it.q_len = d.q_len;
+  if (d.b < 0) {
+    it.b = hg / groups;
+    it.vh = hg - it.b * groups;
+    it.q_start = it.b * d.q_len;
+  } else {
+    it.b = d.b;
+    it.vh = hg;
+    it.q_start = d.q_start;
+  }
+  return it;
+}
+
+// Keys that some row of the tile sees, [lo, hi] (empty when lo > hi).  Chunk
+// token i has position kv_len - q_len + i.
+SWA_PAGED_HD void paged_key_range(int sparse_mode, int pre, int next, int kv_len, int q_len, int tok0, int n_tok,
+                                  int* lo, int* hi) {
+  *lo = 0;
+  *hi = kv_len - 1;
+  if (sparse_mode == 4) {
+    const int p0 = kv_len - q_len + tok0, p1 = p0 + n_tok - 1;
+    *lo = p0 - pre > 0 ? p0 - pre : 0;
+    *hi = p1 + next < *hi ? p1 + next : *hi;
+  }
+}
+
+// Key steps of split s: [begin, end) of the item's `steps`; `*active` = splits
+// that have any.
+SWA_PAGED_HD void paged_split(int steps, int splits, int min_steps, int s, int* begin, int* end, int* active) {
+  int per = (steps + splits - 1) / splits;
+  if (per < min_steps) per = min_steps;
+  *active = per > 0 ? (steps + per - 1) / per : 0;
+  *begin = s * per < steps ? s * per : steps;
+  *end = *begin + per < steps ? *begin + per : steps;
+}
+
+constexpr int kRowsTile = 16;     // rows of a tile of the few-row kernel
+constexpr int kRowsStep = 64;     // keys per step of the few-row kernel (4 warps x 16)
+constexpr int kPagedTileRows = 128;  // rows of a tile of the tensor-memory kernel
+constexpr int kPagedTileStep = 128;  // keys per step of it
+
+template <int CAP>
+cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream);
+// Join the splits' partial results; `step_keys` as of the kernel that wrote them.
+template <int CAP>
+cudaError_t launch_paged_join(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream);
+
+constexpr int kPagedSmallTable = 16;
+constexpr int kPagedLargeTable = 512;
+
+// Codes of the per-CTA page status.
+enum : int32_t { kPageErrEntry = 1, kPageErrLength = 2 };
+
+}  // namespace swa

@@ -25,6 +25,7 @@ SWA_ERR_WORKSPACE = 161101
 SWA_ERR_CUDA = 161102
 SWA_ERR_TIMEOUT = 161103
 SWA_ERR_BOUNDS = 161104
+SWA_ERR_PAGE = 161105
 LAYOUTS = {"BNSD": 0, "TND": 1}
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
 
@@ -58,6 +59,61 @@ class SwaParams(ctypes.Structure):
         ("dropout_gen", ctypes.c_int32),
         ("dropout_seed", ctypes.c_uint64),
         ("dropout_offset", ctypes.c_uint64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class SwaStrides(ctypes.Structure):
+    """Mirror of swa_strides_t (elements)."""
+
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class SwaPageStrides(ctypes.Structure):
+    """Mirror of swa_page_strides_t (elements)."""
+
+    _fields_ = [("page", ctypes.c_int64), ("head", ctypes.c_int64), ("slot", ctypes.c_int64)]
+
+
+class SwaRopeParams(ctypes.Structure):
+    """Mirror of swa_rope_params_t."""
+
+    _fields_ = [
+        ("layout", ctypes.c_int32),
+        ("B", ctypes.c_int64),
+        ("S", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("N_kv", ctypes.c_int64),
+        ("rotary_dim", ctypes.c_int64),
+        ("n_axes", ctypes.c_int32),
+        ("pair_axis", ctypes.POINTER(ctypes.c_int32)),
+        ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+        ("base", ctypes.c_double),
+        ("interleaved", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class SwaPagedParams(ctypes.Structure):
+    """Mirror of swa_paged_params_t."""
+
+    _fields_ = [
+        ("B", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("N_kv", ctypes.c_int64),
+        ("T_q", ctypes.c_int64),
+        ("cu_seqlens_q", ctypes.POINTER(ctypes.c_int64)),
+        ("cache_layout", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int64),
+        ("max_pages", ctypes.c_int64),
+        ("max_kv_len", ctypes.c_int64),
+        ("scale", ctypes.c_double),
+        ("pre_tokens", ctypes.c_int64),
+        ("next_tokens", ctypes.c_int64),
+        ("sparse_mode", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
     ]
 
@@ -144,6 +200,29 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.swa_debug_forward_pairs.restype = None
     L.swa_debug_extent_slack.argtypes = [ctypes.c_int64]
     L.swa_debug_extent_slack.restype = None
+    RP, PP = ctypes.POINTER(SwaRopeParams), ctypes.POINTER(SwaPagedParams)
+    i64 = ctypes.c_int64
+    L.swa_rope_params_default.argtypes = [RP]
+    L.swa_rope_params_default.restype = None
+    # (pointers to stride structs go as void pointers: NULL means dense)
+    L.swa_rope_forward.argtypes = [RP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.swa_rope_forward.restype = st
+    L.swa_rope_backward.argtypes = [RP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.swa_rope_backward.restype = st
+    L.swa_paged_params_default.argtypes = [PP]
+    L.swa_paged_params_default.restype = None
+    L.swa_paged_append_workspace_size.argtypes = [PP, ctypes.POINTER(sz)]
+    L.swa_paged_append_workspace_size.restype = st
+    L.swa_paged_append.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, RP, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.swa_paged_append.restype = st
+    L.swa_paged_forward_workspace_size.argtypes = [PP, ctypes.POINTER(sz)]
+    L.swa_paged_forward_workspace_size.restype = st
+    L.swa_paged_forward.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.swa_paged_forward.restype = st
+    L.swa_paged_append_status.argtypes = [PP, vp, vp]
+    L.swa_paged_append_status.restype = st
+    L.swa_paged_forward_status.argtypes = [PP, vp, vp]
+    L.swa_paged_forward_status.restype = st
     L.swa_last_error.argtypes = []
     L.swa_last_error.restype = ctypes.c_char_p
     return L
@@ -154,7 +233,10 @@ def exported_symbols():
             "swa_backward", "swa_backward_noalloc", "swa_workspace_status", "swa_set_timing_events",
             "swa_last_error", "swa_dropout_mask", "swa_step_host_buffer_size", "swa_step_host",
             "swa_step_host_status", "swa_debug_schedule", "swa_debug_stall", "swa_debug_forward_pairs",
-            "swa_debug_extent_slack"]
+            "swa_debug_extent_slack", "swa_rope_params_default", "swa_rope_forward", "swa_rope_backward",
+            "swa_paged_params_default", "swa_paged_append_workspace_size", "swa_paged_append",
+            "swa_paged_forward_workspace_size", "swa_paged_forward", "swa_paged_append_status",
+            "swa_paged_forward_status"]
 
 
 def _check(status: int):
@@ -381,3 +463,266 @@ def check_step_host(geom, chunks, device_buffer, stream=None):
 def check_workspace(workspace, stream=None):
     """Wait for the stream and raise if a kernel gave up a bounded wait."""
     _check(swa_workspace_status(_ptr(workspace), _stream_handle(stream)))
+
+
+# ------------------------------------- rotary positions and the paged cache --
+_TORCH_DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+class RopeParams:
+    """swa_rope_params_t built from a ``workloads.RopeGeometry`` (keeps its host arrays alive).
+    Build it once per shape; the calls below take either."""
+
+    def __init__(self, geom):
+        self.geom = geom
+        self.c = c = SwaRopeParams()
+        lib().swa_rope_params_default(ctypes.byref(c))
+        c.layout = LAYOUTS[geom.layout]
+        c.B, c.S, c.N, c.D, c.N_kv = geom.B, geom.S, geom.N, geom.D, int(geom.N_kv or 0)
+        c.rotary_dim = int(geom.rotary_dim or 0)
+        c.base, c.interleaved, c.dtype = float(geom.base), int(geom.interleaved), DTYPES[geom.dtype]
+        half = (c.rotary_dim or c.D) // 2
+        axes = geom.axes()
+        if len(axes) != half:
+            raise ValueError(f"sections / pair_axis name {len(axes)} pairs, rotary_dim has {half}")
+        c.n_axes = geom.n_axes
+        self._axes = (ctypes.c_int32 * max(half, 1))(*axes)
+        c.pair_axis = ctypes.cast(self._axes, ctypes.POINTER(ctypes.c_int32))
+        if geom.inv_freq is not None:
+            if len(geom.inv_freq) != half:
+                raise ValueError(f"inv_freq names {len(geom.inv_freq)} pairs, rotary_dim has {half}")
+            self._freq = (ctypes.c_double * max(half, 1))(*[float(x) for x in geom.inv_freq])
+            c.inv_freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))
+        self.torch_dtype = _TORCH_DTYPES[geom.dtype]
+        self._ref = ctypes.byref(c)
+        rows = geom.B * geom.S
+        n_kv = geom.n_kv
+        if geom.layout == "BNSD":
+            self.q_shape, self.k_shape = (geom.B, geom.N, geom.S, geom.D), (geom.B, n_kv, geom.S, geom.D)
+        else:
+            self.q_shape, self.k_shape = (rows, geom.N, geom.D), (rows, n_kv, geom.D)
+        self.n_positions = c.n_axes * rows
+
+    def ref(self):
+        return self._ref
+
+
+class PagedParams:
+    """swa_paged_params_t built from a ``workloads.PagedGeometry`` (keeps its host array alive).
+    Build it once per batch composition; the calls below take either."""
+
+    def __init__(self, geom):
+        self.geom = geom
+        self.c = c = SwaPagedParams()
+        lib().swa_paged_params_default(ctypes.byref(c))
+        c.B, c.N, c.D, c.N_kv = geom.B, geom.N, geom.D, int(geom.N_kv or 0)
+        if len(geom.cu_seqlens_q) != geom.B:
+            raise ValueError(f"cu_seqlens_q has {len(geom.cu_seqlens_q)} entries, B = {geom.B}")
+        self._cu = (ctypes.c_int64 * max(geom.B, 1))(*[int(x) for x in geom.cu_seqlens_q])
+        c.cu_seqlens_q = ctypes.cast(self._cu, ctypes.POINTER(ctypes.c_int64))
+        c.T_q = geom.T_q
+        c.cache_layout = LAYOUTS[geom.cache_layout]
+        c.num_pages, c.page_size, c.max_pages = geom.num_pages, geom.page_size, geom.max_pages
+        c.max_kv_len = int(geom.max_kv_len or 0)
+        c.scale, c.sparse_mode = float(geom.scale), int(geom.sparse_mode)
+        c.pre_tokens, c.next_tokens = int(geom.pre_tokens), int(geom.next_tokens)
+        c.dtype = DTYPES[geom.dtype]
+        self.torch_dtype = _TORCH_DTYPES[geom.dtype]
+        self._ref = ctypes.byref(c)
+        self.q_shape, self.kv_shape = (geom.T_q, geom.N, geom.D), (geom.T_q, geom.n_kv, geom.D)
+        self.stat_shape, self.page_shape = (geom.T_q, geom.N), geom.page_shape()
+
+    def ref(self):
+        return self._ref
+
+
+def _rope_params(geom):
+    return geom if isinstance(geom, RopeParams) else RopeParams(geom)
+
+
+def _paged_params(geom):
+    return geom if isinstance(geom, PagedParams) else PagedParams(geom)
+
+
+def _expect(t, name, shape, dtype, device):
+    """A tensor of this shape and type on this device whose last dimension is contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: its last dimension must be contiguous")
+
+
+def _expect_int32(t, name, numel, device):
+    if t.dtype is not torch.int32 or t.device != device or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {numel} contiguous int32 on {device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+
+
+def _strides(t, layout="TND"):
+    """swa_strides_t of a [B,N,S,D] / [T,N,D] tensor, None when dense."""
+    if t.is_contiguous():
+        return None
+    s = t.stride()
+    return ctypes.byref(SwaStrides(s[0], s[2], s[1]) if layout == "BNSD" else SwaStrides(0, s[0], s[1]))
+
+
+def _page_strides(t, layout):
+    if t.is_contiguous():
+        return None
+    s = t.stride()
+    return ctypes.byref(SwaPageStrides(s[0], s[1], s[2]) if layout == "BNSD" else SwaPageStrides(s[0], s[2], s[1]))
+
+
+def _call_on(device, fn, *args, stream=None):
+    """fn(*args, stream handle) with `device` current, on its current stream unless one is given."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _check(fn(*args, s.cuda_stream))
+    with torch.cuda.device(device):
+        return _check(fn(*args, s.cuda_stream))
+
+
+def _rope_call(fn, geom, q, k, positions, q_out, k_out, stream):
+    p = _rope_params(geom)
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k is required")
+    dev, layout = first.device, p.geom.layout
+    outs = []
+    for name, t, out, shape in (("q", q, q_out, p.q_shape), ("k", k, k_out, p.k_shape)):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            outs.append(None)
+            continue
+        _expect(t, name, shape, p.torch_dtype, dev)
+        if out is None:
+            out = torch.empty(shape, dtype=p.torch_dtype, device=dev)
+        else:
+            _expect(out, name + "_out", shape, p.torch_dtype, dev)
+        outs.append(out)
+    _expect_int32(positions, "positions", p.n_positions, dev)
+    st = lambda t: None if t is None else _strides(t, layout)
+    _call_on(dev, fn, p.ref(), _ptr(q), st(q), _ptr(k), st(k), _ptr(positions), _ptr(outs[0]), st(outs[0]),
+             _ptr(outs[1]), st(outs[1]), stream=stream)
+    return outs[0], outs[1]
+
+
+def rope(geom, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Enqueue swa_rope_forward: q and k (either may be None) rotated by their
+    positions (int32, [n_axes, B*S] or [n_axes, B, S]); returns (q_out, k_out).
+    q_out / k_out may be q / k themselves (in place)."""
+    return _rope_call(lib().swa_rope_forward, geom, q, k, positions, q_out, k_out, stream)
+
+
+def rope_backward(geom, dq_out, dk_out, positions, dq=None, dk=None, stream=None):
+    """Enqueue swa_rope_backward: the gradients of rope()'s q and k from those
+    of its results; returns (dq, dk)."""
+    return _rope_call(lib().swa_rope_backward, geom, dq_out, dk_out, positions, dq, dk, stream)
+
+
+def swa_paged_append_workspace_size(params: PagedParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().swa_paged_append_workspace_size(params.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def swa_paged_forward_workspace_size(params: PagedParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().swa_paged_forward_workspace_size(params.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def paged_append_workspace(geom, device="cuda:0"):
+    """A workspace for paged_append calls of this geometry."""
+    return torch.empty(swa_paged_append_workspace_size(_paged_params(geom)), dtype=torch.uint8, device=device)
+
+
+def paged_forward_workspace(geom, device="cuda:0"):
+    """A workspace for paged_forward calls of this geometry."""
+    return torch.empty(swa_paged_forward_workspace_size(_paged_params(geom)), dtype=torch.uint8, device=device)
+
+
+def _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev):
+    _expect(k_pages, "k_pages", p.page_shape, p.torch_dtype, dev)
+    _expect(v_pages, "v_pages", p.page_shape, p.torch_dtype, dev)
+    g = p.geom
+    if block_table.shape != (g.B, g.max_pages) or block_table.dtype is not torch.int32 or block_table.device != dev \
+            or (block_table.stride(1) != 1 and g.max_pages > 1) or (block_table.stride(0) < g.max_pages and g.B > 1):
+        raise ValueError(f"block_table: expected ({g.B}, {g.max_pages}) int32 on {dev} with contiguous rows, got "
+                         f"{tuple(block_table.shape)} {block_table.dtype} on {block_table.device}")
+    _expect_int32(kv_lens, "kv_lens", g.B, dev)
+    return block_table.stride(0) if g.B > 1 else 0
+
+
+def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, positions=None, q=None, q_out=None,
+                 workspace=None, stream=None):
+    """Enqueue swa_paged_append: the chunk's k and v [T_q, N_kv, D] into the
+    pages; with `rope` (a RopeGeometry / RopeParams) k is rotated on the way, and
+    q too, into q_out.  Returns q_out (None without q)."""
+    p = _paged_params(geom)
+    dev = k.device
+    _expect(k, "k", p.kv_shape, p.torch_dtype, dev)
+    _expect(v, "v", p.kv_shape, p.torch_dtype, dev)
+    table_stride = _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev)
+    r = None if rope is None else _rope_params(rope)
+    if positions is not None and r is not None:
+        _expect_int32(positions, "positions", r.n_positions, dev)
+    if q is not None:
+        _expect(q, "q", p.q_shape, p.torch_dtype, dev)
+        if q_out is None:
+            q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=dev)
+    if q_out is not None:
+        _expect(q_out, "q_out", p.q_shape, p.torch_dtype, dev)
+    if workspace is None:
+        workspace = paged_append_workspace(p, dev)
+    layout = p.geom.cache_layout
+    st = lambda t: None if t is None else _strides(t)
+    _call_on(dev, lib().swa_paged_append, p.ref(), _ptr(k), st(k), _ptr(v), st(v), _ptr(k_pages),
+             _page_strides(k_pages, layout), _ptr(v_pages), _page_strides(v_pages, layout), _ptr(block_table),
+             table_stride, _ptr(kv_lens), None if r is None else r.ref(), _ptr(positions), _ptr(q), st(q),
+             _ptr(q_out), st(q_out), _ptr(workspace), workspace.numel(), stream=stream)
+    return q_out
+
+
+def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, softmax_max=None, softmax_sum=None,
+                  workspace=None, stream=None):
+    """Enqueue swa_paged_forward: attention of the chunk's q [T_q, N, D] over
+    the paged cache; returns (out, softmax_max, softmax_sum)."""
+    p = _paged_params(geom)
+    dev = q.device
+    _expect(q, "q", p.q_shape, p.torch_dtype, dev)
+    table_stride = _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev)
+    if out is None:
+        out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=dev)
+    if softmax_max is None:
+        softmax_max = torch.empty(p.stat_shape, dtype=torch.float32, device=dev)
+    if softmax_sum is None:
+        softmax_sum = torch.empty(p.stat_shape, dtype=torch.float32, device=dev)
+    for t, name, shape, dt in ((out, "out", p.q_shape, p.torch_dtype),
+                               (softmax_max, "softmax_max", p.stat_shape, torch.float32),
+                               (softmax_sum, "softmax_sum", p.stat_shape, torch.float32)):
+        if t.shape != shape or t.dtype is not dt or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {tuple(shape)} {dt} on {dev}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+    if workspace is None:
+        workspace = paged_forward_workspace(p, dev)
+    layout = p.geom.cache_layout
+    _call_on(dev, lib().swa_paged_forward, p.ref(), _ptr(q), _strides(q), _ptr(k_pages),
+             _page_strides(k_pages, layout), _ptr(v_pages), _page_strides(v_pages, layout), _ptr(block_table),
+             table_stride, _ptr(kv_lens), _ptr(out), _ptr(softmax_max), _ptr(softmax_sum), _ptr(workspace),
+             workspace.numel(), stream=stream)
+    return out, softmax_max, softmax_sum
+
+
+def check_paged_append(geom, workspace, stream=None):
+    """Wait for the stream and raise what the last paged_append with this workspace met on the device."""
+    _call_on(workspace.device, lib().swa_paged_append_status, _paged_params(geom).ref(), _ptr(workspace),
+             stream=stream)
+
+
+def check_paged_forward(geom, workspace, stream=None):
+    """Wait for the stream and raise what the last paged_forward with this workspace met on the device."""
+    _call_on(workspace.device, lib().swa_paged_forward_status, _paged_params(geom).ref(), _ptr(workspace),
+             stream=stream)

@@ -84,6 +84,80 @@ class Geometry:
 
 
 @dataclass
+class RopeGeometry:
+    """A rotation of q [B,N,S,D] / [B*S,N,D] and k (N_kv heads); see swa_rope_params_t."""
+
+    layout: str
+    B: int
+    S: int
+    N: int
+    D: int
+    N_kv: int = 0  # heads of k; 0 means N
+    rotary_dim: int = 0  # 0 means D
+    sections: list = field(default_factory=list)  # pairs turned by each axis, in order; [] means one axis
+    pair_axis: list | None = None  # instead of sections: the axis of every pair
+    inv_freq: list | None = None  # radians per position of every pair; None: base ** (-2 i / rotary_dim)
+    base: float = 10000.0
+    interleaved: bool = False
+    dtype: str = "bf16"
+
+    @property
+    def n_kv(self) -> int:
+        return self.N_kv or self.N
+
+    def axes(self) -> list:
+        """The axis of every pair."""
+        if self.pair_axis is not None:
+            return list(self.pair_axis)
+        half = (self.rotary_dim or self.D) // 2
+        return [a for a, n in enumerate(self.sections) for _ in range(n)] if self.sections else [0] * half
+
+    @property
+    def n_axes(self) -> int:
+        return max(len(self.sections), max(self.axes()) + 1)
+
+
+@dataclass
+class PagedGeometry:
+    """A chunk of new tokens of B sequences over a paged cache; see swa_paged_params_t."""
+
+    B: int
+    N: int
+    D: int
+    cu_seqlens_q: list  # cumulative chunk ends, no leading 0
+    num_pages: int
+    page_size: int
+    max_pages: int  # block table columns
+    N_kv: int = 0
+    max_kv_len: int = 0  # 0 means max_pages * page_size
+    cache_layout: str = "BNSD"  # a page is [N_kv, page_size, D], or "TND": [page_size, N_kv, D]
+    scale: float = 1.0
+    pre_tokens: int = INT32_MAX
+    next_tokens: int = INT32_MAX
+    sparse_mode: int = 0
+    dtype: str = "bf16"
+
+    @property
+    def n_kv(self) -> int:
+        return self.N_kv or self.N
+
+    @property
+    def T_q(self) -> int:
+        return max(self.cu_seqlens_q)
+
+    def page_shape(self):
+        a = (self.n_kv, self.page_size) if self.cache_layout == "BNSD" else (self.page_size, self.n_kv)
+        return (self.num_pages, *a, self.D)
+
+    def q_lens(self):
+        out, prev = [], 0
+        for e in self.cu_seqlens_q:
+            out.append(max(0, e - prev))
+            prev = e
+        return out
+
+
+@dataclass
 class Workload:
     name: str
     geom: Geometry

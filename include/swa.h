@@ -96,8 +96,11 @@ typedef enum {
   SWA_ERR_WORKSPACE = 161101,     /* workspace NULL or smaller than the size query says */
   SWA_ERR_CUDA = 161102,          /* a CUDA runtime call failed (text in swa_last_error) */
   SWA_ERR_TIMEOUT = 161103,       /* a kernel gave up a bounded wait (swa_workspace_status) */
-  SWA_ERR_BOUNDS = 161104         /* bounds-checked build only: a kernel skipped an access outside its
+  SWA_ERR_BOUNDS = 161104,        /* bounds-checked build only: a kernel skipped an access outside its
                                      tensor (swa_workspace_status) */
+  SWA_ERR_PAGE = 161105           /* a block table entry or a cache length that a paged call read on the
+                                     device is out of range (swa_paged_forward_status,
+                                     swa_paged_append_status) */
 } swa_status_t;
 
 typedef struct {
@@ -259,6 +262,184 @@ SWA_API swa_status_t swa_step_host_status(const swa_params_t *p, int chunks, con
  * SWA_ERR_CUDA. */
 SWA_API swa_status_t swa_dropout_mask(const swa_params_t *p, uint8_t *mask, size_t mask_bytes,
                                       swa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, a paged key/value cache, and attention over it
+ * (additions of this library; the pages have no counterpart): what runs
+ * beside swa_forward when a model with the BAND window is trained or served.
+ *
+ * Rotation.  The first rotary_dim = R elements of every head row are R/2
+ * pairs.  Pair i of the row at integer positions pos[0..n_axes) is turned by
+ * the angle t = pos[pair_axis[i]] * inv_freq[i] (radians):
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ * Pair i is elements (i, i + R/2), or (2i, 2i + 1) when interleaved = 1.
+ * Elements past R are copied.  The backward turns by -t (the transpose of the
+ * rotation).  The angle is formed as pos * inv_freq / 2 pi modulo 1 in 64-bit
+ * fixed point, so positions anywhere in the int32 range keep the accuracy of
+ * small ones; the products are fp32 and rounded once to the element type.
+ *
+ * Every tensor may be strided: a swa_strides_t gives the distances, in
+ * elements, between batches, rows (tokens) and heads; a NULL stands for the
+ * dense layout.  The D elements of a head row are contiguous; tensors start
+ * on 16 bytes and strides are multiples of 8 elements (q and k may so be
+ * slices of one fused projection). */
+typedef struct {
+  int64_t batch, row, head; /* elements; batch is unused for TND */
+} swa_strides_t;
+
+typedef struct {
+  int32_t layout;           /* swa_layout_t: BNSD [B,N,S,D], or TND [B*S,N,D] */
+  int64_t B, S;             /* batch, rows; positions are [n_axes, B*S] */
+  int64_t N, D;             /* heads of q, head dim (8..128, a multiple of 8) */
+  int64_t N_kv;             /* heads of k; 0 (the default) means N_kv = N */
+  int64_t rotary_dim;       /* R, a multiple of 8 up to D; 0 (the default) means D */
+  int32_t n_axes;           /* 1..4, default 1 */
+  const int32_t *pair_axis; /* host, R/2 axis indices, or NULL: every pair on axis 0 */
+  const double *inv_freq;   /* host, R/2 angles per position (radians, finite, |.| <= 2^20), or NULL:
+                               base^(-2i/R) for pair i */
+  double base;              /* default 10000; > 0 and finite */
+  int32_t interleaved;      /* 0 (default): pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+  int32_t dtype;            /* swa_dtype_t of q, k and the results */
+} swa_rope_params_t;
+
+/* Fill `p` with the defaults named above; everything else zero / NULL. */
+SWA_API void swa_rope_params_default(swa_rope_params_t *p);
+
+/* Rotate q and k (either may be NULL, with its result; not both).
+ *   q, k          device, p->dtype, N and N_kv heads
+ *   positions     device, int32 [n_axes, B*S], row b*S + s of a BNSD batch
+ *   q_out, k_out  device, p->dtype; may be q and k themselves with the same
+ *                 strides (in place), must not overlap them otherwise
+ * swa_rope_backward takes the gradients of q_out and k_out and writes those of
+ * q and k.  Neither needs a workspace.
+ * Errors: SWA_ERR_PARAM_NULLPTR, SWA_ERR_PARAM_INVALID, SWA_ERR_UNSUPPORTED,
+ * SWA_ERR_CUDA; nothing is enqueued when a status other than SWA_OK is
+ * returned. */
+SWA_API swa_status_t swa_rope_forward(const swa_rope_params_t *p, const void *q, const swa_strides_t *q_strides,
+                                      const void *k, const swa_strides_t *k_strides, const int32_t *positions,
+                                      void *q_out, const swa_strides_t *q_out_strides, void *k_out,
+                                      const swa_strides_t *k_out_strides, swa_stream_t stream);
+SWA_API swa_status_t swa_rope_backward(const swa_rope_params_t *p, const void *dq_out,
+                                       const swa_strides_t *dq_out_strides, const void *dk_out,
+                                       const swa_strides_t *dk_out_strides, const int32_t *positions, void *dq,
+                                       const swa_strides_t *dq_strides, void *dk, const swa_strides_t *dk_strides,
+                                       swa_stream_t stream);
+
+/* Paged cache.  Keys and values of all sequences live in pages of page_size
+ * tokens.  Token j of sequence b is slot j mod page_size of page
+ * block_table[b][j / page_size].  A page is laid out as its batch entry would
+ * be: cache_layout BNSD [num_pages, N_kv, page_size, D], TND
+ * [num_pages, page_size, N_kv, D]; other strides by a swa_page_strides_t
+ * (multiples of 8 elements; NULL: dense).  Page offsets are 64-bit.
+ *
+ * The new tokens ("chunk") of all sequences are packed TND: q [T_q, N, D] with
+ * the host array cu_seqlens_q as for swa_forward (length-0 sequences and a
+ * trailing run of zeros allowed).  kv_lens[b] (device, so that a captured graph
+ * can be replayed as the sequences grow) is the length of sequence b with its
+ * chunk, q_len_b: chunk token i has position kv_lens[b] - q_len_b + i.  A
+ * token whose position is negative does not exist in the cache (a padded
+ * batch may so give an unused sequence kv_lens[b] = 0): it is not stored, and
+ * its attention follows the formula, the BAND around its position.
+ *
+ * kv_lens and block_table are read on the device.  A length outside
+ * [0, min(max_kv_len, max_pages * page_size)] counts as 0, and a page number
+ * outside [0, num_pages) is never followed: its tokens are not stored, and
+ * read as zero keys and values.  Both are reported by the status calls as
+ * SWA_ERR_PAGE.  Only entries of pages that hold a token of the chunk (append)
+ * or a key that some query of the chunk sees (attention) are looked at: pages
+ * that fell out of the BAND window may be freed and their entries hold
+ * anything.  What a page holds at slots no query of the call sees (past a
+ * sequence's length, before its window) is ignored, NaN and infinity included.
+ * A non-finite key or value that one query of a chunk sees may reach every
+ * query of that chunk. */
+typedef struct {
+  int64_t page, head, slot; /* elements between pages, heads and slots */
+} swa_page_strides_t;
+
+typedef struct {
+  int64_t B, N, D;             /* sequences, query heads, head dim (8..128, a multiple of 8) */
+  int64_t N_kv;                /* key/value heads; 0 (the default) means N_kv = N; N a multiple of N_kv */
+  int64_t T_q;                 /* rows of the packed chunk */
+  const int64_t *cu_seqlens_q; /* host, length B, cumulative ends as in swa_params_t */
+  int32_t cache_layout;        /* swa_layout_t of a page */
+  int64_t num_pages;           /* pages of the cache, 1..2^31 - 1 */
+  int64_t page_size;           /* tokens per page, a multiple of 16 up to 65536 */
+  int64_t max_pages;           /* block table columns, 1..2^24 */
+  int64_t max_kv_len;          /* largest kv_lens[b] of any (re)play of this call, up to 2^28; 0 (the
+                                  default): max_pages * page_size.  How the keys are split over the GPU
+                                  follows from it */
+  double scale;                /* score scale, default 1.0 */
+  int64_t pre_tokens;          /* BAND, around each token's position; defaults 2147483647 */
+  int64_t next_tokens;
+  int32_t sparse_mode;         /* 0 (every cached token is visible) or 4 (BAND) */
+  int32_t dtype;               /* SWA_DTYPE_BF16 (0, default) or SWA_DTYPE_FP16: q, k, v, out and the
+                                  pages.  fp32 is not built (SWA_ERR_UNSUPPORTED) */
+} swa_paged_params_t;
+
+SWA_API void swa_paged_params_default(swa_paged_params_t *p);
+
+/* Store a chunk's keys and values in the cache.
+ *   k, v          device, p->dtype, [T_q, N_kv, D]
+ *   k_pages, v_pages
+ *                 device; only the chunk's slots are written.  Two chunk
+ *                 tokens must not map to one slot
+ *   block_table   device, int32 [B, max_pages], rows table_stride entries
+ *                 apart (0: max_pages)
+ *   kv_lens       device, int32 [B], lengths with the chunk
+ *   rope          NULL, or a rotation applied to k on its way into the cache
+ *                 (layout TND, B*S = T_q, the same N, N_kv, D and dtype); v is
+ *                 never rotated
+ *   positions     device, int32 [n_axes, T_q], or NULL: every axis at the
+ *                 token's position in its sequence (0 where that is negative)
+ *   q, q_out      NULL, or (with rope only) queries [T_q, N, D] rotated along
+ *                 with k into q_out, in the same launch
+ *   workspace     device, >= swa_paged_append_workspace_size bytes, 256-byte
+ *                 aligned; holds the status only
+ * Errors: as swa_rope_forward, plus SWA_ERR_WORKSPACE. */
+SWA_API swa_status_t swa_paged_append_workspace_size(const swa_paged_params_t *p, size_t *bytes);
+SWA_API swa_status_t swa_paged_append(const swa_paged_params_t *p, const void *k, const swa_strides_t *k_strides,
+                                      const void *v, const swa_strides_t *v_strides, void *k_pages,
+                                      const swa_page_strides_t *k_page_strides, void *v_pages,
+                                      const swa_page_strides_t *v_page_strides, const int32_t *block_table,
+                                      int64_t table_stride, const int32_t *kv_lens, const swa_rope_params_t *rope,
+                                      const int32_t *positions, const void *q, const swa_strides_t *q_strides,
+                                      void *q_out, const swa_strides_t *q_out_strides, void *workspace,
+                                      size_t workspace_bytes, swa_stream_t stream);
+
+/* Attention of a chunk over the cache (which holds the chunk's own tokens
+ * too): swa_forward's formula with query i of sequence b at position
+ * p = kv_lens[b] - q_len_b + i, which sees key j iff p - pre_tokens <= j <=
+ * p + next_tokens and 0 <= j < kv_lens[b] (mode 4), or every key (mode 0).  A
+ * row that sees no key gets out = 0, softmax_max = -inf, softmax_sum = 0.
+ *   q             device, p->dtype, [T_q, N, D], may be strided
+ *   k_pages, v_pages, block_table, table_stride, kv_lens
+ *                 as for swa_paged_append; read only
+ *   out           device, p->dtype, dense [T_q, N, D]
+ *   softmax_max, softmax_sum
+ *                 device, fp32 [T_q, N]; either may be NULL
+ *   workspace     device, >= swa_paged_forward_workspace_size bytes, 256-byte
+ *                 aligned: status, and the partial results of keys split over
+ *                 several CTAs.  Needs no initialisation; a workspace may be
+ *                 reused by later calls on the same stream, but not by calls
+ *                 (or replays of graphs) running concurrently
+ * Errors: as swa_forward.  The results do not depend on how the keys were
+ * split beyond fp32 rounding, and are the same bits from run to run. */
+SWA_API swa_status_t swa_paged_forward_workspace_size(const swa_paged_params_t *p, size_t *bytes);
+SWA_API swa_status_t swa_paged_forward(const swa_paged_params_t *p, const void *q, const swa_strides_t *q_strides,
+                                       const void *k_pages, const swa_page_strides_t *k_page_strides,
+                                       const void *v_pages, const swa_page_strides_t *v_page_strides,
+                                       const int32_t *block_table, int64_t table_stride, const int32_t *kv_lens,
+                                       void *out, float *softmax_max, float *softmax_sum, void *workspace,
+                                       size_t workspace_bytes, swa_stream_t stream);
+
+/* Wait for `stream`, then report what the last paged call that used
+ * `workspace` met on the device: SWA_OK, SWA_ERR_PAGE (a length or page number
+ * out of range, see above), SWA_ERR_TIMEOUT, or SWA_ERR_BOUNDS (bounds-checked
+ * build).  `p` as in that call, with the same device current. */
+SWA_API swa_status_t swa_paged_append_status(const swa_paged_params_t *p, const void *workspace,
+                                             swa_stream_t stream);
+SWA_API swa_status_t swa_paged_forward_status(const swa_paged_params_t *p, const void *workspace,
+                                              swa_stream_t stream);
 
 /* Wait for `stream`, then report whether any kernel of the last call that
  * used `workspace` gave up a bounded wait: SWA_OK or SWA_ERR_TIMEOUT
