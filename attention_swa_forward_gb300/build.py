@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "libswa.so")
 CHECKED_BUILD_DIR = os.path.join(PKG, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libswa_checked.so")
 SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_pair.cu", "swa_bwd_dkv.cu", "swa_bwd_dq.cu", "swa_aux.cu",
-           "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged.cpp"]
+           "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged_tile.cu", "swa_paged.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

@@ -704,7 +704,7 @@ swa_status_t swa_debug_schedule(const swa_params_t* p, int32_t pass, int32_t* it
   return SWA_OK;
 }
 
-void swa_debug_stall(int32_t kernels) { g_stall.store(kernels & 7, std::memory_order_relaxed); }
+void swa_debug_stall(int32_t kernels) { g_stall.store(kernels & 15, std::memory_order_relaxed); }
 void swa_debug_extent_slack(int64_t elems) { g_extent_slack.store(std::max<int64_t>(elems, 0), std::memory_order_relaxed); }
 void swa_debug_forward_pairs(int32_t mode) {
   g_fwd_pairs.store(mode >= 0 && mode <= 2 ? mode : 0, std::memory_order_relaxed);

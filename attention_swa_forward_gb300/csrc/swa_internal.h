@@ -130,7 +130,7 @@ struct Geometry {
 };
 
 // Geometry::stall bits.
-enum : int32_t { kStallForward = 1, kStallKeyMajor = 2, kStallQueryMajor = 4 };
+enum : int32_t { kStallForward = 1, kStallKeyMajor = 2, kStallQueryMajor = 4, kStallPaged = 8 };
 
 struct FwdArgs {
   Geometry g;

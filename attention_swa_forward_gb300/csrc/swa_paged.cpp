@@ -248,6 +248,27 @@ swa_status_t paged_plan(const swa_paged_params_t* p, PagedPlan& plan) {
   return SWA_OK;
 }
 
+// The page dimensions by ascending stride (those of one entry last).
+struct PageOrder {
+  int64_t n[3], stride[3];
+  int at[3];  // coordinate (1..3) of slot, head, page
+};
+PageOrder page_order(const swa_page_strides_t& s, const swa_paged_params_t* p, int64_t N_kv) {
+  const int64_t n[3] = {p->page_size, N_kv, p->num_pages}, st[3] = {s.slot, s.head, s.page};
+  int idx[3] = {0, 1, 2};
+  auto key = [&](int x) { return n[x] > 1 ? st[x] : INT64_MAX; };
+  std::stable_sort(idx, idx + 3, [&](int x, int y) { return key(x) < key(y); });
+  PageOrder o{};
+  for (int i = 0; i < 3; ++i) {
+    o.n[i] = n[idx[i]];
+    o.stride[i] = st[idx[i]];
+    // a dimension of one entry: any valid stride
+    if (o.n[i] <= 1) o.stride[i] = i == 0 ? p->D : o.stride[i - 1];
+    o.at[idx[i]] = i + 1;
+  }
+  return o;
+}
+
 swa_status_t page_strides(const swa_page_strides_t* given, const swa_paged_params_t* p, int64_t N_kv, const char* name,
                           swa_page_strides_t* s, int64_t* extent) {
   const int64_t P = p->page_size, D = p->D;
@@ -261,6 +282,11 @@ swa_status_t page_strides(const swa_page_strides_t* given, const swa_paged_param
   const long double last =
       (long double)(p->num_pages - 1) * s->page + (long double)(N_kv - 1) * s->head + (long double)(P - 1) * s->slot;
   if (last > (long double)(int64_t(1) << 60)) return fail(SWA_ERR_PARAM_INVALID, "%s: strides too large", name);
+  const PageOrder o = page_order(*s, p, N_kv);
+  for (int i = 1; i < 3; ++i)
+    if (o.n[i] > 1 && (o.stride[i] % o.stride[i - 1] != 0 || o.stride[i] / o.stride[i - 1] < o.n[i - 1]))
+      return fail(SWA_ERR_UNSUPPORTED, "%s: stride %lld is not a multiple, past %lld entries, of stride %lld", name,
+                  (long long)o.stride[i], (long long)o.n[i - 1], (long long)o.stride[i - 1]);
   *extent = (p->num_pages - 1) * s->page + (N_kv - 1) * s->head + (P - 1) * s->slot + D;
   return SWA_OK;
 }
@@ -301,6 +327,30 @@ swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, cons
   g.n_v = less_slack(g.n_v);
   g.n_table = (p->B - 1) * table_stride + p->max_pages;
   g.n_lens = p->B;
+  return SWA_OK;
+}
+
+// Tensor map of the pages: boxes of `box_rows` slots x 64 columns, 128-byte
+// swizzle; columns past D and pages past the last read as zeros.
+swa_status_t page_map(CUtensorMap* m, PageDims* dims, const void* ptr, const swa_page_strides_t& s,
+                      const swa_paged_params_t* p, int64_t N_kv, int box_rows, const char* name) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const PageOrder o = page_order(s, p, N_kv);
+  cuuint64_t d[4] = {static_cast<cuuint64_t>(p->D)}, st[3];
+  cuuint32_t box[4] = {64, 1, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    d[i + 1] = static_cast<cuuint64_t>(o.n[i]);
+    st[i] = static_cast<cuuint64_t>(o.stride[i]) * 2;
+  }
+  box[o.at[0]] = static_cast<cuuint32_t>(box_rows);
+  *dims = PageDims{o.at[0], o.at[1], o.at[2]};
+  const CUresult r = fn(m, p->dtype == SWA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        4, const_cast<void*>(ptr), d, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", name, (int)r);
   return SWA_OK;
 }
 
@@ -370,23 +420,27 @@ struct Part {
 };
 struct ForwardPlan {
   PagedPlan seq;
-  Part rows;
+  // sequences with at most 16 query rows per key/value head (chunk length x
+  // group), and the others
+  Part rows, tile;
   size_t total = 0;
 };
+bool few_rows(int64_t q_len, int64_t group) { return q_len * group <= kRowsTile; }
 
 swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   swa_status_t st = paged_plan(p, f.seq);
   if (st != SWA_OK) return st;
   const int64_t G = p->N / f.seq.N_kv, DP = p->D <= 64 ? 64 : 128;
   f.total = kHeaderBytes;
-  auto lay_out = [&](Part& part, int64_t most_rows, int64_t step, int64_t resident, int64_t min_steps) {
+  auto lay_out = [&](Part& part, bool few, int64_t most_rows, int64_t step, int64_t resident, int64_t min_steps) {
     part.gs = divisor_up_to(G, most_rows);
     part.tok = most_rows / part.gs;
     part.rows = most_rows;
     part.step = step;
     part.min_steps = min_steps;
     part.items = 0;
-    for (int64_t n : f.seq.len) part.items += ceil_div(n, part.tok) * (p->N / part.gs);
+    for (int64_t n : f.seq.len)
+      if (few_rows(n, G) == few) part.items += ceil_div(n, part.tok) * (p->N / part.gs);
     // keys a tile can see, in steps (one more: a run may begin inside a step)
     int64_t keys = f.seq.max_kv;
     if (p->sparse_mode == 4) {
@@ -405,14 +459,16 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       f.total = part.o_at + round256(rows * DP * 4);
     }
   };
-  lay_out(f.rows, kRowsTile, kRowsStep, 4 * 2 * kSms, 2);
-  if (f.rows.items > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many query rows for one call");
+  lay_out(f.rows, true, kRowsTile, kRowsStep, 4 * 2 * kSms, 2);
+  lay_out(f.tile, false, kPagedTileRows, kPagedTileStep, kSms, 4);
+  if (f.rows.items > 2147483647 || f.tile.items > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many query rows for one call");
   return SWA_OK;
 }
 
 template <int CAP>
 cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
-                     cudaStream_t s) {
+                     const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  const bool few = &part == &f.rows;
   a.gs = static_cast<int32_t>(part.gs);
   a.tok = static_cast<int32_t>(part.tok);
   a.groups = static_cast<int32_t>(p->N / part.gs);
@@ -424,7 +480,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   a.part_ml = reinterpret_cast<float2*>(ws + part.ml_at);
   a.part_o = reinterpret_cast<float*>(ws + part.o_at);
   auto go = [&](PagedTable<CAP>& tab) {
-    cudaError_t e = launch_paged_rows(a, tab, s);
+    cudaError_t e = few ? launch_paged_rows(a, tab, s) : launch_paged_tile(a, tab, mk, mv, s);
     if (e == cudaSuccess && a.splits > 1) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
     a.item_base += tab.n_items;
     a.clear_err = 0;
@@ -440,6 +496,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     return go(tab);
   }
   auto take = [&](int b, PagedDesc& d, PagedTable<CAP>& tab) {
+    if (few_rows(f.seq.len[b], a.group) != few) return false;
     d.q_start = static_cast<int32_t>(f.seq.start[b]);
     d.q_len = static_cast<int32_t>(f.seq.len[b]);
     d.b = b;
@@ -451,10 +508,9 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   return each_table<CAP>(f.seq, take, go);
 }
 
-swa_status_t read_status(size_t n, const void* workspace, size_t at, swa_stream_t stream) {
-  if (!workspace) return fail(SWA_ERR_PARAM_NULLPTR, "workspace is NULL");
-  swa_status_t st = swa_workspace_status(workspace, stream);
-  if (st != SWA_OK) return st;
+// The first page status of n words at `at` that is not 0.
+swa_status_t read_pages(size_t n, const void* workspace, size_t at) {
+  if (n == 0) return SWA_OK;
   std::vector<int32_t> host(n);
   const cudaError_t e =
       cudaMemcpy(host.data(), static_cast<const uint8_t*>(workspace) + at, n * 4, cudaMemcpyDeviceToHost);
@@ -669,25 +725,42 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
   cudaError_t e = cudaSuccess;
   if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
   if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
-  if (f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable)
-    e = run_part<kPagedSmallTable>(p, f, f.rows, a, s);
-  else
-    e = run_part<kPagedLargeTable>(p, f, f.rows, a, s);
+  CUtensorMap mk{}, mv{};
+  if (f.tile.items > 0) {
+    const int64_t low = p->page_size & -p->page_size;
+    a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
+    st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
+                  a.box_rows, "k_pages");
+    if (st == SWA_OK)
+      st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
+                    a.box_rows, "v_pages");
+    if (st != SWA_OK) return st;
+  }
+  const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
+  for (const Part* part : {&f.tile, &f.rows}) {
+    if (part->items == 0 || e != cudaSuccess) continue;
+    e = small ? run_part<kPagedSmallTable>(p, f, *part, a, mk, mv, s)
+              : run_part<kPagedLargeTable>(p, f, *part, a, mk, mv, s);
+    a.clear_err = 0;
+  }
   return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
 }
 
 swa_status_t swa_paged_append_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
   PagedPlan plan;
-  const swa_status_t st = paged_plan(p, plan);
-  if (st != SWA_OK) return st;
-  return read_status(append_ctas(p, plan), workspace, kHeaderBytes, stream);
+  swa_status_t st = paged_plan(p, plan);
+  if (st == SWA_OK) st = swa_workspace_status(workspace, stream);
+  return st == SWA_OK ? read_pages(append_ctas(p, plan), workspace, kHeaderBytes) : st;
 }
 
 swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
   ForwardPlan f;
-  const swa_status_t st = forward_plan(p, f);
+  swa_status_t st = forward_plan(p, f);
   if (st != SWA_OK) return st;
-  return read_status(f.rows.items * f.rows.splits, workspace, f.rows.status_at, stream);
+  st = swa_workspace_status(workspace, stream);
+  for (const Part* part : {&f.rows, &f.tile})
+    if (st == SWA_OK) st = read_pages(part->items * part->splits, workspace, part->status_at);
+  return st;
 }
 
 }  // extern "C"

@@ -82,6 +82,12 @@ cudaError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, cudaStre
 inline int rope_vec(int dtype, int64_t R) { return dtype == SWA_DTYPE_FP32 || R % 16 != 0 ? 4 : 8; }
 
 // -------------------------------------------------------------- attention --
+// Which coordinate (1..3) of a page tensor map is the slot, the head, the
+// page: a map's dimensions go by ascending stride.
+struct PageDims {
+  int32_t slot_at, head_at, page_at;
+};
+
 // Row tile: `tok` tokens x `gs` query heads that share one key/value head,
 // row r = token r / gs, head r mod gs of head group vh (heads vh*gs ...).
 struct PagedArgs {
@@ -96,6 +102,8 @@ struct PagedArgs {
   int32_t min_steps;  // key steps a split takes at least
   int32_t rows_pad;   // rows of a partial tile
   int32_t stall;      // test hook (kStallPaged)
+  int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128
+  PageDims kd, vd;
   int64_t q_row, q_head;
   const void* q;
   const void* k_pages;
@@ -129,7 +137,7 @@ SWA_PAGED_HD PagedItem resolve_paged(const PagedTable<CAP>& tab, int groups, int
   // sequence, then head group, then tile: the CTAs in flight share a
   // sequence's pages (its head groups) and a head group's keys (its tiles)
   const int hg = local / d.tiles;
-  it.tile = local - hg * d.tiles;
+  it.tile = d.tiles - 1 - (local - hg * d.tiles);  // the latest tokens, which see most, first
   it.q_len = d.q_len;
   if (d.b < 0) {
     it.b = hg / groups;
@@ -173,6 +181,9 @@ constexpr int kPagedTileStep = 128;  // keys per step of it
 
 template <int CAP>
 cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream);
+template <int CAP>
+cudaError_t launch_paged_tile(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk,
+                              const CUtensorMap& mv, cudaStream_t stream);
 // Join the splits' partial results; `step_keys` as of the kernel that wrote them.
 template <int CAP>
 cudaError_t launch_paged_join(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream);

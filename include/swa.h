@@ -330,7 +330,9 @@ SWA_API swa_status_t swa_rope_backward(const swa_rope_params_t *p, const void *d
  * block_table[b][j / page_size].  A page is laid out as its batch entry would
  * be: cache_layout BNSD [num_pages, N_kv, page_size, D], TND
  * [num_pages, page_size, N_kv, D]; other strides by a swa_page_strides_t
- * (multiples of 8 elements; NULL: dense).  Page offsets are 64-bit.
+ * (NULL: dense): multiples of 8 elements, and in ascending order each a
+ * multiple of the one before and past all its entries (as a tensor map
+ * needs), so K and V may share one allocation.  Page offsets are 64-bit.
  *
  * The new tokens ("chunk") of all sequences are packed TND: q [T_q, N, D] with
  * the host array cu_seqlens_q as for swa_forward (length-0 sequences and a
@@ -486,7 +488,8 @@ SWA_API void swa_set_timing_events(void *const *events);
  *
  * swa_debug_stall: while `kernels` is non-zero, every later call makes the
  * compute warps of the selected kernels (bit 0 forward, bit 1 key-major
- * dK / dV, bit 2 query-major dQ) first wait on a barrier that nothing
+ * dK / dV, bit 2 query-major dQ, bit 3 swa_paged_forward's kernel for more
+ * than 16 query rows per sequence and key/value head) first wait on a barrier that nothing
  * completes.  That wait gives up after its 2 s limit like any other, the
  * kernel drains its copies and tensor-core work in flight, frees its tensor
  * memory and returns, and swa_workspace_status then reports
