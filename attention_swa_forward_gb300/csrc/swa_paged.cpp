@@ -470,6 +470,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
                      const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   const bool few = &part == &f.rows;
   a.gs = static_cast<int32_t>(part.gs);
+  a.gs_magic = static_cast<uint32_t>(ceil_div(65536, part.gs));
   a.tok = static_cast<int32_t>(part.tok);
   a.groups = static_cast<int32_t>(p->N / part.gs);
   a.splits = static_cast<int32_t>(part.splits);

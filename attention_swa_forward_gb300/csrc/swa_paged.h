@@ -93,6 +93,7 @@ struct PageDims {
 struct PagedArgs {
   PagedGeom g;
   int32_t gs, tok, groups;  // groups = N / gs head groups
+  uint32_t gs_magic;        // ceil(2^16 / gs)
   int32_t group;            // N / N_kv: head group vh reads key/value head vh * gs / group
   int32_t f16;
   int32_t sparse_mode;

@@ -13,13 +13,16 @@
 //  * Packing the G heads of a key/value head into the rows (128 / G tokens per
 //    tile) reads a key tile once for all of them, fills tiles of short chunks,
 //    and cuts the masked part of the tiles at the window's edges by G.
-//  * Warp 4 gathers a key tile from pages: each lane issues one TMA box (up to
-//    128 slots x 64 columns) at the page its own block table entry names, read
-//    one tile ahead.  An entry that is not to be followed becomes the
-//    coordinate past the last page, which TMA fills with zeros.
+//  * Warps 4 and 7 gather the K and the V tiles from pages: each lane issues one
+//    TMA box (up to 128 slots x 64 columns) at the page its own block table
+//    entry names, loaded two tiles ahead.  An entry that is not to be followed
+//    becomes the coordinate past the last page, which TMA fills with zeros.
+//    (One warp for both, waiting for its table entries one tile ahead, took
+//    ~3500 cycles per tile and held everything up: 765 us against 426 of the
+//    dense forward on a causal 8192-token prompt.)
 //  * Q rows are gathered by the softmax warps (any strides; rows past the tile
 //    are zero).
-//  * A key tile at either end of the visible run may hold slots that no row
+//  * A key tile at either end of the chunk's keys may hold slots that no query
 //    sees (stale or never written, possibly NaN): warp 6 zeroes those rows of
 //    V in shared memory, since 0 * NaN would reach O.
 // TMEM columns as in swa_fwd.cu: S0 [0,128), S1 [128,256), O [256,256+D),
@@ -31,7 +34,7 @@ namespace swa {
 namespace {
 
 constexpr int kStages = 3;
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 
 template <int D>
 struct TileSmem {
@@ -50,6 +53,55 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256, kColP = 384;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // as in swa_fwd.cu
+
+// Row r of a tile belongs to its token r / gs (r < 128; gs_magic = ceil(2^16 / gs), exact there).
+__device__ __forceinline__ int row_token(int r, uint32_t gs_magic) { return static_cast<int>((r * gs_magic) >> 16); }
+
+// Where one lane of a gathering warp finds its part of successive key tiles:
+// box `box` (box_rows slots) of the tile, in atom column `atom`.
+struct PageWalk {
+  int entry, slot;    // block table column and first slot of the next tile's box
+  int step_e, step_s;  // 128 slots on
+  int j;              // its first key
+  int lo, hi, box_rows, page_size, num_pages;
+  const int32_t* row;  // the sequence's block table row
+  int64_t left;        // entries of the table from `row` on (bounds-checked build)
+  int32_t* err;
+
+  __device__ __forceinline__ void start(const PagedArgs& a, int b, int j0, int box, int lo_, int hi_) {
+    lo = lo_;
+    hi = hi_;
+    box_rows = a.box_rows;
+    page_size = a.g.page_size;
+    num_pages = a.g.num_pages;
+    j = j0 + box * box_rows;
+    entry = j / page_size;
+    slot = j - entry * page_size;
+    step_e = kPagedTileStep / page_size;
+    step_s = kPagedTileStep - step_e * page_size;
+    row = a.g.table + b * a.g.table_stride;
+    left = a.g.n_table - b * a.g.table_stride;
+    err = a.err;
+  }
+  // The raw entry of the next tile's box and its first slot (num_pages and -1
+  // when no key of it is seen), and on to the tile after.  Nothing waits for
+  // the load here.
+  __device__ __forceinline__ void next(bool mine, int& raw, int& at) {
+    raw = num_pages;
+    at = -1;
+    if (mine && j <= hi && j + box_rows > lo) {
+      at = slot;
+      raw = in_bounds(entry, 1, left, err) ? __ldg(row + entry) : -1;
+    }
+    j += kPagedTileStep;
+    entry += step_e;
+    slot += step_s;
+    if (slot >= page_size) {
+      slot -= page_size;
+      ++entry;
+    }
+  }
+};
 
 template <int D, bool F16, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -83,25 +135,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv_t0 = t_first + st0, n_kv = st1 - st0;
   const int hk = w.vh * a.gs / a.group;  // the key/value head of the tile's rows
 
-  if (warp == 4 && lane == 0) {
-    mbar_init(&s.q_full, kPagedTileRows);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.k_empty[i], 1);
-      mbar_init(&s.v_empty[i], 1);
+  // Q, by the softmax warps: 32 rows each, 16 bytes a lane; rows past the tile
+  // are zero.  Nothing here depends on the cache, so the loads go out first.
+  if (warp < 4) {
+    constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;  // 16 chunks: 2 rows a step; 8: 4 rows
+    const int ch = lane % kChunks;
+    uint4 v[32 / kRowsPer];
+#pragma unroll
+    for (int x = 0; x < 32 / kRowsPer; ++x) {
+      const int rr = warp * 32 + x * kRowsPer + lane / kChunks;
+      const int ii = row_token(rr, a.gs_magic);
+      const int64_t e = static_cast<int64_t>(w.q_start + tok0 + ii) * a.q_row +
+                        static_cast<int64_t>(w.vh * a.gs + rr - ii * a.gs) * a.q_head + ch * 8;
+      v[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < n_rows && ch * 8 < g.D && in_bounds(e, 8, a.n_q, a.err))
+        v[x] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.s_free[i], kPagedTileRows);
-      mbar_init(&s.p_full[i], kPagedTileRows);
+#pragma unroll
+    for (int x = 0; x < 32 / kRowsPer; ++x) st_chunk_sw128(s.q, warp * 32 + x * kRowsPer + lane / kChunks, ch, v[x]);
+    fence_proxy_async_smem();
+  }
+
+  // The gathering warps: lane = (box, atom column).
+  const int box = lane / (D / 64), atom = lane % (D / 64);
+  const bool mine = box < kPagedTileStep / a.box_rows;
+  int bad = bad_len ? kPageErrLength : 0;
+  PageWalk walk;
+  int raw0 = g.num_pages, at0 = -1, raw1 = g.num_pages, at1 = -1;  // entries of this tile and the next
+  auto put = [&](uint8_t* tile, const CUtensorMap* map, const PageDims& pd, uint64_t* bar, int raw, int slot) {
+    int page = raw;
+    if (page < 0 || page > g.num_pages) {
+      bad = max(bad, static_cast<int>(kPageErrEntry));
+      page = g.num_pages;
+    } else if (page == g.num_pages && slot >= 0) {
+      bad = max(bad, static_cast<int>(kPageErrEntry));
     }
-    mbar_init(&s.o_done[0], 1);
-    mbar_init(&s.o_done[1], 1);
-    mbar_init(&s.drain_s, 1);
-    mbar_init(&s.drain_pv, 1);
-    mbar_init(&s.never, 1);
-    fence_mbar_init();
+    slot = max(slot, 0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+    __syncwarp();
+    if (mine) {
+      const int c1 = pd.slot_at == 1 ? slot : (pd.head_at == 1 ? hk : page);
+      const int c2 = pd.slot_at == 2 ? slot : (pd.head_at == 2 ? hk : page);
+      const int c3 = pd.slot_at == 3 ? slot : (pd.head_at == 3 ? hk : page);
+      tma_load_4d(tile + atom * kAtomBytes + box * a.box_rows * 128, map, bar, atom * 64, c1, c2, c3);
+    }
+  };
+  if (warp == 4 || warp == 7) {
+    walk.start(a, w.b, kv_t0 * kPagedTileStep, box, lo, hi);
+    walk.next(mine && n_kv > 0, raw0, at0);
+    walk.next(mine && n_kv > 1, raw1, at1);
+  }
+  if (warp == 4) {
+    if (lane == 0) {
+      mbar_init(&s.q_full, kPagedTileRows);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&s.k_full[i], 1);
+        mbar_init(&s.v_full[i], 1);
+        mbar_init(&s.k_empty[i], 1);
+        mbar_init(&s.v_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s.s_full[i], 1);
+        mbar_init(&s.s_free[i], kPagedTileRows);
+        mbar_init(&s.p_full[i], kPagedTileRows);
+      }
+      mbar_init(&s.o_done[0], 1);
+      mbar_init(&s.o_done[1], 1);
+      mbar_init(&s.drain_s, 1);
+      mbar_init(&s.drain_pv, 1);
+      mbar_init(&s.never, 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
+    __syncwarp();
+    // the first K tile before the CTA-wide barrier, so that its latency runs
+    // while TMEM is allocated
+    if (n_kv > 0) put(s.k[0], &mk, a.kd, &s.k_full[0], raw0, at0);
   }
   if (warp == 5) {
     tmem_alloc(&s.tmem_base, kTmemCols);
@@ -112,74 +222,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = s.tmem_base;
 
-  if (warp == 4) {
-    // ------------------------------------------- producer: pages -> tiles --
-    int bad = bad_len ? kPageErrLength : 0;
-    if (n_kv > 0) {
-      // lane = (box of box_rows slots, atom column): one TMA copy of K and one
-      // of V per lane and tile
-      const int boxes = kPagedTileStep / a.box_rows;
-      const int box = lane / (D / 64), atom = lane % (D / 64);
-      const bool mine = box < boxes;
-      // this lane's page and first slot in key tile `it`; num_pages: zeros
-      auto find = [&](int it, int& page, int& slot) {
-        const int j = (kv_t0 + it) * kPagedTileStep + box * a.box_rows;
-        page = g.num_pages;
-        slot = 0;
-        if (!mine || it >= n_kv || j > hi || j + a.box_rows <= lo) return;
-        const int entry = j / g.page_size;
-        slot = j - entry * g.page_size;
-        const int64_t e = w.b * g.table_stride + entry;
-        const int found = in_bounds(e, 1, g.n_table, a.err) ? __ldg(g.table + e) : -1;
-        if (found >= 0 && found < g.num_pages) page = found;
-        else bad = max(bad, static_cast<int>(kPageErrEntry));
-      };
-      auto load = [&](uint8_t* tile, const CUtensorMap* map, const PageDims& pd, uint64_t* bar, int page, int slot) {
-        if (!mine) return;
-        const int c1 = pd.slot_at == 1 ? slot : (pd.head_at == 1 ? hk : page);
-        const int c2 = pd.slot_at == 2 ? slot : (pd.head_at == 2 ? hk : page);
-        const int c3 = pd.slot_at == 3 ? slot : (pd.head_at == 3 ? hk : page);
-        tma_load_4d(tile + atom * kAtomBytes + box * a.box_rows * 128, map, bar, atom * 64, c1, c2, c3);
-      };
-      if (lane == 0) {
-        tma_prefetch_desc(&mk);
-        tma_prefetch_desc(&mv);
+  if (warp == 4 || warp == 7) {
+    // ------------------------------------------- producers: pages -> tiles --
+    const bool is_k = warp == 4;
+    uint64_t* full = is_k ? s.k_full : s.v_full;
+    uint64_t* empty = is_k ? s.k_empty : s.v_empty;
+    int issued = 0;
+    for (int it = 0; it < n_kv; ++it) {
+      const int st = it % kStages;
+      if (!is_k || it > 0) {  // (K(0) is on its way)
+        if (it >= kStages &&
+            !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (it / kStages - 1) & 1, a.err, kErrFwdLoad)))
+          break;
+        if (is_k) put(s.k[st], &mk, a.kd, &full[st], raw0, at0);
+        else put(s.v[st], &mv, a.vd, &full[st], raw0, at0);
       }
-      int page, slot, page_n, slot_n;
-      find(0, page, slot);
-      int k_issued = 0, v_issued = 0;
-      for (int it = 0; it < n_kv; ++it) {
-        const int st = it % kStages;
-        const uint32_t use = it / kStages;
-        find(it + 1, page_n, slot_n);  // the next tile's entries, in flight behind this tile's copies
-        bool ok = true;
-        if (lane == 0) {
-          if (it >= kStages) ok = mbar_wait(&s.k_empty[st], (use - 1) & 1, a.err, kErrFwdLoad);
-          if (ok) mbar_arrive_expect_tx(&s.k_full[st], kTileBytes);
-        }
-        if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0)) break;
-        load(s.k[st], &mk, a.kd, &s.k_full[st], page, slot);
-        ++k_issued;
-        if (lane == 0) {
-          if (it >= kStages) ok = mbar_wait(&s.v_empty[st], (use - 1) & 1, a.err, kErrFwdLoad);
-          if (ok) mbar_arrive_expect_tx(&s.v_full[st], kTileBytes);
-        }
-        if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0)) break;
-        load(s.v[st], &mv, a.vd, &s.v_full[st], page, slot);
-        ++v_issued;
-        page = page_n;
-        slot = slot_n;
-      }
-      if (lane == 0) {  // every copy issued has landed before the CTA may exit
-        for (int st = 0; st < kStages; ++st) {
-          const int uk = (k_issued - st + kStages - 1) / kStages, uv = (v_issued - st + kStages - 1) / kStages;
-          if (uk > 0) mbar_wait_drain(&s.k_full[st], (uk - 1) & 1);
-          if (uv > 0) mbar_wait_drain(&s.v_full[st], (uv - 1) & 1);
-        }
+      ++issued;
+      raw0 = raw1;
+      at0 = at1;
+      walk.next(mine && it + 2 < n_kv, raw1, at1);
+    }
+    if (lane == 0) {  // every copy issued has landed before the CTA may exit
+      for (int st = 0; st < kStages; ++st) {
+        const int uses = (issued - st + kStages - 1) / kStages;
+        if (uses > 0) mbar_wait_drain(&full[st], (uses - 1) & 1);
       }
     }
     bad = __reduce_max_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) a.page_err[slot_id] = bad;
+    if (is_k && lane == 0) a.page_err[slot_id] = bad;
   } else if (warp == 5) {
     // ------------------------------------------------ S = Q K^T issuer --
     if (lane == 0 && n_kv > 0) {
@@ -209,13 +279,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- O += P V issuer --
     if (n_kv > 0) {
       constexpr uint32_t kIdO = idesc_f16_f32(kTileM, D, false, true, F16);
+      int seen_lo, seen_hi;
+      paged_key_range(a.sparse_mode, a.pre, a.next, kv_len, w.q_len, 0, w.q_len, &seen_lo, &seen_hi);
       for (int it = 0; it < n_kv; ++it) {
         const int pb = it & 1, st = it % kStages;
         const int j0 = (kv_t0 + it) * kPagedTileStep;
-        if (j0 < lo || j0 + kPagedTileStep - 1 > hi) {
-          // rows of V that no row of the tile sees
+        if (j0 < seen_lo || j0 + kPagedTileStep - 1 > seen_hi) {
+          // rows of V that no query of the chunk sees
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s.v_full[st], (it / kStages) & 1, a.err, kErrFwdMma))) break;
-          const int head_rows = max(lo - j0, 0), tail_at = min(hi - j0 + 1, kPagedTileStep);
+          const int head_rows = max(seen_lo - j0, 0), tail_at = min(seen_hi - j0 + 1, kPagedTileStep);
           const int dead = head_rows + kPagedTileStep - tail_at;
           for (int x = lane; x < dead * (D / 8); x += 32) {
             const int d = x / (D / 8), c = x % (D / 8);
@@ -251,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------ softmax + epilogue (rows) --
     const int r = threadIdx.x;  // 0..127 == TMEM lane
-    const int i = r / a.gs;     // token of the tile
+    const int i = row_token(r, a.gs_magic);  // token of the tile
     const bool row_valid = r < n_rows;
     const int p_row = kv_len - w.q_len + tok0 + i;
     int wlo = 0, whi = kv_len - 1;
@@ -270,24 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_lo = max(0, p0 + n_tok - 1 - a.pre);
       all_hi = min(kv_len - 1, p0 + a.next);
     }
-    // Q: the warp's 32 rows, 16 bytes a lane, 128 / D rows... per step
-    {
-      constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;  // 16 chunks: 2 rows; 8: 4 rows
-      const int ch = lane % kChunks;
-#pragma unroll 8
-      for (int x = 0; x < 32 / kRowsPer; ++x) {
-        const int rr = warp * 32 + x * kRowsPer + lane / kChunks;
-        const int ii = rr / a.gs;
-        const int64_t e = static_cast<int64_t>(w.q_start + tok0 + ii) * a.q_row +
-                          static_cast<int64_t>(w.vh * a.gs + rr - ii * a.gs) * a.q_head + ch * 8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < n_rows && ch * 8 < g.D && in_bounds(e, 8, a.n_q, a.err))
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
-        st_chunk_sw128(s.q, rr, ch, v);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&s.q_full);
-    }
+    mbar_arrive(&s.q_full);  // (Q was gathered before the CTA-wide barrier)
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const float c = a.scale_log2;
     float m_use = -INFINITY, m_true = -INFINITY, l = 0.f;
