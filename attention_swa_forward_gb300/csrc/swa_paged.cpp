@@ -14,6 +14,10 @@ namespace {
 constexpr int64_t kSms = 152;  // SMs of the part this library is built for; sizes grids only
 constexpr int64_t kMaxKv = int64_t(1) << 28;
 constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is below 2^40 bytes
+// Keys one CTA of the few-row kernel takes at most, so that one long sequence
+// does not hold a batch up.  201 sequences of up to 2000 keys and one of 131072:
+// 358 us, 354 with 8192 (twice the CTAs, most with nothing to do), 408 with 4096.
+constexpr int64_t kRowsMostKeys = 16384;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kTwoPi = 6.283185307179586;
 
@@ -132,16 +136,24 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
   return SWA_OK;
 }
 
-// Thread split of the heads named in a.heads: units of 2 * VEC elements.
-void rope_split(RopeArgs& a, int dtype, int64_t rows) {
-  const int vec = rope_vec(dtype, a.R);
+// Split of the tokens over CTAs, and of a CTA over its threads: units of
+// 2 * VEC elements, row_lanes rows at a time.
+void set_split(RopeArgs& a, int dtype, int64_t rows) {
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
   a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.H - 1) / a.H);
-  a.units = static_cast<int32_t>(ceil_div(a.D, 2 * vec));
+  a.units = static_cast<int32_t>(ceil_div(a.D, 2 * rope_vec(dtype, a.R)));
   a.row_lanes = kRopeThreads / a.units;
-  // few tokens: one per CTA, so that every SM has some; many: 16, whose
-  // angles one pass of the CTA's threads computes
-  a.tok = static_cast<int32_t>(std::min<int64_t>(kRopeMaxTok, std::max<int64_t>(1, rows / (4 * kSms))));
+  const int x = a.heads[0] ? 0 : 1;
+  a.tok_inner = a.src_r[x] < a.src_h[x] ? 1 : 0;
+  // few tokens: one per CTA, so that every SM has its four; many: up to 8,
+  // while they stay within 80 KB (fp32, 12345 tokens of 12 KB: 49 us with 4,
+  // 52 with 8)
+  const int64_t bytes = int64_t(a.H) * a.D * (dtype == SWA_DTYPE_FP32 ? 4 : 2);
+  a.tok = 1;
+  while (a.tok < kRopeMaxTok && rows >= 2 * a.tok * 4 * kSms && 2 * a.tok * bytes <= 80 * 1024) {
+    a.tok *= 2;
+    ++a.tok_shift;
+  }
 }
 
 swa_status_t rope_call(const swa_rope_params_t* p, const void* q, const swa_strides_t* q_s, const void* k,
@@ -189,7 +201,7 @@ swa_status_t rope_call(const swa_rope_params_t* p, const void* q, const swa_stri
   a.n_pos = a.rows;
   a.S = static_cast<int32_t>(bnsd ? p->S : a.rows);
   a.positions = positions;
-  rope_split(a, p->dtype, a.rows);
+  set_split(a, p->dtype, a.rows);
   const cudaError_t e = launch_rope(a, p->dtype, p->interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SWA_OK : cuda_fail(e, "rotary launch");
 }
@@ -360,9 +372,9 @@ swa_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
   return SWA_OK;
 }
 
-// Launch on the sequences that `take` fills an entry for, at most CAP of them per table.
+// Launch on the sequences (in `order`, or as they come) that `take` fills an entry for, at most CAP of them per table.
 template <int CAP, typename Take, typename Launch>
-cudaError_t each_table(const PagedPlan& plan, Take&& take, Launch&& launch) {
+cudaError_t each_table(const PagedPlan& plan, const std::vector<int32_t>& order, Take&& take, Launch&& launch) {
   static thread_local std::unique_ptr<PagedTable<CAP>> storage;
   if (!storage) storage.reset(new PagedTable<CAP>());
   PagedTable<CAP>& tab = *storage;
@@ -373,9 +385,10 @@ cudaError_t each_table(const PagedPlan& plan, Take&& take, Launch&& launch) {
     std::memset(&tab, 0, sizeof tab);
     return e;
   };
-  for (size_t b = 0; b < plan.len.size(); ++b) {
+  for (size_t x = 0; x < plan.len.size(); ++x) {
+    const int32_t b = order.empty() ? static_cast<int32_t>(x) : order[x];
     PagedDesc d{};
-    if (plan.len[b] == 0 || !take(static_cast<int>(b), d, tab)) continue;
+    if (plan.len[b] == 0 || !take(b, d, tab)) continue;
     tab.d[tab.count++] = d;
     if (tab.count == CAP) {
       const cudaError_t e = flush();
@@ -391,31 +404,14 @@ int64_t live_sequences(const PagedPlan& plan) {
   return n;
 }
 
-// ----------------------------------------------------------------- append --
-int64_t append_tok(const swa_paged_params_t* p) {
-  return std::min<int64_t>(kRopeMaxTok, std::max<int64_t>(1, p->T_q / (4 * kSms)));
-}
-// CTAs of an append call: each launch covers the tokens of its table's sequences.
-int64_t append_ctas(const swa_paged_params_t* p, const PagedPlan& plan) {
-  const int64_t tok = append_tok(p);
-  if (plan.uniform > 0) return ceil_div(p->T_q, tok);
-  int64_t ctas = 0, count = 0, rows = 0;
-  for (int64_t n : plan.len) {
-    if (n == 0) continue;
-    rows += n;
-    if (++count == kPagedLargeTable) {
-      ctas += ceil_div(rows, tok);
-      count = rows = 0;
-    }
-  }
-  return ctas + ceil_div(rows, tok);
-}
+// Workspace of an append call: the header and one page status per token.
+size_t append_bytes(const swa_paged_params_t* p) { return kHeaderBytes + round256(static_cast<size_t>(p->T_q) * 4); }
 
 // -------------------------------------------------------------- attention --
 // The row tiles and splits of one kernel over the sequences it takes.
 struct Part {
   int64_t gs = 1, tok = 1, rows = 0;  // heads and tokens of a tile, rows of a partial
-  int64_t items = 0, splits = 1, min_steps = 1, step = 1;
+  int64_t items = 0, splits = 1, par = 1, cap = 1, least = 1, step = 1;
   size_t status_at = 0, ml_at = 0, o_at = 0;  // workspace offsets
 };
 struct ForwardPlan {
@@ -432,12 +428,11 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   if (st != SWA_OK) return st;
   const int64_t G = p->N / f.seq.N_kv, DP = p->D <= 64 ? 64 : 128;
   f.total = kHeaderBytes;
-  auto lay_out = [&](Part& part, bool few, int64_t most_rows, int64_t step, int64_t resident, int64_t min_steps) {
+  auto lay_out = [&](Part& part, bool few, int64_t most_rows, int64_t step) {
     part.gs = divisor_up_to(G, most_rows);
     part.tok = most_rows / part.gs;
     part.rows = most_rows;
     part.step = step;
-    part.min_steps = min_steps;
     part.items = 0;
     for (int64_t n : f.seq.len)
       if (few_rows(n, G) == few) part.items += ceil_div(n, part.tok) * (p->N / part.gs);
@@ -448,8 +443,24 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       if (w < (long double)keys) keys = std::max<int64_t>(1, static_cast<int64_t>(w));
     }
     const int64_t steps = ceil_div(keys, step) + 1;
-    part.splits = part.items == 0 ? 1 : std::max<int64_t>(1, std::min(ceil_div(steps, min_steps), ceil_div(resident, part.items)));
-    part.splits = std::min<int64_t>(part.splits, 65535);
+    const int64_t items = std::max<int64_t>(part.items, 1);
+    if (few) {
+      // One CTA draws up to ~46 GB/s, so one per SM nearly saturates HBM and
+      // two per SM are resident: just over one per SM, or one per item where
+      // the items are as many.  Measured (64 items of 8192 keys): 49 us in 128
+      // CTAs, 48 in 256, 60 in 320, which start a second wave; 8 items of
+      // 131072 keys: 83 us in 152, 92 in 304.
+      part.par = std::min(ceil_div(kSms, items), steps);
+      part.cap = kRowsMostKeys / step + 2;
+      part.least = 1;
+    } else {
+      // A CTA costs ~7 us beside its steps of 0.78 us, and a split writes and
+      // reads 64 KB more: only where SMs would stay empty
+      part.least = 4;
+      part.par = items > kSms / 2 ? 1 : std::min(kSms / items, ceil_div(steps, part.least));
+      part.cap = steps;
+    }
+    part.splits = std::max(part.par, ceil_div(steps, part.cap));
     part.status_at = f.total;
     f.total += round256(part.items * part.splits * 4);
     if (part.splits > 1) {
@@ -459,30 +470,34 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       f.total = part.o_at + round256(rows * DP * 4);
     }
   };
-  lay_out(f.rows, true, kRowsTile, kRowsStep, 4 * 2 * kSms, 2);
-  lay_out(f.tile, false, kPagedTileRows, kPagedTileStep, kSms, 4);
+  lay_out(f.rows, true, kRowsTile, kRowsStep);
+  lay_out(f.tile, false, kPagedTileRows, kPagedTileStep);
   if (f.rows.items > 2147483647 || f.tile.items > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many query rows for one call");
   return SWA_OK;
 }
 
 template <int CAP>
 cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
-                     const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+                     const CUtensorMap& mk, const CUtensorMap& mv, bool joins, cudaStream_t s) {
   const bool few = &part == &f.rows;
   a.gs = static_cast<int32_t>(part.gs);
   a.gs_magic = static_cast<uint32_t>(ceil_div(65536, part.gs));
   a.tok = static_cast<int32_t>(part.tok);
   a.groups = static_cast<int32_t>(p->N / part.gs);
   a.splits = static_cast<int32_t>(part.splits);
-  a.min_steps = static_cast<int32_t>(part.min_steps);
+  a.par = static_cast<int32_t>(part.par);
+  a.cap = static_cast<int32_t>(part.cap);
+  a.least = static_cast<int32_t>(part.least);
   a.rows_pad = static_cast<int32_t>(part.rows);
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
   a.page_err = reinterpret_cast<int32_t*>(ws + part.status_at);
   a.part_ml = reinterpret_cast<float2*>(ws + part.ml_at);
   a.part_o = reinterpret_cast<float*>(ws + part.o_at);
   auto go = [&](PagedTable<CAP>& tab) {
-    cudaError_t e = few ? launch_paged_rows(a, tab, s) : launch_paged_tile(a, tab, mk, mv, s);
-    if (e == cudaSuccess && a.splits > 1) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
+    cudaError_t e = cudaSuccess;
+    if (joins) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
+    else if (few) e = launch_paged_rows(a, tab, s);
+    else e = launch_paged_tile(a, tab, mk, mv, s);
     a.item_base += tab.n_items;
     a.clear_err = 0;
     return e;
@@ -506,7 +521,14 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     tab.n_items += d.tiles * a.groups;
     return true;
   };
-  return each_table<CAP>(f.seq, take, go);
+  // long chunks first: they tend to hold the heaviest tiles
+  std::vector<int32_t> order;
+  if (!few) {
+    order.resize(f.seq.len.size());
+    for (size_t b = 0; b < order.size(); ++b) order[b] = static_cast<int32_t>(b);
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return f.seq.len[x] > f.seq.len[y]; });
+  }
+  return each_table<CAP>(f.seq, order, take, go);
 }
 
 // The first page status of n words at `at` that is not 0.
@@ -563,7 +585,7 @@ swa_status_t swa_paged_append_workspace_size(const swa_paged_params_t* p, size_t
   PagedPlan plan;
   const swa_status_t st = paged_plan(p, plan);
   if (st != SWA_OK) return st;
-  *bytes = kHeaderBytes + round256(append_ctas(p, plan) * 4);
+  *bytes = append_bytes(p);
   return SWA_OK;
 }
 
@@ -595,7 +617,7 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
   if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
   st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.pg);
   if (st != SWA_OK) return st;
-  const size_t need = kHeaderBytes + round256(append_ctas(p, plan) * 4);
+  const size_t need = append_bytes(p);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
 
   a.D = static_cast<int32_t>(p->D);
@@ -634,7 +656,7 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
   a.S = static_cast<int32_t>(p->T_q);
   a.n_pos = p->T_q;
   a.positions = positions;
-  rope_split(a, p->dtype, p->T_q);
+  set_split(a, p->dtype, p->T_q);
   a.err = static_cast<int32_t*>(workspace);
   a.page_err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -663,12 +685,11 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
       a.rows = last.q_start + last.q_len;
       const int n = static_cast<int>(ceil_div(a.rows - a.tok_begin, a.tok));
       const cudaError_t le = launch_append(a, tab, p->dtype, il, n, s);
-      a.page_err += n;
       a.clear_err = 0;
       return le;
     };
-    e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, take, go)
-                                                 : each_table<kPagedLargeTable>(plan, take, go);
+    e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, go)
+                                                 : each_table<kPagedLargeTable>(plan, {}, take, go);
   }
   return e == cudaSuccess ? SWA_OK : cuda_fail(e, "append launch");
 }
@@ -738,12 +759,22 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     if (st != SWA_OK) return st;
   }
   const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
-  for (const Part* part : {&f.tile, &f.rows}) {
-    if (part->items == 0 || e != cudaSuccess) continue;
-    e = small ? run_part<kPagedSmallTable>(p, f, *part, a, mk, mv, s)
-              : run_part<kPagedLargeTable>(p, f, *part, a, mk, mv, s);
+  auto run = [&](const Part& part, bool joins) {
+    if (part.items == 0 || e != cudaSuccess || (joins && part.splits <= 1)) return;
+    e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, joins, s)
+              : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, joins, s);
     a.clear_err = 0;
-  }
+  };
+  // A batch of both kinds whose tables fit one launch each: the few-row kernel
+  // runs beside the other's last wave.  The joins come last: each waits for
+  // the grid before it, and that one for the tiles.
+  const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable;
+  a.signal = both ? 1 : 0;
+  run(f.tile, false);
+  a.overlap = both ? 1 : 0;
+  run(f.rows, false);
+  run(f.tile, true);
+  run(f.rows, true);
   return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
 }
 
@@ -751,7 +782,7 @@ swa_status_t swa_paged_append_status(const swa_paged_params_t* p, const void* wo
   PagedPlan plan;
   swa_status_t st = paged_plan(p, plan);
   if (st == SWA_OK) st = swa_workspace_status(workspace, stream);
-  return st == SWA_OK ? read_pages(append_ctas(p, plan), workspace, kHeaderBytes) : st;
+  return st == SWA_OK ? read_pages(p->T_q, workspace, kHeaderBytes) : st;
 }
 
 swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {

@@ -42,7 +42,7 @@ struct PagedGeom {
 };
 
 // ------------------------------------------------------- rotary / append --
-constexpr int kRopeMaxTok = 16;  // rows (tokens) per CTA at most
+constexpr int kRopeMaxTok = 8;  // rows (tokens) per CTA at most
 constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
@@ -58,7 +58,8 @@ struct RopeArgs {
   int32_t D, R;
   int32_t units;      // 2 * VEC-element units of a head row
   int32_t row_lanes;  // rows a CTA takes at a time: threads / units
-  int32_t tok;        // tokens per CTA
+  int32_t tok, tok_shift;  // tokens per CTA, a power of two
+  int32_t tok_inner;  // 1: walk the tokens of a head first
   int32_t n_axes, inverse;
   int32_t S;          // rows per batch
   int64_t rows;       // tokens in all
@@ -67,7 +68,7 @@ struct RopeArgs {
   PagedGeom pg;       // append only
   int32_t* err;       // append: status word; else NULL
   int32_t clear_err;  // append: 1 in the first launch of a call
-  int32_t* page_err;  // append: this launch's per-CTA page status
+  int32_t* page_err;  // append: page status per token
   int32_t tok_begin;  // append: first token of this launch
   uint64_t freq[64];  // angle per position as a fraction of a turn, 2^64 = one turn
   uint8_t axis[64];
@@ -100,7 +101,7 @@ struct PagedArgs {
   int32_t pre, next;  // clamped so that position sums stay inside int32
   float scale_log2;
   int32_t splits;     // CTAs per item along the keys, at most
-  int32_t min_steps;  // key steps a split takes at least
+  int32_t par, cap, least;  // paged_split
   int32_t rows_pad;   // rows of a partial tile
   int32_t stall;      // test hook (kStallPaged)
   int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128
@@ -117,9 +118,14 @@ struct PagedArgs {
   int32_t item_base;  // items of earlier launches of the call
   int32_t* err;
   int32_t clear_err;
+  int32_t signal;     // tile kernel: let the next grid start with the last wave
+  int32_t overlap;    // few-row kernel: that next grid
   int32_t* page_err;  // per CTA of the call, [items][splits]
   int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build
 };
+
+// Row r of a tile belongs to its token r / gs (r < 128; gs_magic = ceil(2^16 / gs), exact there).
+SWA_PAGED_HD int row_token(int r, uint32_t gs_magic) { return static_cast<int>((r * gs_magic) >> 16); }
 
 // A resolved work item.
 struct PagedItem {
@@ -165,12 +171,16 @@ SWA_PAGED_HD void paged_key_range(int sparse_mode, int pre, int next, int kv_len
   }
 }
 
-// Key steps of split s: [begin, end) of the item's `steps`; `*active` = splits
-// that have any.
-SWA_PAGED_HD void paged_split(int steps, int splits, int min_steps, int s, int* begin, int* end, int* active) {
-  int per = (steps + splits - 1) / splits;
-  if (per < min_steps) per = min_steps;
-  *active = per > 0 ? (steps + per - 1) / per : 0;
+// Key steps of split s: [begin, end) of the item's `steps`, in `*active` equal
+// runs.  A run takes a `par`-th of them (as many CTAs as fill the GPU), at
+// most `cap` (a sequence far longer than the others must not hold one CTA up)
+// and at least `least`.
+SWA_PAGED_HD void paged_split(int steps, int par, int cap, int least, int s, int* begin, int* end, int* active) {
+  int per = (steps + par - 1) / par;
+  if (per > cap) per = cap;
+  if (per < least) per = least;
+  *active = steps > 0 ? (steps + per - 1) / per : 0;
+  if (*active > 1) per = (steps + *active - 1) / *active;
   *begin = s * per < steps ? s * per : steps;
   *end = *begin + per < steps ? *begin + per : steps;
 }

@@ -8,12 +8,19 @@
 // Bound by HBM: each key and value is read once for the 16 rows of a tile (the
 // tokens x query heads that share the key/value head).  A CTA of 4 warps takes
 // a run of 64-key steps; each warp owns 16 keys of every step and runs by
-// itself: its own 3-stage ring of cp.async copies (16-byte chunks XOR-swizzled
-// against bank conflicts), its own maximum and sum, S = Q K^T and O += P V by
-// mma.sync m16n8k16.  With at most 16 rows a 128-row tcgen05 tile would be
-// seven eighths padding and its barrier hand-offs would set the latency, while
-// the legacy tensor path has several times the rate that HBM can feed here.
-// The warps' results are joined in shared memory at the end.
+// itself: its own 3-stage rings of cp.async copies of K and V (16-byte chunks
+// XOR-swizzled against bank conflicts), its own maximum and sum, S = Q K^T and
+// O += P V by mma.sync m16n8k16.  With at most 16 rows a 128-row tcgen05 tile
+// would be seven eighths padding and its barrier hand-offs would set the
+// latency, while the legacy tensor path has several times the rate that HBM
+// can feed here.  What a warp does per 16 keys bounds a CTA's rate: with all
+// fragments of a group loaded before the first product, a stage refilled as
+// soon as they are in registers, and no per-row tests inside the visible run,
+// a CTA draws 46 GB/s (32 before).  Measured: 256 sequences x 1024-key windows
+// 137 us (the copy rate's own time), 64 x 4096 145 us (0.96 of it), 24
+// sequences of up to 8192 keys, 16 heads of 64, 81 us (0.88), one sequence of
+// 131072 keys 84 us (0.94).  The warps' results are joined in shared memory at
+// the end.
 //
 // A 16-key group lies in one page (page sizes are multiples of 16).  Keys no
 // row of the tile sees are never read: their chunks are zero-filled, so a NaN
@@ -24,7 +31,7 @@
 namespace swa {
 namespace {
 
-constexpr int kRowsWarps = 4;
+constexpr int kRowsWarps = kRowsStep / 16;
 constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr int kRowsStages = 3;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -52,11 +59,11 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -82,48 +89,29 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   constexpr int kChunks = DP / 8;  // 16-byte chunks of a key row
   const PagedGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
+  // Behind the tile kernel of the same call (overlap), whose CTAs signalled
+  // after their own wait, every earlier grid has completed: this one may run
+  // beside that kernel's last wave, and its first CTA waits for it at the end.
+  if (!a.overlap) griddep_wait();
   griddep_launch_dependents();
   const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
   const int split = blockIdx.y;
   if (a.clear_err && blockIdx.x == 0 && split == 0 && threadIdx.x == 0) *a.err = 0;
   const int64_t item = a.item_base + static_cast<int64_t>(blockIdx.x);
-  int bad = 0;
-  int kv_len = in_bounds(w.b, 1, g.n_lens, a.err) ? g.kv_lens[w.b] : 0;
-  if (kv_len < 0 || kv_len > g.kv_limit) {
-    bad = kPageErrLength;
-    kv_len = 0;
-  }
   const int tok0 = w.tile * a.tok;
   const int n_tok = min(a.tok, w.q_len - tok0), n_rows = n_tok * a.gs;
-  int lo, hi;
-  paged_key_range(a.sparse_mode, a.pre, a.next, kv_len, w.q_len, tok0, n_tok, &lo, &hi);
-  // steps of 64 keys = 4 groups of 16, from the group that holds lo
-  const int g0 = lo >> 4;
-  const int steps = lo <= hi ? ((hi >> 4) - g0) / kRowsWarps + 1 : 0;
-  int st0, st1, active;
-  paged_split(steps, a.splits, a.min_steps, split, &st0, &st1, &active);
-  if (split > 0 && split >= active) {  // nothing to do (split 0 writes the result of an empty item)
-    if (threadIdx.x == 0) a.page_err[item * a.splits + split] = 0;
-    return;
-  }
+  const int kv_raw = in_bounds(w.b, 1, g.n_lens, a.err) ? g.kv_lens[w.b] : 0;  // in flight behind the loads of Q
 
   // Q as A fragments: rows lane / 4 and lane / 4 + 8
   const int nk = (g.D + 15) >> 4;
   uint32_t qf[DP / 16][4];
-  int row_lo[2], row_hi[2];  // visible keys of the thread's two rows
+  int row_tok[2];  // tokens of the thread's two rows
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = (lane >> 2) + 8 * x;
     const bool valid = r < n_rows;
-    const int i = valid ? r / a.gs : 0;
-    row_lo[x] = 0;
-    row_hi[x] = kv_len - 1;
-    if (a.sparse_mode == 4) {
-      const int p = kv_len - w.q_len + tok0 + i;
-      row_lo[x] = max(0, p - a.pre);
-      row_hi[x] = min(kv_len - 1, p + a.next);
-    }
+    const int i = valid ? row_token(r, a.gs_magic) : 0;
+    row_tok[x] = i;
     const int h = w.vh * a.gs + (r - i * a.gs);
     const int64_t e = static_cast<int64_t>(w.q_start + tok0 + i) * a.q_row + h * a.q_head;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + e;
@@ -136,6 +124,45 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
                                 ? *reinterpret_cast<const uint32_t*>(q + c)
                                 : 0u;
       }
+  }
+
+  int bad = 0;
+  int kv_len = kv_raw;
+  if (kv_len < 0 || kv_len > g.kv_limit) {
+    bad = kPageErrLength;
+    kv_len = 0;
+  }
+  int lo, hi;
+  paged_key_range(a.sparse_mode, a.pre, a.next, kv_len, w.q_len, tok0, n_tok, &lo, &hi);
+  // steps of 64 keys = 4 groups of 16, from the group that holds lo
+  const int g0 = lo >> 4;
+  const int steps = lo <= hi ? ((hi >> 4) - g0) / kRowsWarps + 1 : 0;
+  int st0, st1, active;
+  paged_split(steps, a.par, a.cap, a.least, split, &st0, &st1, &active);
+  const bool direct = active <= 1;  // no other CTA has keys of this item: write the result itself
+  if (split > 0 && split >= active) {  // nothing to do (split 0 writes the result of an empty item)
+    if (threadIdx.x == 0) a.page_err[item * a.splits + split] = 0;
+    return;
+  }
+
+  int row_lo[2], row_hi[2];  // visible keys of the thread's two rows
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    row_lo[x] = 0;
+    row_hi[x] = kv_len - 1;
+    if (a.sparse_mode == 4) {
+      const int p = kv_len - w.q_len + tok0 + row_tok[x];
+      row_lo[x] = max(0, p - a.pre);
+      row_hi[x] = min(kv_len - 1, p + a.next);
+    }
+  }
+
+  // keys every row of the tile sees: from the last token's first to the first token's last
+  int all_lo = 0, all_hi = kv_len - 1;
+  if (a.sparse_mode == 4) {
+    const int p0 = kv_len - w.q_len + tok0;
+    all_lo = max(0, p0 + n_tok - 1 - a.pre);
+    all_hi = min(kv_len - 1, p0 + a.next);
   }
 
   const int hk = w.vh * a.gs / a.group;
@@ -162,23 +189,39 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   };
   const int row_in = lane / kChunks, chunk = lane % kChunks;  // the lane's part of 32 / kChunks rows
   const int live_chunks = 2 * nk;                             // chunks the products read
-  auto issue = [&](int it) {
-    if ((it & 31) == 0) fetch_pages(it);
+  // The copies of K (V) of the warp's group `it`.  A stage is free once its
+  // fragments are in registers, so close to a ring of each is in flight; every call commits one group, empty past the end.  A group
+  // whose 16 keys are all seen needs no per-row test.
+  const int in_d = chunk * 8 < g.D;
+  const uint32_t lane_dst = ring + row_in * Smem::kRowBytes;
+  auto issue = [&](int it, bool is_v) {
+    if ((it & 31) == 0 && !is_v) fetch_pages(it);
     const int page = __shfl_sync(0xFFFFFFFFu, my_page, it & 31), slot = __shfl_sync(0xFFFFFFFFu, my_slot, it & 31);
     if (it < n_it && chunk < live_chunks) {
       const int j0 = (gw + it * kRowsWarps) * 16;
-      const uint32_t kd = ring + (it % kRowsStages) * 2 * Smem::kGroupBytes, vd = kd + Smem::kGroupBytes;
-      const bool in_d = chunk * 8 < g.D;
+      const uint32_t dst = lane_dst + ((it % kRowsStages) * 2 + (is_v ? 1 : 0)) * Smem::kGroupBytes;
+      const uint16_t* base = is_v ? vb : kb;
+      const int64_t step = is_v ? g.v_slot : g.k_slot;
+      const int64_t e0 = page * (is_v ? g.v_page : g.k_page) + (slot + row_in) * step + chunk * 8;
+      const bool whole = page >= 0 && j0 >= lo && j0 + 15 <= hi;
+      const int64_t head = hk * (is_v ? g.v_head : g.k_head), extent = is_v ? g.n_v : g.n_k;
+      if (SWA_CHECKS == 0 && whole) {
+        const uint16_t* src = in_d ? base + e0 : base;
+        const int64_t hop = in_d ? step * (32 / kChunks) : 0;
 #pragma unroll
-      for (int x = 0; x < 16 * kChunks / 32; ++x) {
-        const int r = x * (32 / kChunks) + row_in;
-        bool ok = page >= 0 && in_d && j0 + r >= lo && j0 + r <= hi;
-        const int64_t ke = page * g.k_page + (slot + r) * g.k_slot + chunk * 8;
-        const int64_t ve = page * g.v_page + (slot + r) * g.v_slot + chunk * 8;
-        if (ok) ok = in_bounds(hk * g.k_head + ke, 8, g.n_k, a.err) && in_bounds(hk * g.v_head + ve, 8, g.n_v, a.err);
-        const uint32_t o = r * Smem::kRowBytes + ((chunk ^ (r & 7)) << 4);
-        cp_async16(kd + o, ok ? kb + ke : kb, ok);
-        cp_async16(vd + o, ok ? vb + ve : vb, ok);
+        for (int x = 0; x < 16 * kChunks / 32; ++x) {
+          const int r = x * (32 / kChunks) + row_in;
+          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + ((chunk ^ (r & 7)) << 4), src, in_d);
+          src += hop;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16 * kChunks / 32; ++x) {
+          const int r = x * (32 / kChunks) + row_in;
+          const int64_t e = e0 + x * (32 / kChunks) * step;
+          const bool ok = in_d && page >= 0 && j0 + r >= lo && j0 + r <= hi && in_bounds(head + e, 8, extent, a.err);
+          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + ((chunk ^ (r & 7)) << 4), ok ? base + e : base, ok);
+        }
       }
     }
     cp_async_commit();
@@ -193,31 +236,56 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   const float c = a.scale_log2;
 
 #pragma unroll
-  for (int it = 0; it < kRowsStages - 1; ++it) issue(it);
+  for (int it = 0; it < kRowsStages; ++it) {
+    issue(it, false);
+    issue(it, true);
+  }
+  const bool fold = c > 0.f;  // the scale folds into the exponent's multiply-add
+  const int mat = lane >> 3, lr = lane & 7;
+  const uint32_t k_row = ((mat >> 1) * 8 + lr) * Smem::kRowBytes, v_row = ((mat & 1) * 8 + lr) * Smem::kRowBytes;
   for (int it = 0; it < n_it; ++it) {
-    issue(it + kRowsStages - 1);
-    cp_async_wait<kRowsStages - 1>();
+    cp_async_wait<2 * kRowsStages - 1>();  // K(it) is the oldest group in flight
     __syncwarp();
     const int j0 = (gw + it * kRowsWarps) * 16;
-    if (j0 <= hi) {  // (the last step may be short of groups)
-      const uint32_t kd = ring + (it % kRowsStages) * 2 * Smem::kGroupBytes, vd = kd + Smem::kGroupBytes;
-      const int mat = lane >> 3, lr = lane & 7;
-      float sc[2][4];  // scores of keys 0-7 and 8-15
+    const uint32_t kd = ring + (it % kRowsStages) * 2 * Smem::kGroupBytes, vd = kd + Smem::kGroupBytes;
+    float sc[2][4];  // scores of keys 0-7 and 8-15
+    {
+      uint32_t b[DP / 16][4];
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+        if (kk < nk) ldsm_x4(b[kk], kd + k_row + (((kk * 2 + (mat & 1)) ^ lr) << 4));
+      __syncwarp();
+      issue(it + kRowsStages, false);  // K's stage is free
+      // even and odd steps apart: two chains per accumulator instead of one of twice the length
+      float s2[2][2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) sc[x][y] = 0.f;
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        if (kk >= nk) break;
-        uint32_t b[4];
-        const int r = (mat >> 1) * 8 + lr, ch = kk * 2 + (mat & 1);
-        ldsm_x4(b, kd + r * Smem::kRowBytes + ((ch ^ (r & 7)) << 4));
-        mma16816<F16>(sc[0], qf[kk], b[0], b[1]);
-        mma16816<F16>(sc[1], qf[kk], b[2], b[3]);
-      }
-      // scale, mask, running maximum
-      float mx[2] = {-INFINITY, -INFINITY};
+          for (int z = 0; z < 4; ++z) s2[x][y][z] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+        if (kk < nk) {
+          mma16816<F16>(s2[kk & 1][0], qf[kk], b[kk][0], b[kk][1]);
+          mma16816<F16>(s2[kk & 1][1], qf[kk], b[kk][2], b[kk][3]);
+        }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) sc[y][z] = s2[0][y][z] + s2[1][y][z];
+    }
+    cp_async_wait<2 * kRowsStages - 1>();  // V(it): its fragments load behind the softmax
+    __syncwarp();
+    uint32_t vf[DP / 16][4];
+#pragma unroll
+    for (int nb = 0; nb < DP / 16; ++nb)
+      if (nb < nk) ldsm_x4_trans(vf[nb], vd + v_row + (((nb * 2 + (mat >> 1)) ^ lr) << 4));
+    __syncwarp();
+    issue(it + kRowsStages, true);  // V's stage is free
+    // mask (groups at the ends of the visible run only), running maximum
+    float mx[2] = {-INFINITY, -INFINITY};
+    if (!fold || j0 < all_lo || j0 + 15 > all_hi) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -225,52 +293,49 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
           const int x = y >> 1;
           const int j = j0 + t * 8 + (lane & 3) * 2 + (y & 1);
           const bool vis = j >= row_lo[x] && j <= row_hi[x];
-          sc[t][y] = vis ? sc[t][y] * c : -INFINITY;
-          mx[x] = fmaxf(mx[x], sc[t][y]);
+          sc[t][y] = vis ? (fold ? sc[t][y] : sc[t][y] * c) : -INFINITY;
         }
-      bool grow = false;
-      float mn[2];
+    }
+    const float cf = fold ? c : 1.f;
+    bool grow = false;
+    float mn[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      mx[x] = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
+      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], 1));
+      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], 2));
+      m_true[x] = mn[x] = fmaxf(m_true[x], mx[x] * cf);
+      grow |= mn[x] > m[x] + kRescale;
+    }
+    if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], 1));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xFFFFFFFFu, mx[x], 2));
-        m_true[x] = mn[x] = fmaxf(m_true[x], mx[x]);
-        grow |= mn[x] > m[x] + kRescale;
-      }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float alpha = mn[x] > m[x] ? ex2_approx(m[x] - mn[x]) : 1.f;  // (also when m is -inf: 0)
+        m[x] = mn[x];
+        l[x] *= alpha;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float alpha = mn[x] > m[x] ? ex2_approx(m[x] - mn[x]) : 1.f;  // (also when m is -inf: 0)
-          m[x] = mn[x];
-          l[x] *= alpha;
-#pragma unroll
-          for (int t = 0; t < DP / 8; ++t) {
-            o[t][2 * x] *= alpha;
-            o[t][2 * x + 1] *= alpha;
-          }
+        for (int t = 0; t < DP / 8; ++t) {
+          o[t][2 * x] *= alpha;
+          o[t][2 * x + 1] *= alpha;
         }
-      }
-      uint32_t p[4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float ms = m[x] == -INFINITY ? 0.f : m[x];
-        const float p0 = ex2_approx(sc[0][2 * x] - ms), p1 = ex2_approx(sc[0][2 * x + 1] - ms);
-        const float p2 = ex2_approx(sc[1][2 * x] - ms), p3 = ex2_approx(sc[1][2 * x + 1] - ms);
-        l[x] += (p0 + p1) + (p2 + p3);
-        p[x] = pack2<F16>(p0, p1);      // keys 0-7
-        p[2 + x] = pack2<F16>(p2, p3);  // keys 8-15
-      }
-#pragma unroll
-      for (int nb = 0; nb < DP / 16; ++nb) {
-        if (nb >= nk) break;
-        uint32_t b[4];
-        const int r = (mat & 1) * 8 + lr, ch = nb * 2 + (mat >> 1);
-        ldsm_x4_trans(b, vd + r * Smem::kRowBytes + ((ch ^ (r & 7)) << 4));
-        mma16816<F16>(o[2 * nb], p, b[0], b[1]);
-        mma16816<F16>(o[2 * nb + 1], p, b[2], b[3]);
       }
     }
-    __syncwarp();  // the stage may be overwritten
+    uint32_t p[4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float ms = m[x] == -INFINITY ? 0.f : m[x];
+      const float p0 = ex2_approx(fmaf(sc[0][2 * x], cf, -ms)), p1 = ex2_approx(fmaf(sc[0][2 * x + 1], cf, -ms));
+      const float p2 = ex2_approx(fmaf(sc[1][2 * x], cf, -ms)), p3 = ex2_approx(fmaf(sc[1][2 * x + 1], cf, -ms));
+      l[x] += (p0 + p1) + (p2 + p3);
+      p[x] = pack2<F16>(p0, p1);      // keys 0-7
+      p[2 + x] = pack2<F16>(p2, p3);  // keys 8-15
+    }
+#pragma unroll
+    for (int nb = 0; nb < DP / 16; ++nb)
+      if (nb < nk) {
+        mma16816<F16>(o[2 * nb], p, vf[nb][0], vf[nb][1]);
+        mma16816<F16>(o[2 * nb + 1], p, vf[nb][2], vf[nb][3]);
+      }
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -320,13 +385,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       acc[2] += ov.z * f;
       acc[3] += ov.w * f;
     }
-    if (a.splits > 1) {
+    if (!direct) {
       const int64_t pr = (item * a.splits + split) * a.rows_pad + r;
       *reinterpret_cast<float4*>(a.part_o + pr * DP + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (col == 0) a.part_ml[pr] = make_float2(M, L);
     } else {
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      const int i = r / a.gs, h = w.vh * a.gs + (r - i * a.gs);
+      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+      const int i = row_token(r, a.gs_magic), h = w.vh * a.gs + (r - i * a.gs);
       const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
       if (col < g.D && in_bounds(row * g.D + col, 4, a.n_out, a.err))
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D + col) =
@@ -337,37 +402,48 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       }
     }
   }
+  if (a.overlap && blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();  // (no early return: split 0 always runs)
 }
 
-// Join the splits of a row tile: one warp per row, its lanes over the columns.
-// Reads items x active splits partial rows once; a few microseconds behind the
-// kernel that wrote them, launched so that its prologue overlaps that tail.
+// Join the splits of a row tile: WPR warps per row over its splits (each reads
+// a partial row with one load per lane), then over their sums in shared
+// memory; one warp up to 8 splits, eight past that.  Reads the active partial
+// rows once; a few microseconds
+// behind the kernel that wrote them, launched so that its prologue overlaps
+// that tail.  (One warp per row took 30 us for the 152 splits of one
+// 131072-token sequence.)
 constexpr int kJoinWarps = 8;
-template <int DP, bool F16, int CAP>
+template <int DP, bool F16, int WPR, int CAP>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     swa_paged_join_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab,
                           const int step_keys) {
   constexpr int kPer = DP / 32;  // columns of a lane: 4 or 2
+  __shared__ float s_acc[WPR][DP], s_l[WPR], s_m[WPR];
   const PagedGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
-  griddep_launch_dependents();
   const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
-  const int r = blockIdx.y * kJoinWarps + warp;
+  const int r = blockIdx.y * (kJoinWarps / WPR) + warp / WPR, part = warp % WPR;
   const int tok0 = w.tile * a.tok;
   const int n_tok = min(a.tok, w.q_len - tok0);
-  if (r >= n_tok * a.gs) return;
+  // (the lengths come from grids before the one that wrote the partial rows)
   int kv_len = in_bounds(w.b, 1, g.n_lens, a.err) ? g.kv_lens[w.b] : 0;
   if (kv_len < 0 || kv_len > g.kv_limit) kv_len = 0;
   int lo, hi, st0, st1, active;
   paged_key_range(a.sparse_mode, a.pre, a.next, kv_len, w.q_len, tok0, n_tok, &lo, &hi);
   const int first = step_keys == kRowsStep ? lo >> 4 << 4 : lo / step_keys * step_keys;
   const int steps = lo <= hi ? (hi - first) / step_keys + 1 : 0;
-  paged_split(steps, a.splits, a.min_steps, 0, &st0, &st1, &active);
+  paged_split(steps, a.par, a.cap, a.least, 0, &st0, &st1, &active);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (r >= n_tok * a.gs) return;  // (with WPR > 1 a CTA is one row: all of it returns)
+  static_assert(WPR == 1 || WPR == kJoinWarps, "a CTA is one row or one row per warp");
+  if (active <= 1) return;  // written by the CTA that had the keys
   const int64_t item = a.item_base + static_cast<int64_t>(blockIdx.x);
   const int64_t p0 = item * a.splits * a.rows_pad + r;
+  // each warp: its splits' maximum, then their sum relative to it
   float M = -INFINITY;
-  for (int x = lane; x < active; x += 32) M = fmaxf(M, a.part_ml[p0 + static_cast<int64_t>(x) * a.rows_pad].x);
+  for (int x = part + WPR * lane; x < active; x += 32 * WPR)
+    M = fmaxf(M, a.part_ml[p0 + static_cast<int64_t>(x) * a.rows_pad].x);
 #pragma unroll
   for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
   const float ms = M == -INFINITY ? 0.f : M;
@@ -375,7 +451,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
   for (int y = 0; y < kPer; ++y) acc[y] = 0.f;
 #pragma unroll 4
-  for (int x = 0; x < active; ++x) {
+  for (int x = part; x < active; x += WPR) {
     const int64_t p = p0 + static_cast<int64_t>(x) * a.rows_pad;
     const float2 ml = a.part_ml[p];
     const float f = ex2_approx(ml.x - ms);
@@ -392,8 +468,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       acc[1] += v.y * f;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const int i = r / a.gs, h = w.vh * a.gs + (r - i * a.gs);
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) s_acc[warp][lane * kPer + y] = acc[y];
+    if (lane == 0) {
+      s_l[warp] = L;
+      s_m[warp] = M;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    M = s_m[0];
+#pragma unroll
+    for (int x = 1; x < kJoinWarps; ++x) M = fmaxf(M, s_m[x]);
+    const float mt = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[y] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) {
+      const float f = ex2_approx(s_m[x] - mt);
+      L += s_l[x] * f;
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) acc[y] += s_acc[x][lane * kPer + y] * f;
+    }
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  const int i = row_token(r, a.gs_magic), h = w.vh * a.gs + (r - i * a.gs);
   const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
   const int col = lane * kPer;
   if (col < g.D && in_bounds(row * g.D + col, kPer, a.n_out, a.err)) {
@@ -423,8 +523,11 @@ cudaError_t launch_rows_t(const PagedArgs& a, const PagedTable<CAP>& tab, cudaSt
 template <int DP, bool F16, int CAP>
 cudaError_t launch_join_t(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream) {
   const int rows = a.tok * a.gs;
-  return launch_pdl(swa_paged_join_kernel<DP, F16, CAP>, dim3(tab.n_items, (rows + kJoinWarps - 1) / kJoinWarps),
-                    dim3(kJoinWarps * 32), 0, stream, a, tab, step_keys);
+  if (a.splits <= 8)
+    return launch_pdl(swa_paged_join_kernel<DP, F16, 1, CAP>, dim3(tab.n_items, (rows + kJoinWarps - 1) / kJoinWarps),
+                      dim3(kJoinWarps * 32), 0, stream, a, tab, step_keys);
+  return launch_pdl(swa_paged_join_kernel<DP, F16, kJoinWarps, CAP>, dim3(tab.n_items, rows), dim3(kJoinWarps * 32), 0,
+                    stream, a, tab, step_keys);
 }
 
 }  // namespace

@@ -54,9 +54,6 @@ constexpr uint32_t kColO = 256, kColP = 384;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // as in swa_fwd.cu
 
-// Row r of a tile belongs to its token r / gs (r < 128; gs_magic = ceil(2^16 / gs), exact there).
-__device__ __forceinline__ int row_token(int r, uint32_t gs_magic) { return static_cast<int>((r * gs_magic) >> 16); }
-
 // Where one lane of a gathering warp finds its part of successive key tiles:
 // box `box` (box_rows slots) of the tile, in atom column `atom`.
 struct PageWalk {
@@ -112,6 +109,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTileBytes = TileSmem<D>::kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
+  // the few-row kernel of the same call may fill the SMs that the last wave
+  // leaves (it waits for this grid at its end); nothing else starts early
+  if (a.signal) griddep_launch_dependents();
   if (a.clear_err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
   const PagedGeom& g = a.g;
   const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t_first = lo >> 7;
   const int steps = lo <= hi ? (hi >> 7) - t_first + 1 : 0;
   int st0, st1, active;
-  paged_split(steps, a.splits, a.min_steps, split, &st0, &st1, &active);
+  paged_split(steps, a.par, a.cap, a.least, split, &st0, &st1, &active);
+  const bool direct = active <= 1;  // no other CTA has keys of this item: write the result itself
   if (split > 0 && split >= active) {  // nothing to do (split 0 writes the result of an empty item)
     if (threadIdx.x == 0) a.page_err[slot_id] = 0;
     return;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // relative to the true maximum from here on
       const bool empty = m_true == -INFINITY;
       const float f = empty ? 0.f : ex2_approx(m_use - m_true);
-      const float mul = a.splits > 1 ? f : (l > 0.f || l != l ? 1.f / l : 0.f);
+      const float mul = !direct ? f : (l > 0.f || l != l ? 1.f / l : 0.f);
       const int h = w.vh * a.gs + (r - i * a.gs);
       const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
       const int64_t pr = slot_id * a.rows_pad + r;
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q4 = 0; q4 < 4; ++q4) {
             const int col = ch * 32 + q4 * 8;
             if (col >= g.D) continue;
-            if (a.splits > 1) {
+            if (!direct) {
               store8<F16>(a.part_o, pr * D + col, &o[q4 * 8], true);
             } else if (in_bounds(row * g.D + col, 8, a.n_out, a.err)) {
               store8<F16>(a.out, row * g.D + col, &o[q4 * 8], false);
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (row_valid) {
-        if (a.splits > 1) {
+        if (!direct) {
           a.part_ml[pr] = make_float2(m_true, l * f);
         } else if (in_bounds(row, 1, a.n_stats, a.err)) {
           if (a.smax) a.smax[row] = empty ? -INFINITY : m_true * kLn2;

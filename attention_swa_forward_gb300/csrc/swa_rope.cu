@@ -1,7 +1,7 @@
 // swa_rope.cu — rotary positions of q and k, and the append of a chunk's keys
 // and values to the paged cache (include/swa.h).
 //
-// One kernel: a CTA takes up to 16 tokens, all heads of q, k (and v) of each.
+// One kernel: a CTA takes up to 8 tokens, all heads of q, k (and v) of each.
 // Pair i of a row at position p turns by p * inv_freq[i].  The angle is kept as
 // a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1)):
 // p * F_i mod 2^64 is the angle modulo a turn, exact but for the rounding of
@@ -11,7 +11,12 @@
 //
 // Bound by HBM: every element is read and written once.  Each thread keeps one
 // place in the head row (VEC elements and their partners) and walks over
-// (token, head) rows, four in flight.
+// (token, head) rows, four in flight through registers.  671 MB (32768 tokens,
+// 32 + 8 heads of 128) take 108 us, 0.92 of the measured copy rate.  Walking
+// the heads of a token first in BNSD, 256 bytes at a time, took 122 us; 16
+// tokens per CTA 112, 4 tokens 116; all rows staged through shared memory by
+// cp.async, 4 tokens per CTA, 130: what is left are instructions, not bytes in
+// flight.
 #include "swa_paged.h"
 #include "swa_device.cuh"
 
@@ -46,7 +51,7 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 struct RopeSmem {
   int64_t src[kRopeMaxTok][3], dst[kRopeMaxTok][3];  // element offsets of (token, head 0); dst < 0: not stored
   int32_t pos[kRopeMaxTok];                          // position in its sequence (append)
-  float cs[kRopeMaxTok][64], sn[kRopeMaxTok][64];
+  alignas(16) float cs[kRopeMaxTok][64], sn[kRopeMaxTok][64];
 };
 
 // in_bounds without a status word to report to: the access is skipped.
@@ -57,11 +62,17 @@ __device__ __forceinline__ bool rope_in_bounds(int64_t first, int64_t count, int
 }
 
 template <typename T, int VEC, bool IL>
-__device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs, const float* sn, float sign) {
+__device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs_, const float* sn_) {
+  alignas(16) float cs[VEC], sn[VEC];  // (VEC is a multiple of 4 and so is the first pair)
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4) {
+    *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(cs_ + i);
+    *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(sn_ + i);
+  }
   if constexpr (IL) {  // pairs inside a chunk: VEC / 2 of a, then VEC / 2 of b
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
-      const float ca = cs[i], sa = sn[i] * sign, cb = cs[VEC / 2 + i], sb = sn[VEC / 2 + i] * sign;
+      const float ca = cs[i], sa = sn[i], cb = cs[VEC / 2 + i], sb = sn[VEC / 2 + i];
       const float x0 = to_f(a[2 * i]), y0 = to_f(a[2 * i + 1]), x1 = to_f(b[2 * i]), y1 = to_f(b[2 * i + 1]);
       a[2 * i] = from_f<T>(x0 * ca - y0 * sa);
       a[2 * i + 1] = from_f<T>(y0 * ca + x0 * sa);
@@ -71,7 +82,7 @@ __device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs, 
   } else {  // element i of a pairs with element i of b
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      const float c = cs[i], s = sn[i] * sign, x = to_f(a[i]), y = to_f(b[i]);
+      const float c = cs[i], s = sn[i], x = to_f(a[i]), y = to_f(b[i]);
       a[i] = from_f<T>(x * c - y * s);
       b[i] = from_f<T>(y * c + x * s);
     }
@@ -79,7 +90,7 @@ __device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs, 
 }
 
 template <typename T, int VEC, bool IL, bool PAGED, int CAP>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     swa_rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ PagedTable<CAP> tab) {
   using R = typename Raw<T, VEC>::type;
   __shared__ RopeSmem s;
@@ -138,11 +149,9 @@ __global__ void __launch_bounds__(kRopeThreads)
       s.dst[tid][2] = vd;
     }
   }
-  if constexpr (PAGED) {
-    // (also the barrier before the angles; a CTA's page status is one word)
-    const int any_len = __syncthreads_or(bad == kPageErrLength), any_entry = __syncthreads_or(bad == kPageErrEntry);
-    if (tid == 0) a.page_err[blockIdx.x] = any_len ? kPageErrLength : (any_entry ? kPageErrEntry : 0);
-  }
+  if (PAGED && tid < n_tok) a.page_err[t0 + tid] = bad;
+  __syncthreads();
+
   // the angles of the CTA's tokens
   const int half = a.R >> 1;
   for (int x = tid; x < n_tok * 64; x += kRopeThreads) {
@@ -161,64 +170,78 @@ __global__ void __launch_bounds__(kRopeThreads)
       float sn, cs;
       sincospif(ht, &sn, &cs);
       s.cs[tk][i] = cs;
-      s.sn[tk][i] = sn;
+      s.sn[tk][i] = a.inverse ? -sn : sn;
     }
   }
   __syncthreads();
 
+  // The CTA's (token, head) rows in the order in which they lie in memory:
+  // tokens first where a row's stride is the smaller one (BNSD: the CTA's
+  // tokens of a head are contiguous), heads first otherwise (TND).  Thread =
+  // one place of a row (VEC elements and their partners) of every row_lanes-th
+  // row, four in flight.
   const int u = tid % a.units, lane = tid / a.units;
   if (lane >= a.row_lanes) return;
-  const float sign = a.inverse ? -1.f : 1.f;
-  const int n_rows = n_tok * a.H;
+  const int n_rows = a.tok_inner ? a.H << a.tok_shift : n_tok * a.H;
   constexpr int kBatch = 4;
+  struct Place {
+    int tk, sg, ia, ib;
+    int64_t src, dst;
+  };
+  auto locate = [&](int r, Place& w) -> bool {
+    if (r >= n_rows) return false;
+    int h;
+    if (a.tok_inner) {
+      w.tk = r & (a.tok - 1);
+      h = r >> a.tok_shift;
+      if (w.tk >= n_tok) return false;
+    } else {
+      w.tk = a.H == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.h_magic));
+      h = r - w.tk * a.H;
+    }
+    w.sg = h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2);
+    h -= w.sg == 0 ? 0 : (w.sg == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
+    const int rot = w.sg == 2 ? 0 : a.R;  // v is copied
+    // first chunk and its partner
+    if (!IL && u * VEC < (rot >> 1)) {
+      w.ia = u * VEC;
+      w.ib = (rot >> 1) + u * VEC;
+    } else {
+      w.ia = 2 * u * VEC;
+      w.ib = w.ia + VEC;
+    }
+    w.src = s.src[w.tk][w.sg] + h * a.src_h[w.sg];
+    w.dst = s.dst[w.tk][w.sg];
+    if (PAGED && w.dst < 0) return false;
+    w.dst += h * a.dst_h[w.sg];
+    return true;
+  };
   for (int r0 = lane; r0 < n_rows; r0 += kBatch * a.row_lanes) {
     R ra[kBatch], rb[kBatch];
-    int tk[kBatch], seg[kBatch], ia[kBatch], ib[kBatch];
-    int64_t d[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + k * a.row_lanes;
-      seg[k] = -1;
-      if (r >= n_rows) continue;
-      tk[k] = a.H == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.h_magic));
-      int h = r - tk[k] * a.H;
-      const int sg = h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2);
-      h -= sg == 0 ? 0 : (sg == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
-      const int rot = sg == 2 ? 0 : a.R;  // v is copied
-      // first chunk and its partner
-      if (!IL && u * VEC < (rot >> 1)) {
-        ia[k] = u * VEC;
-        ib[k] = (rot >> 1) + u * VEC;
-      } else {
-        ia[k] = 2 * u * VEC;
-        ib[k] = ia[k] + VEC;
-      }
-      const int64_t so = s.src[tk[k]][sg] + h * a.src_h[sg];
-      d[k] = s.dst[tk[k]][sg];
-      if (PAGED && d[k] < 0) continue;
-      d[k] += h * a.dst_h[sg];
-      seg[k] = sg;
-      const T* p = static_cast<const T*>(a.src[sg]);
-      if (rope_in_bounds(so + ia[k], VEC, a.n_src[sg], a.err)) ra[k] = *reinterpret_cast<const R*>(p + so + ia[k]);
-      if (ib[k] < a.D && rope_in_bounds(so + ib[k], VEC, a.n_src[sg], a.err))
-        rb[k] = *reinterpret_cast<const R*>(p + so + ib[k]);
+      Place w;
+      if (!locate(r0 + k * a.row_lanes, w)) continue;
+      const T* p = static_cast<const T*>(a.src[w.sg]);
+      if (rope_in_bounds(w.src + w.ia, VEC, a.n_src[w.sg], a.err))
+        ra[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + w.ia));
+      if (w.ib < a.D && rope_in_bounds(w.src + w.ib, VEC, a.n_src[w.sg], a.err))
+        rb[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + w.ib));
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (seg[k] < 0) continue;
+      Place w;  // (again: cheaper than keeping four of them)
+      if (!locate(r0 + k * a.row_lanes, w)) continue;
       alignas(16) T xa[VEC], xb[VEC];
       *reinterpret_cast<R*>(xa) = ra[k];
       *reinterpret_cast<R*>(xb) = rb[k];
-      const int sg = seg[k];
-      if (sg != 2 && u * 2 * VEC < a.R) {
-        // the chunk's pairs: VEC of them, from pair u * VEC on in both forms
-        turn<T, VEC, IL>(xa, xb, &s.cs[tk[k]][u * VEC], &s.sn[tk[k]][u * VEC], sign);
-      }
-      T* p = static_cast<T*>(a.dst[sg]);
-      if (rope_in_bounds(d[k] + ia[k], VEC, a.n_dst[sg], a.err))
-        *reinterpret_cast<R*>(p + d[k] + ia[k]) = *reinterpret_cast<R*>(xa);
-      if (ib[k] < a.D && rope_in_bounds(d[k] + ib[k], VEC, a.n_dst[sg], a.err))
-        *reinterpret_cast<R*>(p + d[k] + ib[k]) = *reinterpret_cast<R*>(xb);
+      // the chunk's pairs: VEC of them, from pair u * VEC on in both forms
+      if (w.sg != 2 && u * 2 * VEC < a.R) turn<T, VEC, IL>(xa, xb, &s.cs[w.tk][u * VEC], &s.sn[w.tk][u * VEC]);
+      T* p = static_cast<T*>(a.dst[w.sg]);
+      if (rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err))
+        *reinterpret_cast<R*>(p + w.dst + w.ia) = *reinterpret_cast<R*>(xa);
+      if (w.ib < a.D && rope_in_bounds(w.dst + w.ib, VEC, a.n_dst[w.sg], a.err))
+        *reinterpret_cast<R*>(p + w.dst + w.ib) = *reinterpret_cast<R*>(xb);
     }
   }
 }

@@ -488,10 +488,13 @@ class RopeParams:
         c.n_axes = geom.n_axes
         self._axes = (ctypes.c_int32 * max(half, 1))(*axes)
         c.pair_axis = ctypes.cast(self._axes, ctypes.POINTER(ctypes.c_int32))
-        if geom.inv_freq is not None:
-            if len(geom.inv_freq) != half:
-                raise ValueError(f"inv_freq names {len(geom.inv_freq)} pairs, rotary_dim has {half}")
-            self._freq = (ctypes.c_double * max(half, 1))(*[float(x) for x in geom.inv_freq])
+        if geom.inv_freq is not None and len(geom.inv_freq) != half:
+            raise ValueError(f"inv_freq names {len(geom.inv_freq)} pairs, rotary_dim has {half}")
+        freq = geom.inv_freq
+        if freq is None and c.base > 0:  # the library's default, formed once here instead of in every call
+            freq = [c.base ** (-2.0 * i / (2 * half)) for i in range(half)]
+        if freq is not None:
+            self._freq = (ctypes.c_double * max(half, 1))(*[float(x) for x in freq])
             c.inv_freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))
         self.torch_dtype = _TORCH_DTYPES[geom.dtype]
         self._ref = ctypes.byref(c)
@@ -502,6 +505,7 @@ class RopeParams:
         else:
             self.q_shape, self.k_shape = (rows, geom.N, geom.D), (rows, n_kv, geom.D)
         self.n_positions = c.n_axes * rows
+        self.bnsd = geom.layout == "BNSD"
 
     def ref(self):
         return self._ref
@@ -531,6 +535,8 @@ class PagedParams:
         self._ref = ctypes.byref(c)
         self.q_shape, self.kv_shape = (geom.T_q, geom.N, geom.D), (geom.T_q, geom.n_kv, geom.D)
         self.stat_shape, self.page_shape = (geom.T_q, geom.N), geom.page_shape()
+        self.table_shape, self.lens_shape = (geom.B, geom.max_pages), (geom.B,)
+        self.bnsd_pages = geom.cache_layout == "BNSD"
 
     def ref(self):
         return self._ref
@@ -544,69 +550,100 @@ def _paged_params(geom):
     return geom if isinstance(geom, PagedParams) else PagedParams(geom)
 
 
-def _expect(t, name, shape, dtype, device):
-    """A tensor of this shape and type on this device whose last dimension is contiguous."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} on "
-                         f"{t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: its last dimension must be contiguous")
+def _bad(t, name, shape, dtype, device, what=""):
+    raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on device {device}{what}, got {tuple(t.shape)} {t.dtype} "
+                     f"on {t.device} with strides {t.stride()}")
 
 
-def _expect_int32(t, name, numel, device):
-    if t.dtype is not torch.int32 or t.device != device or t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {numel} contiguous int32 on {device}, got {tuple(t.shape)} {t.dtype} on "
-                         f"{t.device}")
-
-
-def _strides(t, layout="TND"):
-    """swa_strides_t of a [B,N,S,D] / [T,N,D] tensor, None when dense."""
+def _arg(t, name, shape, dtype, device, bnsd=False):
+    """Pointer and swa_strides_t (None when dense) of a [B,N,S,D] / [T,N,D]
+    tensor of this shape and type on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _bad(t, name, shape, dtype, device)
     if t.is_contiguous():
-        return None
+        return t.data_ptr(), None
     s = t.stride()
-    return ctypes.byref(SwaStrides(s[0], s[2], s[1]) if layout == "BNSD" else SwaStrides(0, s[0], s[1]))
+    if s[-1] != 1 and shape[-1] != 1:
+        _bad(t, name, shape, dtype, device, " (the last dimension contiguous)")
+    return t.data_ptr(), ctypes.byref(SwaStrides(s[0], s[2], s[1]) if bnsd else SwaStrides(0, s[0], s[1]))
 
 
-def _page_strides(t, layout):
+def _dense(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of this shape and type on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _bad(t, name, shape, dtype, device, " (contiguous)")
+    return t.data_ptr()
+
+
+def _positions(t, numel, device):
+    if t.dtype is not torch.int32 or t.get_device() != device or t.numel() != numel or not t.is_contiguous():
+        _bad(t, "positions", (numel,), torch.int32, device, " (contiguous)")
+    return t.data_ptr()
+
+
+def _pages(t, name, p, device):
+    if t.dtype is not p.torch_dtype or t.shape != p.page_shape or t.get_device() != device:
+        _bad(t, name, p.page_shape, p.torch_dtype, device)
     if t.is_contiguous():
-        return None
+        return t.data_ptr(), None
     s = t.stride()
-    return ctypes.byref(SwaPageStrides(s[0], s[1], s[2]) if layout == "BNSD" else SwaPageStrides(s[0], s[2], s[1]))
+    if s[-1] != 1 and p.page_shape[-1] != 1:
+        _bad(t, name, p.page_shape, p.torch_dtype, device, " (the last dimension contiguous)")
+    order = (s[0], s[1], s[2]) if p.bnsd_pages else (s[0], s[2], s[1])
+    return t.data_ptr(), ctypes.byref(SwaPageStrides(*order))
 
 
-def _call_on(device, fn, *args, stream=None):
-    """fn(*args, stream handle) with `device` current, on its current stream unless one is given."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _check(fn(*args, s.cuda_stream))
-    with torch.cuda.device(device):
-        return _check(fn(*args, s.cuda_stream))
+def _table(t, p, device):
+    """Pointer and row stride of the block table."""
+    B, most = p.table_shape
+    if t.dtype is not torch.int32 or t.shape != p.table_shape or t.get_device() != device:
+        _bad(t, "block_table", p.table_shape, torch.int32, device)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    s = t.stride()
+    if (s[1] != 1 and most > 1) or (s[0] < most and B > 1):
+        _bad(t, "block_table", p.table_shape, torch.int32, device, " (rows contiguous and apart)")
+    return t.data_ptr(), s[0] if B > 1 else 0
+
+
+def _call_on(device, fn, args, stream):
+    """fn(*args, stream handle) with device index `device` current, on its
+    current stream unless one is given."""
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != SWA_OK:
+        _check(status)
 
 
 def _rope_call(fn, geom, q, k, positions, q_out, k_out, stream):
-    p = _rope_params(geom)
+    p = geom if type(geom) is RopeParams else _rope_params(geom)
     first = q if q is not None else k
     if first is None:
         raise ValueError("q or k is required")
-    dev, layout = first.device, p.geom.layout
-    outs = []
-    for name, t, out, shape in (("q", q, q_out, p.q_shape), ("k", k, k_out, p.k_shape)):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            outs.append(None)
-            continue
-        _expect(t, name, shape, p.torch_dtype, dev)
-        if out is None:
-            out = torch.empty(shape, dtype=p.torch_dtype, device=dev)
-        else:
-            _expect(out, name + "_out", shape, p.torch_dtype, dev)
-        outs.append(out)
-    _expect_int32(positions, "positions", p.n_positions, dev)
-    st = lambda t: None if t is None else _strides(t, layout)
-    _call_on(dev, fn, p.ref(), _ptr(q), st(q), _ptr(k), st(k), _ptr(positions), _ptr(outs[0]), st(outs[0]),
-             _ptr(outs[1]), st(outs[1]), stream=stream)
-    return outs[0], outs[1]
+    dev, dt, bnsd = first.get_device(), p.torch_dtype, p.bnsd
+    qp = qs = kp = ks = qop = qos = kop = kos = None
+    if q is not None:
+        qp, qs = _arg(q, "q", p.q_shape, dt, dev, bnsd)
+        if q_out is None:
+            q_out = torch.empty(p.q_shape, dtype=dt, device=q.device)
+        qop, qos = _arg(q_out, "q_out", p.q_shape, dt, dev, bnsd)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        kp, ks = _arg(k, "k", p.k_shape, dt, dev, bnsd)
+        if k_out is None:
+            k_out = torch.empty(p.k_shape, dtype=dt, device=k.device)
+        kop, kos = _arg(k_out, "k_out", p.k_shape, dt, dev, bnsd)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _call_on(dev, fn, (p._ref, qp, qs, kp, ks, _positions(positions, p.n_positions, dev), qop, qos, kop, kos), stream)
+    return q_out, k_out
 
 
 def rope(geom, q, k, positions, q_out=None, k_out=None, stream=None):
@@ -644,45 +681,37 @@ def paged_forward_workspace(geom, device="cuda:0"):
     return torch.empty(swa_paged_forward_workspace_size(_paged_params(geom)), dtype=torch.uint8, device=device)
 
 
-def _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev):
-    _expect(k_pages, "k_pages", p.page_shape, p.torch_dtype, dev)
-    _expect(v_pages, "v_pages", p.page_shape, p.torch_dtype, dev)
-    g = p.geom
-    if block_table.shape != (g.B, g.max_pages) or block_table.dtype is not torch.int32 or block_table.device != dev \
-            or (block_table.stride(1) != 1 and g.max_pages > 1) or (block_table.stride(0) < g.max_pages and g.B > 1):
-        raise ValueError(f"block_table: expected ({g.B}, {g.max_pages}) int32 on {dev} with contiguous rows, got "
-                         f"{tuple(block_table.shape)} {block_table.dtype} on {block_table.device}")
-    _expect_int32(kv_lens, "kv_lens", g.B, dev)
-    return block_table.stride(0) if g.B > 1 else 0
-
-
 def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, positions=None, q=None, q_out=None,
                  workspace=None, stream=None):
     """Enqueue swa_paged_append: the chunk's k and v [T_q, N_kv, D] into the
     pages; with `rope` (a RopeGeometry / RopeParams) k is rotated on the way, and
     q too, into q_out.  Returns q_out (None without q)."""
-    p = _paged_params(geom)
-    dev = k.device
-    _expect(k, "k", p.kv_shape, p.torch_dtype, dev)
-    _expect(v, "v", p.kv_shape, p.torch_dtype, dev)
-    table_stride = _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev)
-    r = None if rope is None else _rope_params(rope)
-    if positions is not None and r is not None:
-        _expect_int32(positions, "positions", r.n_positions, dev)
+    p = geom if type(geom) is PagedParams else _paged_params(geom)
+    dev, dt = k.get_device(), p.torch_dtype
+    kp, ks = _arg(k, "k", p.kv_shape, dt, dev)
+    vp, vs = _arg(v, "v", p.kv_shape, dt, dev)
+    kpp, kps = _pages(k_pages, "k_pages", p, dev)
+    vpp, vps = _pages(v_pages, "v_pages", p, dev)
+    tp, ts = _table(block_table, p, dev)
+    lp = _dense(kv_lens, "kv_lens", p.lens_shape, torch.int32, dev)
+    rr = pp = qp = qs = qop = qos = None
+    if rope is not None:
+        r = rope if type(rope) is RopeParams else _rope_params(rope)
+        rr = r._ref
+        if positions is not None:
+            pp = _positions(positions, r.n_positions, dev)
+    elif positions is not None:
+        raise ValueError("positions are taken with rope only")
     if q is not None:
-        _expect(q, "q", p.q_shape, p.torch_dtype, dev)
+        qp, qs = _arg(q, "q", p.q_shape, dt, dev)
         if q_out is None:
-            q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=dev)
+            q_out = torch.empty(p.q_shape, dtype=dt, device=q.device)
     if q_out is not None:
-        _expect(q_out, "q_out", p.q_shape, p.torch_dtype, dev)
+        qop, qos = _arg(q_out, "q_out", p.q_shape, dt, dev)
     if workspace is None:
-        workspace = paged_append_workspace(p, dev)
-    layout = p.geom.cache_layout
-    st = lambda t: None if t is None else _strides(t)
-    _call_on(dev, lib().swa_paged_append, p.ref(), _ptr(k), st(k), _ptr(v), st(v), _ptr(k_pages),
-             _page_strides(k_pages, layout), _ptr(v_pages), _page_strides(v_pages, layout), _ptr(block_table),
-             table_stride, _ptr(kv_lens), None if r is None else r.ref(), _ptr(positions), _ptr(q), st(q),
-             _ptr(q_out), st(q_out), _ptr(workspace), workspace.numel(), stream=stream)
+        workspace = paged_append_workspace(p, k.device)
+    _call_on(dev, lib().swa_paged_append, (p._ref, kp, ks, vp, vs, kpp, kps, vpp, vps, tp, ts, lp, rr, pp, qp, qs, qop,
+                                           qos, workspace.data_ptr(), workspace.nbytes), stream)
     return q_out
 
 
@@ -690,39 +719,36 @@ def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, sof
                   workspace=None, stream=None):
     """Enqueue swa_paged_forward: attention of the chunk's q [T_q, N, D] over
     the paged cache; returns (out, softmax_max, softmax_sum)."""
-    p = _paged_params(geom)
-    dev = q.device
-    _expect(q, "q", p.q_shape, p.torch_dtype, dev)
-    table_stride = _check_cache(p, k_pages, v_pages, block_table, kv_lens, dev)
+    p = geom if type(geom) is PagedParams else _paged_params(geom)
+    dev, dt = q.get_device(), p.torch_dtype
+    qp, qs = _arg(q, "q", p.q_shape, dt, dev)
+    kpp, kps = _pages(k_pages, "k_pages", p, dev)
+    vpp, vps = _pages(v_pages, "v_pages", p, dev)
+    tp, ts = _table(block_table, p, dev)
+    lp = _dense(kv_lens, "kv_lens", p.lens_shape, torch.int32, dev)
     if out is None:
-        out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=dev)
+        out = torch.empty(p.q_shape, dtype=dt, device=q.device)
     if softmax_max is None:
-        softmax_max = torch.empty(p.stat_shape, dtype=torch.float32, device=dev)
+        softmax_max = torch.empty(p.stat_shape, dtype=torch.float32, device=q.device)
     if softmax_sum is None:
-        softmax_sum = torch.empty(p.stat_shape, dtype=torch.float32, device=dev)
-    for t, name, shape, dt in ((out, "out", p.q_shape, p.torch_dtype),
-                               (softmax_max, "softmax_max", p.stat_shape, torch.float32),
-                               (softmax_sum, "softmax_sum", p.stat_shape, torch.float32)):
-        if t.shape != shape or t.dtype is not dt or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {tuple(shape)} {dt} on {dev}, got {tuple(t.shape)} "
-                             f"{t.dtype} on {t.device}")
+        softmax_sum = torch.empty(p.stat_shape, dtype=torch.float32, device=q.device)
+    op = _dense(out, "out", p.q_shape, dt, dev)
+    mp = _dense(softmax_max, "softmax_max", p.stat_shape, torch.float32, dev)
+    sp = _dense(softmax_sum, "softmax_sum", p.stat_shape, torch.float32, dev)
     if workspace is None:
-        workspace = paged_forward_workspace(p, dev)
-    layout = p.geom.cache_layout
-    _call_on(dev, lib().swa_paged_forward, p.ref(), _ptr(q), _strides(q), _ptr(k_pages),
-             _page_strides(k_pages, layout), _ptr(v_pages), _page_strides(v_pages, layout), _ptr(block_table),
-             table_stride, _ptr(kv_lens), _ptr(out), _ptr(softmax_max), _ptr(softmax_sum), _ptr(workspace),
-             workspace.numel(), stream=stream)
+        workspace = paged_forward_workspace(p, q.device)
+    _call_on(dev, lib().swa_paged_forward, (p._ref, qp, qs, kpp, kps, vpp, vps, tp, ts, lp, op, mp, sp,
+                                            workspace.data_ptr(), workspace.nbytes), stream)
     return out, softmax_max, softmax_sum
 
 
 def check_paged_append(geom, workspace, stream=None):
     """Wait for the stream and raise what the last paged_append with this workspace met on the device."""
-    _call_on(workspace.device, lib().swa_paged_append_status, _paged_params(geom).ref(), _ptr(workspace),
-             stream=stream)
+    _call_on(workspace.get_device(), lib().swa_paged_append_status, (_paged_params(geom).ref(), workspace.data_ptr()),
+             stream)
 
 
 def check_paged_forward(geom, workspace, stream=None):
     """Wait for the stream and raise what the last paged_forward with this workspace met on the device."""
-    _call_on(workspace.device, lib().swa_paged_forward_status, _paged_params(geom).ref(), _ptr(workspace),
-             stream=stream)
+    _call_on(workspace.get_device(), lib().swa_paged_forward_status, (_paged_params(geom).ref(), workspace.data_ptr()),
+             stream)

@@ -78,7 +78,7 @@ S = swa.SwaStrides
     (BAD, dict(fields=dict(rotary_dim=72))), (BAD, dict(fields=dict(rotary_dim=-8))),
     (UNSUP, dict(fields=dict(rotary_dim=12))), (BAD, dict(fields=dict(n_axes=0))), (BAD, dict(fields=dict(n_axes=5))),
     (BAD, dict(change=dict(sections=[16, 16]), fields=dict(n_axes=1))),
-    (BAD, dict(fields=dict(base=0.0))), (BAD, dict(fields=dict(base=float("inf")))),
+    (BAD, dict(fields=dict(inv_freq=None, base=0.0))), (BAD, dict(fields=dict(inv_freq=None, base=float("inf")))),
     (BAD, dict(change=dict(inv_freq=[float("nan")] * 32))), (BAD, dict(change=dict(inv_freq=[2.0 ** 21] * 32))),
     (BAD, dict(qs=S(0, 257, 64))), (BAD, dict(ks=S(0, -128, 64))), (BAD, dict(qos=S(0, 0, 64))),
     (BAD, dict(kos=S(0, 128, 8))), (BAD, dict(qs=S(0, 1 << 39, 64))),
