@@ -20,6 +20,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libswa.so")
 CHECKED_BUILD_DIR = os.path.join(PKG, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libswa_checked.so")
+# the CPython extension that calls the rotary and paged-cache entry points on torch tensors
+BIND_SOURCE = "swa_bind.cpp"
+BIND_PATH = os.path.join(PKG, "_swa_bind.so")
 SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_pair.cu", "swa_bwd_dkv.cu", "swa_bwd_dq.cu", "swa_aux.cu",
            "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged_tile.cu", "swa_paged.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,12 +49,40 @@ def is_stale(lib_path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def build_bind(verbose: bool = False) -> str:
+    """Compile the CPython extension against the installed torch; returns its path."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           os.path.join(CSRC, BIND_SOURCE), "-o", tmp, "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """Compile every translation unit for sm_103a and link libswa.so (or,
     with `checked`, the bounds-checked libswa_checked.so); returns its path."""
     lib_path = CHECKED_LIB_PATH if checked else LIB_PATH
     build_dir = CHECKED_BUILD_DIR if checked else BUILD_DIR
+    bind = force or is_stale(BIND_PATH)
     if not force and not is_stale(lib_path):
+        if bind:
+            build_bind(verbose)
         return lib_path
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
@@ -67,8 +98,11 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        pending = ex.submit(build_bind, verbose) if bind else None
         objs = list(ex.map(compile_one, SOURCES))
+        if pending is not None:
+            pending.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

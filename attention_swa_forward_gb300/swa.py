@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -16,6 +17,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libswa.so")
 CHECKED_LIB_PATH = os.path.join(_PKG, "libswa_checked.so")
+BIND_PATH = os.path.join(_PKG, "_swa_bind.so")
 
 SWA_OK = 0
 SWA_ERR_PARAM_NULLPTR = 161001
@@ -131,6 +133,8 @@ def lib() -> ctypes.CDLL:
     if override is not None:
         return override
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             _lib = _open(LIB_PATH, "attention_swa_forward_gb300.build.build()")
@@ -504,8 +508,7 @@ class RopeParams:
             self.q_shape, self.k_shape = (geom.B, geom.N, geom.S, geom.D), (geom.B, n_kv, geom.S, geom.D)
         else:
             self.q_shape, self.k_shape = (rows, geom.N, geom.D), (rows, n_kv, geom.D)
-        self.n_positions = c.n_axes * rows
-        self.bnsd = geom.layout == "BNSD"
+        self.addr = ctypes.addressof(c)
 
     def ref(self):
         return self._ref
@@ -533,10 +536,9 @@ class PagedParams:
         c.dtype = DTYPES[geom.dtype]
         self.torch_dtype = _TORCH_DTYPES[geom.dtype]
         self._ref = ctypes.byref(c)
-        self.q_shape, self.kv_shape = (geom.T_q, geom.N, geom.D), (geom.T_q, geom.n_kv, geom.D)
-        self.stat_shape, self.page_shape = (geom.T_q, geom.N), geom.page_shape()
-        self.table_shape, self.lens_shape = (geom.B, geom.max_pages), (geom.B,)
-        self.bnsd_pages = geom.cache_layout == "BNSD"
+        self.q_shape = (geom.T_q, geom.N, geom.D)
+        self.stat_shape = (geom.T_q, geom.N)
+        self.addr = ctypes.addressof(c)
 
     def ref(self):
         return self._ref
@@ -550,99 +552,46 @@ def _paged_params(geom):
     return geom if isinstance(geom, PagedParams) else PagedParams(geom)
 
 
-def _bad(t, name, shape, dtype, device, what=""):
-    raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on device {device}{what}, got {tuple(t.shape)} {t.dtype} "
-                     f"on {t.device} with strides {t.stride()}")
+_bind_module = None
 
 
-def _arg(t, name, shape, dtype, device, bnsd=False):
-    """Pointer and swa_strides_t (None when dense) of a [B,N,S,D] / [T,N,D]
-    tensor of this shape and type on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _bad(t, name, shape, dtype, device)
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] != 1:
-        _bad(t, name, shape, dtype, device, " (the last dimension contiguous)")
-    return t.data_ptr(), ctypes.byref(SwaStrides(s[0], s[2], s[1]) if bnsd else SwaStrides(0, s[0], s[1]))
+def _bind():
+    """The extension that checks the tensors of the calls below and makes them
+    (csrc/swa_bind.cpp, built in-tree with the library); raise if it is absent."""
+    global _bind_module
+    if _bind_module is None:
+        if not os.path.exists(BIND_PATH):
+            raise ImportError(f"{BIND_PATH} is missing: build it with attention_swa_forward_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_swa_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bind_module = module
+    return _bind_module
 
 
-def _dense(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor of this shape and type on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        _bad(t, name, shape, dtype, device, " (contiguous)")
-    return t.data_ptr()
+def _entry(library, name):
+    """Address of a C entry point of `library`."""
+    at = library.__dict__.get("_entries")
+    if at is None:
+        at = library._entries = {}
+    if name not in at:
+        at[name] = ctypes.cast(getattr(library, name), ctypes.c_void_p).value
+    return at[name]
 
 
-def _positions(t, numel, device):
-    if t.dtype is not torch.int32 or t.get_device() != device or t.numel() != numel or not t.is_contiguous():
-        _bad(t, "positions", (numel,), torch.int32, device, " (contiguous)")
-    return t.data_ptr()
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _pages(t, name, p, device):
-    if t.dtype is not p.torch_dtype or t.shape != p.page_shape or t.get_device() != device:
-        _bad(t, name, p.page_shape, p.torch_dtype, device)
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    s = t.stride()
-    if s[-1] != 1 and p.page_shape[-1] != 1:
-        _bad(t, name, p.page_shape, p.torch_dtype, device, " (the last dimension contiguous)")
-    order = (s[0], s[1], s[2]) if p.bnsd_pages else (s[0], s[2], s[1])
-    return t.data_ptr(), ctypes.byref(SwaPageStrides(*order))
-
-
-def _table(t, p, device):
-    """Pointer and row stride of the block table."""
-    B, most = p.table_shape
-    if t.dtype is not torch.int32 or t.shape != p.table_shape or t.get_device() != device:
-        _bad(t, "block_table", p.table_shape, torch.int32, device)
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    s = t.stride()
-    if (s[1] != 1 and most > 1) or (s[0] < most and B > 1):
-        _bad(t, "block_table", p.table_shape, torch.int32, device, " (rows contiguous and apart)")
-    return t.data_ptr(), s[0] if B > 1 else 0
-
-
-def _call_on(device, fn, args, stream):
-    """fn(*args, stream handle) with device index `device` current, on its
-    current stream unless one is given."""
-    if device < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if device == torch._C._cuda_getDevice():
-        status = fn(*args, s)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, s)
+def _rope_call(name, geom, q, k, positions, q_out, k_out, stream):
+    p = geom if type(geom) is RopeParams else _rope_params(geom)
+    if q_out is None and q is not None:
+        q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(p.k_shape, dtype=p.torch_dtype, device=k.device)
+    status = _bind().rope(_entry(lib(), name), p.addr, q, k, positions, q_out, k_out, _handle(stream))
     if status != SWA_OK:
         _check(status)
-
-
-def _rope_call(fn, geom, q, k, positions, q_out, k_out, stream):
-    p = geom if type(geom) is RopeParams else _rope_params(geom)
-    first = q if q is not None else k
-    if first is None:
-        raise ValueError("q or k is required")
-    dev, dt, bnsd = first.get_device(), p.torch_dtype, p.bnsd
-    qp = qs = kp = ks = qop = qos = kop = kos = None
-    if q is not None:
-        qp, qs = _arg(q, "q", p.q_shape, dt, dev, bnsd)
-        if q_out is None:
-            q_out = torch.empty(p.q_shape, dtype=dt, device=q.device)
-        qop, qos = _arg(q_out, "q_out", p.q_shape, dt, dev, bnsd)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if k is not None:
-        kp, ks = _arg(k, "k", p.k_shape, dt, dev, bnsd)
-        if k_out is None:
-            k_out = torch.empty(p.k_shape, dtype=dt, device=k.device)
-        kop, kos = _arg(k_out, "k_out", p.k_shape, dt, dev, bnsd)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    _call_on(dev, fn, (p._ref, qp, qs, kp, ks, _positions(positions, p.n_positions, dev), qop, qos, kop, kos), stream)
     return q_out, k_out
 
 
@@ -650,13 +599,13 @@ def rope(geom, q, k, positions, q_out=None, k_out=None, stream=None):
     """Enqueue swa_rope_forward: q and k (either may be None) rotated by their
     positions (int32, [n_axes, B*S] or [n_axes, B, S]); returns (q_out, k_out).
     q_out / k_out may be q / k themselves (in place)."""
-    return _rope_call(lib().swa_rope_forward, geom, q, k, positions, q_out, k_out, stream)
+    return _rope_call("swa_rope_forward", geom, q, k, positions, q_out, k_out, stream)
 
 
 def rope_backward(geom, dq_out, dk_out, positions, dq=None, dk=None, stream=None):
     """Enqueue swa_rope_backward: the gradients of rope()'s q and k from those
     of its results; returns (dq, dk)."""
-    return _rope_call(lib().swa_rope_backward, geom, dq_out, dk_out, positions, dq, dk, stream)
+    return _rope_call("swa_rope_backward", geom, dq_out, dk_out, positions, dq, dk, stream)
 
 
 def swa_paged_append_workspace_size(params: PagedParams) -> int:
@@ -687,31 +636,16 @@ def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, 
     pages; with `rope` (a RopeGeometry / RopeParams) k is rotated on the way, and
     q too, into q_out.  Returns q_out (None without q)."""
     p = geom if type(geom) is PagedParams else _paged_params(geom)
-    dev, dt = k.get_device(), p.torch_dtype
-    kp, ks = _arg(k, "k", p.kv_shape, dt, dev)
-    vp, vs = _arg(v, "v", p.kv_shape, dt, dev)
-    kpp, kps = _pages(k_pages, "k_pages", p, dev)
-    vpp, vps = _pages(v_pages, "v_pages", p, dev)
-    tp, ts = _table(block_table, p, dev)
-    lp = _dense(kv_lens, "kv_lens", p.lens_shape, torch.int32, dev)
-    rr = pp = qp = qs = qop = qos = None
-    if rope is not None:
-        r = rope if type(rope) is RopeParams else _rope_params(rope)
-        rr = r._ref
-        if positions is not None:
-            pp = _positions(positions, r.n_positions, dev)
-    elif positions is not None:
-        raise ValueError("positions are taken with rope only")
-    if q is not None:
-        qp, qs = _arg(q, "q", p.q_shape, dt, dev)
-        if q_out is None:
-            q_out = torch.empty(p.q_shape, dtype=dt, device=q.device)
-    if q_out is not None:
-        qop, qos = _arg(q_out, "q_out", p.q_shape, dt, dev)
+    r = rope if rope is None or type(rope) is RopeParams else _rope_params(rope)
+    if q is not None and q_out is None:
+        q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=q.device)
     if workspace is None:
         workspace = paged_append_workspace(p, k.device)
-    _call_on(dev, lib().swa_paged_append, (p._ref, kp, ks, vp, vs, kpp, kps, vpp, vps, tp, ts, lp, rr, pp, qp, qs, qop,
-                                           qos, workspace.data_ptr(), workspace.nbytes), stream)
+    status = _bind().paged_append(_entry(lib(), "swa_paged_append"), p.addr, k, v, k_pages, v_pages, block_table,
+                                  kv_lens, 0 if r is None else r.addr, positions, q, q_out, workspace,
+                                  _handle(stream))
+    if status != SWA_OK:
+        _check(status)
     return q_out
 
 
@@ -720,35 +654,31 @@ def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, sof
     """Enqueue swa_paged_forward: attention of the chunk's q [T_q, N, D] over
     the paged cache; returns (out, softmax_max, softmax_sum)."""
     p = geom if type(geom) is PagedParams else _paged_params(geom)
-    dev, dt = q.get_device(), p.torch_dtype
-    qp, qs = _arg(q, "q", p.q_shape, dt, dev)
-    kpp, kps = _pages(k_pages, "k_pages", p, dev)
-    vpp, vps = _pages(v_pages, "v_pages", p, dev)
-    tp, ts = _table(block_table, p, dev)
-    lp = _dense(kv_lens, "kv_lens", p.lens_shape, torch.int32, dev)
     if out is None:
-        out = torch.empty(p.q_shape, dtype=dt, device=q.device)
+        out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=q.device)
     if softmax_max is None:
         softmax_max = torch.empty(p.stat_shape, dtype=torch.float32, device=q.device)
     if softmax_sum is None:
         softmax_sum = torch.empty(p.stat_shape, dtype=torch.float32, device=q.device)
-    op = _dense(out, "out", p.q_shape, dt, dev)
-    mp = _dense(softmax_max, "softmax_max", p.stat_shape, torch.float32, dev)
-    sp = _dense(softmax_sum, "softmax_sum", p.stat_shape, torch.float32, dev)
     if workspace is None:
         workspace = paged_forward_workspace(p, q.device)
-    _call_on(dev, lib().swa_paged_forward, (p._ref, qp, qs, kpp, kps, vpp, vps, tp, ts, lp, op, mp, sp,
-                                            workspace.data_ptr(), workspace.nbytes), stream)
+    status = _bind().paged_forward(_entry(lib(), "swa_paged_forward"), p.addr, q, k_pages, v_pages, block_table,
+                                   kv_lens, out, softmax_max, softmax_sum, workspace, _handle(stream))
+    if status != SWA_OK:
+        _check(status)
     return out, softmax_max, softmax_sum
+
+
+def _status_of(fn, geom, workspace, stream):
+    with torch.cuda.device(workspace.device):
+        _check(fn(_paged_params(geom).ref(), workspace.data_ptr(), _stream_handle(stream)))
 
 
 def check_paged_append(geom, workspace, stream=None):
     """Wait for the stream and raise what the last paged_append with this workspace met on the device."""
-    _call_on(workspace.get_device(), lib().swa_paged_append_status, (_paged_params(geom).ref(), workspace.data_ptr()),
-             stream)
+    _status_of(lib().swa_paged_append_status, geom, workspace, stream)
 
 
 def check_paged_forward(geom, workspace, stream=None):
     """Wait for the stream and raise what the last paged_forward with this workspace met on the device."""
-    _call_on(workspace.get_device(), lib().swa_paged_forward_status, (_paged_params(geom).ref(), workspace.data_ptr()),
-             stream)
+    _status_of(lib().swa_paged_forward_status, geom, workspace, stream)
