@@ -102,6 +102,7 @@ struct PagedArgs {
   float scale_log2;
   int32_t splits;     // CTAs per item along the keys, at most
   int32_t par, cap, least;  // paged_split
+  int32_t cluster;    // few-row kernel: the splits are a cluster, which joins them itself
   int32_t rows_pad;   // rows of a partial tile
   int32_t stall;      // test hook (kStallPaged)
   int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128

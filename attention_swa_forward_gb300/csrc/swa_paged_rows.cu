@@ -68,19 +68,55 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The CTAs of a cluster: barrier over all their threads (every thread arrives
+// and waits; orders shared-memory accesses across the cluster), this CTA's
+// rank, and reads of a peer's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int DP>
 struct RowsSmem {
   static constexpr int kRowBytes = DP * 2;
   static constexpr int kGroupBytes = 16 * kRowBytes;  // 16 keys of K or V
   alignas(128) uint8_t ring[kRowsWarps][kRowsStages][2][kGroupBytes];
   float ml[kRowsWarps][kRowsTile][2];
-  // the warps' O, [warp][row][DP + 4], reuses the ring
+  // the warps' O, [warp][row][DP + 4], reuses the ring, and behind it the
+  // CTA's own joined rows and their maxima and sums, for the cluster
   static constexpr int kOPitch = DP + 4;
-  static_assert(sizeof(float) * kRowsWarps * kRowsTile * kOPitch <= sizeof(uint8_t) * kRowsWarps * kRowsStages * 2 * kGroupBytes,
-                "join space");
+  static constexpr int kRingBytes = kRowsWarps * kRowsStages * 2 * kGroupBytes;
+  static constexpr int kJoinAt = kRowsWarps * kRowsTile * kOPitch;  // floats
+  static constexpr int kMlAt = kJoinAt + kRowsTile * DP;
+  static_assert(4 * (kMlAt + 2 * kRowsTile) <= kRingBytes, "join space");
 };
 
-template <int DP, bool F16, int CAP>
+// CL: the splits of an item are the CTAs of one cluster, which join their rows
+// through each other's shared memory; otherwise partial rows go to the
+// workspace and swa_paged_join_kernel joins them.
+template <int DP, bool F16, bool CL, int CAP>
 __global__ void __launch_bounds__(kRowsThreads, 2)
     swa_paged_rows_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab) {
   using Smem = RowsSmem<DP>;
@@ -140,7 +176,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   int st0, st1, active;
   paged_split(steps, a.par, a.cap, a.least, split, &st0, &st1, &active);
   const bool direct = active <= 1;  // no other CTA has keys of this item: write the result itself
-  if (split > 0 && split >= active) {  // nothing to do (split 0 writes the result of an empty item)
+  if (!CL && split > 0 && split >= active) {  // nothing to do (split 0 writes the result of an empty item)
     if (threadIdx.x == 0) a.page_err[item * a.splits + split] = 0;
     return;
   }
@@ -366,6 +402,19 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   if (threadIdx.x == 0)
     a.page_err[item * a.splits + split] = any_len ? kPageErrLength : (any_entry ? kPageErrEntry : 0);
 
+  // four columns of row r, from their maximum, sum and unnormalised values
+  auto finish = [&](int r, int col, float M, float L, const float (&acc)[4]) {
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const int i = row_token(r, a.gs_magic), h = w.vh * a.gs + (r - i * a.gs);
+    const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
+    if (col < g.D && in_bounds(row * g.D + col, 4, a.n_out, a.err))
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D + col) =
+          make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
+    if (col == 0 && in_bounds(row, 1, a.n_stats, a.err)) {
+      if (a.smax) a.smax[row] = M == -INFINITY ? -INFINITY : M * kLn2;
+      if (a.ssum) a.ssum[row] = L;
+    }
+  };
   // join the four warps: thread = 4 columns of a row
   constexpr int kCols4 = DP / 4;
   for (int x = threadIdx.x; x < n_rows * kCols4; x += kRowsThreads) {
@@ -385,22 +434,43 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       acc[2] += ov.z * f;
       acc[3] += ov.w * f;
     }
-    if (!direct) {
+    if (CL) {
+      *reinterpret_cast<float4*>(so + Smem::kJoinAt + r * DP + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (col == 0) *reinterpret_cast<float2*>(so + Smem::kMlAt + 2 * r) = make_float2(M, L);
+    } else if (!direct) {
       const int64_t pr = (item * a.splits + split) * a.rows_pad + r;
       *reinterpret_cast<float4*>(a.part_o + pr * DP + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (col == 0) a.part_ml[pr] = make_float2(M, L);
     } else {
-      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-      const int i = row_token(r, a.gs_magic), h = w.vh * a.gs + (r - i * a.gs);
-      const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
-      if (col < g.D && in_bounds(row * g.D + col, 4, a.n_out, a.err))
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D + col) =
-            make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
-      if (col == 0 && in_bounds(row, 1, a.n_stats, a.err)) {
-        if (a.smax) a.smax[row] = M == -INFINITY ? -INFINITY : M * kLn2;
-        if (a.ssum) a.ssum[row] = L;
-      }
+      finish(r, col, M, L, acc);
     }
+  }
+  if constexpr (CL) {
+    // row r of the item is finished by the CTA of rank r mod splits
+    cluster_sync();
+    const uint32_t rank = cluster_rank(), mine = smem_u32(so + Smem::kJoinAt), mine_ml = smem_u32(so + Smem::kMlAt);
+    for (int x = threadIdx.x;; x += kRowsThreads) {
+      const int r = static_cast<int>(rank) + x / kCols4 * a.splits, col = (x % kCols4) * 4;
+      if (r >= n_rows) break;
+      float M = -INFINITY;
+#pragma unroll 8
+      for (int v = 0; v < a.splits; ++v) M = fmaxf(M, ld_peer2(peer_smem(mine_ml + 8 * r, v)).x);
+      const float ms = M == -INFINITY ? 0.f : M;
+      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int v = 0; v < a.splits; ++v) {
+        const float2 ml = ld_peer2(peer_smem(mine_ml + 8 * r, v));
+        const float4 ov = ld_peer4(peer_smem(mine + 4 * (r * DP + col), v));
+        const float f = ex2_approx(ml.x - ms);
+        L += ml.y * f;
+        acc[0] += ov.x * f;
+        acc[1] += ov.y * f;
+        acc[2] += ov.z * f;
+        acc[3] += ov.w * f;
+      }
+      finish(r, col, M, L, acc);
+    }
+    cluster_sync();  // a CTA's shared memory stays until its peers have read it
   }
   if (a.overlap && blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();  // (no early return: split 0 always runs)
 }
@@ -510,14 +580,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-template <int DP, bool F16, int CAP>
+template <int DP, bool F16, bool CL, int CAP>
 cudaError_t launch_rows_t(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream) {
   const size_t smem = sizeof(RowsSmem<DP>);
+  auto kernel = swa_paged_rows_kernel<DP, F16, CL, CAP>;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit(swa_paged_rows_kernel<DP, F16, CAP>, smem, smem_set);
+  const cudaError_t e = set_smem_limit(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(swa_paged_rows_kernel<DP, F16, CAP>, dim3(tab.n_items, a.splits), dim3(kRowsThreads), smem, stream,
-                    a, tab);
+  const dim3 grid(tab.n_items, a.splits), block(kRowsThreads);
+  if constexpr (!CL) {
+    return launch_pdl(kernel, grid, block, smem, stream, a, tab);
+  } else {
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(a.splits);
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, tab);
+  }
 }
 
 template <int DP, bool F16, int CAP>
@@ -535,9 +624,14 @@ cudaError_t launch_join_t(const PagedArgs& a, const PagedTable<CAP>& tab, int st
 template <int CAP>
 cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream) {
   if (tab.n_items == 0) return cudaSuccess;
+  if (a.cluster) {
+    if (a.g.D <= 64)
+      return a.f16 ? launch_rows_t<64, true, true>(a, tab, stream) : launch_rows_t<64, false, true>(a, tab, stream);
+    return a.f16 ? launch_rows_t<128, true, true>(a, tab, stream) : launch_rows_t<128, false, true>(a, tab, stream);
+  }
   if (a.g.D <= 64)
-    return a.f16 ? launch_rows_t<64, true>(a, tab, stream) : launch_rows_t<64, false>(a, tab, stream);
-  return a.f16 ? launch_rows_t<128, true>(a, tab, stream) : launch_rows_t<128, false>(a, tab, stream);
+    return a.f16 ? launch_rows_t<64, true, false>(a, tab, stream) : launch_rows_t<64, false, false>(a, tab, stream);
+  return a.f16 ? launch_rows_t<128, true, false>(a, tab, stream) : launch_rows_t<128, false, false>(a, tab, stream);
 }
 template <int CAP>
 cudaError_t launch_paged_join(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream) {

@@ -352,3 +352,23 @@ def test_prompt_in_chunks_then_tokens_equals_the_dense_forward():
         assert ((ss / want[2][c]) - 1).abs().max() <= 2 * (2 * e + S * 2.0 ** -24)
         at += m
     assert at == S
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    """Every parameter drawn at once."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (1,), generator=g))]
+    num = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    N_kv = pick(1, 2, 3)
+    B = num(1, 6)
+    q_lens = [pick(0, 1, 1, 2, num(1, 20), num(1, 200)) for _ in range(B)]
+    q_lens[num(0, B - 1)] = num(1, 150)
+    kv_lens = [max(0, n + pick(0, 0, num(0, 40), num(0, 900)) - pick(0, 0, 0, num(0, 5))) for n in q_lens]
+    kw = dict(N=N_kv * pick(1, 2, 3, 4, 5, 8, 16, 17), N_kv=N_kv, D=8 * num(1, 16), dtype=pick("bf16", "fp16"),
+              cache_layout=pick("BNSD", "TND"), sparse_mode=pick(0, 4, 4, 4))
+    if kw["sparse_mode"] == 4:
+        kw.update(pre_tokens=pick(INF, num(0, 300), num(-3, 20)), next_tokens=pick(0, 0, num(3, 40), INF))
+    geom = geometry(q_lens, kv_lens, 16 * pick(1, 2, 3, 5, 8, 9), **kw)
+    geom.max_kv_len = pick(0, max(max(kv_lens), 1))
+    check(geom, kv_lens, seed)
