@@ -132,7 +132,7 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
     const double turns = f / kTwoPi;
     double frac = turns - std::floor(turns);
     if (frac >= 1.0) frac = 0.0;  // a tiny negative angle rounds up to a whole turn
-    a.freq[i] = static_cast<uint64_t>(std::ldexp(frac, 64));
+    a.freq[i] = static_cast<uint64_t>(frac * 18446744073709551616.0);  // 2^64, exact
     a.axis[i] = static_cast<uint8_t>(ax);
   }
   return SWA_OK;

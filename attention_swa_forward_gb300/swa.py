@@ -227,6 +227,9 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.swa_paged_append_status.restype = st
     L.swa_paged_forward_status.argtypes = [PP, vp, vp]
     L.swa_paged_forward_status.restype = st
+    # addresses for the extension module, which calls them on tensors
+    L.entries = {n: ctypes.cast(getattr(L, n), vp).value
+                 for n in ("swa_rope_forward", "swa_rope_backward", "swa_paged_append", "swa_paged_forward")}
     L.swa_last_error.argtypes = []
     L.swa_last_error.restype = ctypes.c_char_p
     return L
@@ -558,25 +561,18 @@ _bind_module = None
 def _bind():
     """The extension that checks the tensors of the calls below and makes them
     (csrc/swa_bind.cpp, built in-tree with the library); raise if it is absent."""
+    return _bind_module if _bind_module is not None else _load_bind()
+
+
+def _load_bind():
     global _bind_module
-    if _bind_module is None:
-        if not os.path.exists(BIND_PATH):
-            raise ImportError(f"{BIND_PATH} is missing: build it with attention_swa_forward_gb300.build.build()")
-        spec = importlib.util.spec_from_file_location("_swa_bind", BIND_PATH)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        _bind_module = module
-    return _bind_module
-
-
-def _entry(library, name):
-    """Address of a C entry point of `library`."""
-    at = library.__dict__.get("_entries")
-    if at is None:
-        at = library._entries = {}
-    if name not in at:
-        at[name] = ctypes.cast(getattr(library, name), ctypes.c_void_p).value
-    return at[name]
+    if not os.path.exists(BIND_PATH):
+        raise ImportError(f"{BIND_PATH} is missing: build it with attention_swa_forward_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_swa_bind", BIND_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _bind_module = module
+    return module
 
 
 def _handle(stream):
@@ -589,7 +585,7 @@ def _rope_call(name, geom, q, k, positions, q_out, k_out, stream):
         q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=q.device)
     if k_out is None and k is not None:
         k_out = torch.empty(p.k_shape, dtype=p.torch_dtype, device=k.device)
-    status = _bind().rope(_entry(lib(), name), p.addr, q, k, positions, q_out, k_out, _handle(stream))
+    status = _bind().rope(lib().entries[name], p.addr, q, k, positions, q_out, k_out, _handle(stream))
     if status != SWA_OK:
         _check(status)
     return q_out, k_out
@@ -641,7 +637,7 @@ def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, 
         q_out = torch.empty(p.q_shape, dtype=p.torch_dtype, device=q.device)
     if workspace is None:
         workspace = paged_append_workspace(p, k.device)
-    status = _bind().paged_append(_entry(lib(), "swa_paged_append"), p.addr, k, v, k_pages, v_pages, block_table,
+    status = _bind().paged_append(lib().entries["swa_paged_append"], p.addr, k, v, k_pages, v_pages, block_table,
                                   kv_lens, 0 if r is None else r.addr, positions, q, q_out, workspace,
                                   _handle(stream))
     if status != SWA_OK:
@@ -662,7 +658,7 @@ def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, sof
         softmax_sum = torch.empty(p.stat_shape, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = paged_forward_workspace(p, q.device)
-    status = _bind().paged_forward(_entry(lib(), "swa_paged_forward"), p.addr, q, k_pages, v_pages, block_table,
+    status = _bind().paged_forward(lib().entries["swa_paged_forward"], p.addr, q, k_pages, v_pages, block_table,
                                    kv_lens, out, softmax_max, softmax_sum, workspace, _handle(stream))
     if status != SWA_OK:
         _check(status)
