@@ -147,15 +147,22 @@ void set_split(RopeArgs& a, int dtype, int64_t rows) {
   a.row_lanes = kRopeThreads / a.units;
   const int x = a.heads[0] ? 0 : 1;
   a.tok_inner = a.src_r[x] < a.src_h[x] ? 1 : 0;
-  // few tokens: one per CTA, so that every SM has its four; many: up to 8,
-  // while they stay within 80 KB (fp32, 12345 tokens of 12 KB: 49 us with 4,
-  // 52 with 8)
+  // Tokens per CTA: the fewest token times over all rounds of resident CTAs,
+  // a CTA costing about one token beside its own; a CTA's tokens stay within
+  // 80 KB.  32768 tokens of 40 heads in BNSD: 106 us with 8 (7 rounds), 112
+  // with 16, 116 with 4.
+  const int64_t slots = kSms * (a.heads[2] ? kAppendResident : kRopeResident);
   const int64_t bytes = int64_t(a.H) * a.D * (dtype == SWA_DTYPE_FP32 ? 4 : 2);
-  a.tok = 1;
-  while (a.tok < kRopeMaxTok && rows >= 2 * a.tok * 4 * kSms && 2 * a.tok * bytes <= 80 * 1024) {
-    a.tok *= 2;
-    ++a.tok_shift;
+  int64_t best = 0;
+  for (int tok = 1; tok <= (a.tok_inner ? 8 : kRopeMaxTok) && (tok == 1 || tok * bytes <= 80 * 1024);
+       tok += a.tok_inner ? tok : 1) {
+    const int64_t cost = ceil_div(ceil_div(rows, tok), slots) * (tok + 1);
+    if (best == 0 || cost < best) {
+      best = cost;
+      a.tok = tok;
+    }
   }
+  while ((1 << a.tok_shift) < a.tok) ++a.tok_shift;
 }
 
 swa_status_t rope_call(const swa_rope_params_t* p, const void* q, const swa_strides_t* q_s, const void* k,

@@ -42,7 +42,8 @@ struct PagedGeom {
 };
 
 // ------------------------------------------------------- rotary / append --
-constexpr int kRopeMaxTok = 8;  // rows (tokens) per CTA at most
+constexpr int kRopeMaxTok = 16;  // rows (tokens) per CTA at most
+constexpr int kRopeResident = 4, kAppendResident = 5;  // CTAs per SM
 constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
@@ -58,7 +59,7 @@ struct RopeArgs {
   int32_t D, R;
   int32_t units;      // 2 * VEC-element units of a head row
   int32_t row_lanes;  // rows a CTA takes at a time: threads / units
-  int32_t tok, tok_shift;  // tokens per CTA, a power of two
+  int32_t tok, tok_shift;  // tokens per CTA (tok_inner: a power of two, 1 << tok_shift)
   int32_t tok_inner;  // 1: walk the tokens of a head first
   int32_t n_axes, inverse;
   int32_t S;          // rows per batch

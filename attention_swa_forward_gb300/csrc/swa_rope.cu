@@ -1,7 +1,7 @@
 // swa_rope.cu — rotary positions of q and k, and the append of a chunk's keys
 // and values to the paged cache (include/swa.h).
 //
-// One kernel: a CTA takes up to 8 tokens, all heads of q, k (and v) of each.
+// One kernel: a CTA takes up to 16 tokens, all heads of q, k (and v) of each.
 // Pair i of a row at position p turns by p * inv_freq[i].  The angle is kept as
 // a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1)):
 // p * F_i mod 2^64 is the angle modulo a turn, exact but for the rounding of
@@ -90,7 +90,7 @@ __device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs_,
 }
 
 template <typename T, int VEC, bool IL, bool PAGED, int CAP>
-__global__ void __launch_bounds__(kRopeThreads, 4)
+__global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeResident)
     swa_rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ PagedTable<CAP> tab) {
   using R = typename Raw<T, VEC>::type;
   __shared__ RopeSmem s;
@@ -179,11 +179,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
   // tokens first where a row's stride is the smaller one (BNSD: the CTA's
   // tokens of a head are contiguous), heads first otherwise (TND).  Thread =
   // one place of a row (VEC elements and their partners) of every row_lanes-th
-  // row, four in flight.
+  // row, a few in flight.
   const int u = tid % a.units, lane = tid / a.units;
   if (lane >= a.row_lanes) return;
   const int n_rows = a.tok_inner ? a.H << a.tok_shift : n_tok * a.H;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = PAGED ? 2 : 4;
   struct Place {
     int tk, sg, ia, ib;
     int64_t src, dst;
