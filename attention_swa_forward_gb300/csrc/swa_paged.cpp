@@ -96,6 +96,20 @@ swa_status_t tensor_strides(const swa_strides_t* given, int32_t layout, int64_t 
   return SWA_OK;
 }
 
+// No C++ exception leaves a C entry point.
+template <typename F>
+swa_status_t guarded(F&& body) noexcept {
+  try {
+    try {
+      return body();
+    } catch (...) {
+      return fail(SWA_ERR_CUDA, "out of host memory");
+    }
+  } catch (...) {  // (not even for the message)
+    return SWA_ERR_CUDA;
+  }
+}
+
 // ----------------------------------------------------------------- rotary --
 swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
   if (!p) return fail(SWA_ERR_PARAM_NULLPTR, "params is NULL");
@@ -239,7 +253,8 @@ swa_status_t paged_plan(const swa_paged_params_t* p, PagedPlan& plan) {
     return fail(SWA_ERR_PARAM_INVALID, "sparse_mode should be 0 or 4, got %d", p->sparse_mode);
   if (p->sparse_mode == 4 && (long double)p->pre_tokens + (long double)p->next_tokens < 0)
     return fail(SWA_ERR_PARAM_INVALID, "pre_tokens + next_tokens < 0: every row would be empty");
-  if (!std::isfinite(p->scale)) return fail(SWA_ERR_PARAM_INVALID, "scale is not finite");
+  if (!std::isfinite(static_cast<float>(p->scale * kLog2e)))
+    return fail(SWA_ERR_PARAM_INVALID, "scale is not a finite fp32 number");
   if (p->cache_layout != SWA_LAYOUT_BNSD && p->cache_layout != SWA_LAYOUT_TND)
     return fail(SWA_ERR_PARAM_INVALID, "cache_layout %d is neither BNSD (0) nor TND (1)", p->cache_layout);
   if (p->num_pages < 1 || p->num_pages > 2147483647)
@@ -584,15 +599,19 @@ swa_status_t swa_rope_forward(const swa_rope_params_t* p, const void* q, const s
                               const swa_strides_t* k_strides, const int32_t* positions, void* q_out,
                               const swa_strides_t* q_out_strides, void* k_out, const swa_strides_t* k_out_strides,
                               swa_stream_t stream) {
-  return rope_call(p, q, q_strides, k, k_strides, positions, q_out, q_out_strides, k_out, k_out_strides, 0, stream);
+  return guarded([&]() -> swa_status_t {
+    return rope_call(p, q, q_strides, k, k_strides, positions, q_out, q_out_strides, k_out, k_out_strides, 0, stream);
+  });
 }
 
 swa_status_t swa_rope_backward(const swa_rope_params_t* p, const void* dq_out, const swa_strides_t* dq_out_strides,
                                const void* dk_out, const swa_strides_t* dk_out_strides, const int32_t* positions,
                                void* dq, const swa_strides_t* dq_strides, void* dk, const swa_strides_t* dk_strides,
                                swa_stream_t stream) {
-  return rope_call(p, dq_out, dq_out_strides, dk_out, dk_out_strides, positions, dq, dq_strides, dk, dk_strides, 1,
-                   stream);
+  return guarded([&]() -> swa_status_t {
+    return rope_call(p, dq_out, dq_out_strides, dk_out, dk_out_strides, positions, dq, dq_strides, dk, dk_strides, 1,
+                     stream);
+  });
 }
 
 void swa_paged_params_default(swa_paged_params_t* p) {
@@ -604,12 +623,14 @@ void swa_paged_params_default(swa_paged_params_t* p) {
 }
 
 swa_status_t swa_paged_append_workspace_size(const swa_paged_params_t* p, size_t* bytes) {
-  if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
-  PagedPlan plan;
-  const swa_status_t st = paged_plan(p, plan);
-  if (st != SWA_OK) return st;
-  *bytes = append_bytes(p);
-  return SWA_OK;
+  return guarded([&]() -> swa_status_t {
+    if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
+    PagedPlan plan;
+    const swa_status_t st = paged_plan(p, plan);
+    if (st != SWA_OK) return st;
+    *bytes = append_bytes(p);
+    return SWA_OK;
+  });
 }
 
 swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const swa_strides_t* k_strides,
@@ -620,110 +641,114 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
                               const int32_t* positions, const void* q, const swa_strides_t* q_strides, void* q_out,
                               const swa_strides_t* q_out_strides, void* workspace, size_t workspace_bytes,
                               swa_stream_t stream) {
-  PagedPlan plan;
-  swa_status_t st = paged_plan(p, plan);
-  if (st != SWA_OK) return st;
-  RopeArgs a{};
-  if (rope) {
-    int64_t rope_kv;
-    if ((st = rope_plan(rope, a, &rope_kv)) != SWA_OK) return st;
-    if (rope->layout != SWA_LAYOUT_TND || rope->B * rope->S != p->T_q || rope->N != p->N || rope_kv != plan.N_kv ||
-        rope->D != p->D || rope->dtype != p->dtype)
-      return fail(SWA_ERR_PARAM_INVALID, "rope must be TND with B * S = T_q and the cache's N, N_kv, D and dtype");
-    if (reinterpret_cast<uintptr_t>(positions) & 3u)
-      return fail(SWA_ERR_PARAM_INVALID, "positions must be 4-byte aligned");
-  } else if (positions || q || q_out) {
-    return fail(SWA_ERR_PARAM_INVALID, "positions, q and q_out are taken with rope only");
-  }
-  if ((q == nullptr) != (q_out == nullptr)) return fail(SWA_ERR_PARAM_NULLPTR, "q and q_out come together");
-  if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
-  if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
-  st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.pg);
-  if (st != SWA_OK) return st;
-  const size_t need = append_bytes(p);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
+  return guarded([&]() -> swa_status_t {
+    PagedPlan plan;
+    swa_status_t st = paged_plan(p, plan);
+    if (st != SWA_OK) return st;
+    RopeArgs a{};
+    if (rope) {
+      int64_t rope_kv;
+      if ((st = rope_plan(rope, a, &rope_kv)) != SWA_OK) return st;
+      if (rope->layout != SWA_LAYOUT_TND || rope->B * rope->S != p->T_q || rope->N != p->N || rope_kv != plan.N_kv ||
+          rope->D != p->D || rope->dtype != p->dtype)
+        return fail(SWA_ERR_PARAM_INVALID, "rope must be TND with B * S = T_q and the cache's N, N_kv, D and dtype");
+      if (reinterpret_cast<uintptr_t>(positions) & 3u)
+        return fail(SWA_ERR_PARAM_INVALID, "positions must be 4-byte aligned");
+    } else if (positions || q || q_out) {
+      return fail(SWA_ERR_PARAM_INVALID, "positions, q and q_out are taken with rope only");
+    }
+    if ((q == nullptr) != (q_out == nullptr)) return fail(SWA_ERR_PARAM_NULLPTR, "q and q_out come together");
+    if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
+    if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
+    st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.pg);
+    if (st != SWA_OK) return st;
+    const size_t need = append_bytes(p);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
 
-  a.D = static_cast<int32_t>(p->D);
-  const void* src[3] = {q, k, v};
-  const swa_strides_t* ss[3] = {q_strides, k_strides, v_strides};
-  const int64_t heads[3] = {q ? p->N : 0, plan.N_kv, plan.N_kv};
-  const char* names[3] = {"q", "k", "v"};
-  for (int x = 0; x < 3; ++x) {
-    if (!src[x]) continue;
-    swa_strides_t s;
-    int64_t n;
-    st = tensor_strides(ss[x], SWA_LAYOUT_TND, 1, p->T_q, heads[x], p->D, false, names[x], &s, &n);
-    if (st != SWA_OK) return st;
-    a.src[x] = src[x];
-    a.src_r[x] = s.row;
-    a.src_h[x] = s.head;
-    a.n_src[x] = less_slack(n);
-    a.heads[x] = static_cast<int32_t>(heads[x]);
-  }
-  if (q) {
-    swa_strides_t s;
-    int64_t n;
-    st = tensor_strides(q_out_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q_out", &s, &n);
-    if (st != SWA_OK) return st;
-    a.dst_r[0] = s.row;
-    a.dst_h[0] = s.head;
-    a.n_dst[0] = less_slack(n);
-  }
-  a.dst[0] = q_out;
-  a.dst[1] = k_pages;
-  a.dst[2] = v_pages;
-  a.dst_h[1] = a.pg.k_head;
-  a.dst_h[2] = a.pg.v_head;
-  a.n_dst[1] = a.pg.n_k;
-  a.n_dst[2] = a.pg.n_v;
-  a.S = static_cast<int32_t>(p->T_q);
-  a.n_pos = p->T_q;
-  a.positions = positions;
-  set_split(a, p->dtype, p->T_q);
-  a.err = static_cast<int32_t*>(workspace);
-  a.page_err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  a.clear_err = SWA_CHECKS ? 0 : 1;
-  if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
-  if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
-  const bool il = rope && rope->interleaved != 0;
-  if (plan.uniform > 0) {
-    PagedTable<kPagedSmallTable> tab{};
-    tab.count = 1;
-    tab.d[0].b = -1;
-    tab.d[0].q_len = static_cast<int32_t>(plan.uniform);
-    a.rows = p->T_q;
-    e = launch_append(a, tab, p->dtype, il, static_cast<int>(ceil_div(p->T_q, a.tok)), s);
-  } else {
-    auto take = [&](int b, PagedDesc& d, auto&) {
-      d.q_start = static_cast<int32_t>(plan.start[b]);
-      d.q_len = static_cast<int32_t>(plan.len[b]);
-      d.b = b;
-      return true;
-    };
-    auto go = [&](auto& tab) {
-      const PagedDesc& last = tab.d[tab.count - 1];
-      a.tok_begin = tab.d[0].q_start;
-      a.rows = last.q_start + last.q_len;
-      const int n = static_cast<int>(ceil_div(a.rows - a.tok_begin, a.tok));
-      const cudaError_t le = launch_append(a, tab, p->dtype, il, n, s);
-      a.clear_err = 0;
-      return le;
-    };
-    e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, go)
-                                                 : each_table<kPagedLargeTable>(plan, {}, take, go);
-  }
-  return e == cudaSuccess ? SWA_OK : cuda_fail(e, "append launch");
+    a.D = static_cast<int32_t>(p->D);
+    const void* src[3] = {q, k, v};
+    const swa_strides_t* ss[3] = {q_strides, k_strides, v_strides};
+    const int64_t heads[3] = {q ? p->N : 0, plan.N_kv, plan.N_kv};
+    const char* names[3] = {"q", "k", "v"};
+    for (int x = 0; x < 3; ++x) {
+      if (!src[x]) continue;
+      swa_strides_t s;
+      int64_t n;
+      st = tensor_strides(ss[x], SWA_LAYOUT_TND, 1, p->T_q, heads[x], p->D, false, names[x], &s, &n);
+      if (st != SWA_OK) return st;
+      a.src[x] = src[x];
+      a.src_r[x] = s.row;
+      a.src_h[x] = s.head;
+      a.n_src[x] = less_slack(n);
+      a.heads[x] = static_cast<int32_t>(heads[x]);
+    }
+    if (q) {
+      swa_strides_t s;
+      int64_t n;
+      st = tensor_strides(q_out_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q_out", &s, &n);
+      if (st != SWA_OK) return st;
+      a.dst_r[0] = s.row;
+      a.dst_h[0] = s.head;
+      a.n_dst[0] = less_slack(n);
+    }
+    a.dst[0] = q_out;
+    a.dst[1] = k_pages;
+    a.dst[2] = v_pages;
+    a.dst_h[1] = a.pg.k_head;
+    a.dst_h[2] = a.pg.v_head;
+    a.n_dst[1] = a.pg.n_k;
+    a.n_dst[2] = a.pg.n_v;
+    a.S = static_cast<int32_t>(p->T_q);
+    a.n_pos = p->T_q;
+    a.positions = positions;
+    set_split(a, p->dtype, p->T_q);
+    a.err = static_cast<int32_t*>(workspace);
+    a.page_err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    a.clear_err = SWA_CHECKS ? 0 : 1;
+    if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+    const bool il = rope && rope->interleaved != 0;
+    if (plan.uniform > 0) {
+      PagedTable<kPagedSmallTable> tab{};
+      tab.count = 1;
+      tab.d[0].b = -1;
+      tab.d[0].q_len = static_cast<int32_t>(plan.uniform);
+      a.rows = p->T_q;
+      e = launch_append(a, tab, p->dtype, il, static_cast<int>(ceil_div(p->T_q, a.tok)), s);
+    } else {
+      auto take = [&](int b, PagedDesc& d, auto&) {
+        d.q_start = static_cast<int32_t>(plan.start[b]);
+        d.q_len = static_cast<int32_t>(plan.len[b]);
+        d.b = b;
+        return true;
+      };
+      auto go = [&](auto& tab) {
+        const PagedDesc& last = tab.d[tab.count - 1];
+        a.tok_begin = tab.d[0].q_start;
+        a.rows = last.q_start + last.q_len;
+        const int n = static_cast<int>(ceil_div(a.rows - a.tok_begin, a.tok));
+        const cudaError_t le = launch_append(a, tab, p->dtype, il, n, s);
+        a.clear_err = 0;
+        return le;
+      };
+      e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, go)
+                                                   : each_table<kPagedLargeTable>(plan, {}, take, go);
+    }
+    return e == cudaSuccess ? SWA_OK : cuda_fail(e, "append launch");
+  });
 }
 
 swa_status_t swa_paged_forward_workspace_size(const swa_paged_params_t* p, size_t* bytes) {
-  if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
-  ForwardPlan f;
-  const swa_status_t st = forward_plan(p, f);
-  if (st != SWA_OK) return st;
-  *bytes = f.total;
-  return SWA_OK;
+  return guarded([&]() -> swa_status_t {
+    if (!bytes) return fail(SWA_ERR_PARAM_NULLPTR, "bytes is NULL");
+    ForwardPlan f;
+    const swa_status_t st = forward_plan(p, f);
+    if (st != SWA_OK) return st;
+    *bytes = f.total;
+    return SWA_OK;
+  });
 }
 
 swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const swa_strides_t* q_strides,
@@ -731,91 +756,97 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
                                const swa_page_strides_t* v_page_strides, const int32_t* block_table,
                                int64_t table_stride, const int32_t* kv_lens, void* out, float* softmax_max,
                                float* softmax_sum, void* workspace, size_t workspace_bytes, swa_stream_t stream) {
-  ForwardPlan f;
-  swa_status_t st = forward_plan(p, f);
-  if (st != SWA_OK) return st;
-  if ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(out, "out")) != SWA_OK) return st;
-  if ((reinterpret_cast<uintptr_t>(softmax_max) | reinterpret_cast<uintptr_t>(softmax_sum)) & 3u)
-    return fail(SWA_ERR_PARAM_INVALID, "softmax_max and softmax_sum must be 4-byte aligned");
-  PagedArgs a{};
-  st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.g);
-  if (st != SWA_OK) return st;
-  swa_strides_t qs;
-  // the row stride may not fold rows onto each other: tensor maps want it
-  st = tensor_strides(q_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q", &qs, &a.n_q);
-  if (st != SWA_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, f.total)) != SWA_OK) return st;
-  a.n_q = less_slack(a.n_q);
-  a.group = static_cast<int32_t>(p->N / f.seq.N_kv);
-  a.f16 = p->dtype == SWA_DTYPE_FP16 ? 1 : 0;
-  a.sparse_mode = p->sparse_mode;
-  const int64_t lim = int64_t(1) << 29;  // positions stay within +-2^28: no sum passes int32
-  a.pre = static_cast<int32_t>(std::min(std::max(p->pre_tokens, -lim), lim));
-  a.next = static_cast<int32_t>(std::min(std::max(p->next_tokens, -lim), lim));
-  a.scale_log2 = static_cast<float>(p->scale * kLog2e);
-  a.stall = debug_stall_bits();
-  a.q_row = qs.row;
-  a.q_head = qs.head;
-  a.q = q;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.out = out;
-  a.smax = softmax_max;
-  a.ssum = softmax_sum;
-  a.err = static_cast<int32_t*>(workspace);
-  a.clear_err = SWA_CHECKS ? 0 : 1;
-  a.n_out = less_slack(p->T_q * p->N * p->D);
-  a.n_stats = less_slack(p->T_q * p->N);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
-  if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
-  CUtensorMap mk{}, mv{};
-  if (f.tile.items > 0) {
-    const int64_t low = p->page_size & -p->page_size;
-    a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
-    st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
-                  a.box_rows, "k_pages");
-    if (st == SWA_OK)
-      st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
-                    a.box_rows, "v_pages");
+  return guarded([&]() -> swa_status_t {
+    ForwardPlan f;
+    swa_status_t st = forward_plan(p, f);
     if (st != SWA_OK) return st;
-  }
-  const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
-  auto run = [&](const Part& part, bool joins) {
-    if (part.items == 0 || e != cudaSuccess || (joins && (part.splits <= 1 || part.cluster))) return;
-    e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, joins, s)
-              : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, joins, s);
-    a.clear_err = 0;
-  };
-  // A batch of both kinds whose tables fit one launch each: the few-row kernel
-  // runs beside the other's last wave.  The joins come last: each waits for
-  // the grid before it, and that one for the tiles.
-  const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable;
-  a.signal = both ? 1 : 0;
-  run(f.tile, false);
-  a.overlap = both ? 1 : 0;
-  run(f.rows, false);
-  run(f.tile, true);
-  run(f.rows, true);
-  return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
+    if ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(out, "out")) != SWA_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(softmax_max) | reinterpret_cast<uintptr_t>(softmax_sum)) & 3u)
+      return fail(SWA_ERR_PARAM_INVALID, "softmax_max and softmax_sum must be 4-byte aligned");
+    PagedArgs a{};
+    st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.g);
+    if (st != SWA_OK) return st;
+    swa_strides_t qs;
+    // the row stride may not fold rows onto each other: tensor maps want it
+    st = tensor_strides(q_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q", &qs, &a.n_q);
+    if (st != SWA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, f.total)) != SWA_OK) return st;
+    a.n_q = less_slack(a.n_q);
+    a.group = static_cast<int32_t>(p->N / f.seq.N_kv);
+    a.f16 = p->dtype == SWA_DTYPE_FP16 ? 1 : 0;
+    a.sparse_mode = p->sparse_mode;
+    const int64_t lim = int64_t(1) << 29;  // positions stay within +-2^28: no sum passes int32
+    a.pre = static_cast<int32_t>(std::min(std::max(p->pre_tokens, -lim), lim));
+    a.next = static_cast<int32_t>(std::min(std::max(p->next_tokens, -lim), lim));
+    a.scale_log2 = static_cast<float>(p->scale * kLog2e);
+    a.stall = debug_stall_bits();
+    a.q_row = qs.row;
+    a.q_head = qs.head;
+    a.q = q;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.out = out;
+    a.smax = softmax_max;
+    a.ssum = softmax_sum;
+    a.err = static_cast<int32_t*>(workspace);
+    a.clear_err = SWA_CHECKS ? 0 : 1;
+    a.n_out = less_slack(p->T_q * p->N * p->D);
+    a.n_stats = less_slack(p->T_q * p->N);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    CUtensorMap mk{}, mv{};
+    if (f.tile.items > 0) {
+      const int64_t low = p->page_size & -p->page_size;
+      a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
+      st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
+                    a.box_rows, "k_pages");
+      if (st == SWA_OK)
+        st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
+                      a.box_rows, "v_pages");
+      if (st != SWA_OK) return st;
+    }
+    if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+    const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
+    auto run = [&](const Part& part, bool joins) {
+      if (part.items == 0 || e != cudaSuccess || (joins && (part.splits <= 1 || part.cluster))) return;
+      e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, joins, s)
+                : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, joins, s);
+      a.clear_err = 0;
+    };
+    // A batch of both kinds whose tables fit one launch each: the few-row kernel
+    // runs beside the other's last wave.  The joins come last: each waits for
+    // the grid before it, and that one for the tiles.
+    const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable;
+    a.signal = both ? 1 : 0;
+    run(f.tile, false);
+    a.overlap = both ? 1 : 0;
+    run(f.rows, false);
+    run(f.tile, true);
+    run(f.rows, true);
+    return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
+  });
 }
 
 swa_status_t swa_paged_append_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
-  PagedPlan plan;
-  swa_status_t st = paged_plan(p, plan);
-  if (st == SWA_OK) st = swa_workspace_status(workspace, stream);
-  return st == SWA_OK ? read_pages(p->T_q, workspace, kHeaderBytes) : st;
+  return guarded([&]() -> swa_status_t {
+    PagedPlan plan;
+    swa_status_t st = paged_plan(p, plan);
+    if (st == SWA_OK) st = swa_workspace_status(workspace, stream);
+    return st == SWA_OK ? read_pages(p->T_q, workspace, kHeaderBytes) : st;
+  });
 }
 
 swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* workspace, swa_stream_t stream) {
-  ForwardPlan f;
-  swa_status_t st = forward_plan(p, f);
-  if (st != SWA_OK) return st;
-  st = swa_workspace_status(workspace, stream);
-  for (const Part* part : {&f.rows, &f.tile})
-    if (st == SWA_OK) st = read_pages(part->items * part->splits, workspace, part->status_at);
-  return st;
+  return guarded([&]() -> swa_status_t {
+    ForwardPlan f;
+    swa_status_t st = forward_plan(p, f);
+    if (st != SWA_OK) return st;
+    st = swa_workspace_status(workspace, stream);
+    for (const Part* part : {&f.rows, &f.tile})
+      if (st == SWA_OK) st = read_pages(part->items * part->splits, workspace, part->status_at);
+    return st;
+  });
 }
 
 }  // extern "C"

@@ -74,6 +74,11 @@ CASES = {
     "d8": ([1, 140], [40, 140], 16, dict(N=2, N_kv=1, D=8, sparse_mode=4, next_tokens=0)),
     "mqa_48": ([3], [200], 16, dict(N=48, N_kv=1, D=64, sparse_mode=4, next_tokens=0)),
     "mqa_256": ([2], [150], 16, dict(N=256, N_kv=1, D=32, sparse_mode=4, next_tokens=0)),
+    "one_page": ([1], [10], 16, dict(N=1, D=64, extra_pages=0)),
+    "one_page_chunk": ([10], [14], 16, dict(N=4, N_kv=1, D=64, extra_pages=0, sparse_mode=4, next_tokens=0)),
+    "one_long_among_many": ([1] * 40, [20000] + [30] * 39, 64, dict(N=4, N_kv=4, D=16)),
+    "page_144": ([1, 150], [1000, 700], 144, dict(N=4, N_kv=2, D=64, sparse_mode=4, next_tokens=0,
+                                                  cache_layout="TND")),
     "chunk_split": ([160], [4000], 64, dict(N=2, N_kv=1, D=128, sparse_mode=4, next_tokens=0)),
 }
 

@@ -120,7 +120,8 @@ def paged(change=None, fields=None):
     (BAD, dict(fields=dict(dtype=7))), (BAD, dict(fields=dict(sparse_mode=2))),
     (BAD, dict(fields=dict(sparse_mode=4, pre_tokens=3, next_tokens=-4))),
     (OK, dict(fields=dict(sparse_mode=0, pre_tokens=3, next_tokens=-4))),
-    (BAD, dict(fields=dict(scale=float("nan")))), (BAD, dict(fields=dict(cache_layout=5))),
+    (BAD, dict(fields=dict(scale=float("nan")))), (BAD, dict(fields=dict(scale=1e39))),
+    (BAD, dict(fields=dict(cache_layout=5))),
     (BAD, dict(fields=dict(num_pages=0))), (BAD, dict(fields=dict(num_pages=1 << 31))),
     (BAD, dict(fields=dict(page_size=0))), (BAD, dict(fields=dict(page_size=1 << 17))),
     (UNSUP, dict(fields=dict(page_size=24))), (UNSUP, dict(fields=dict(page_size=8))),
@@ -161,6 +162,7 @@ def forward_status(lib, p=None, **args):
     (BAD, dict(out=FAKE + 1)), (BAD, dict(sm=FAKE + 2)), (BAD, dict(table=FAKE + 1)), (BAD, dict(lens=FAKE + 3)),
     (WS, dict(ws=None)), (WS, dict(ws=FAKE + 16)), (WS, dict(n=255)), (BAD, dict(ts=4)), (BAD, dict(ts=-5)),
     (BAD, dict(qs=S(0, 0, 64))), (BAD, dict(qs=S(0, 256, 60))), (BAD, dict(ks=PS(0, 64, 128))),
+    (UNSUP, dict(ks=PS(2048 + 8, 1024, 64))), (UNSUP, dict(vs=PS(4096, 512, 64))), 
     (BAD, dict(vs=PS(2048, 1024, 60))), (BAD, dict(ks=PS(2048, 8, 64))), (BAD, dict(ks=PS(1 << 39, 1024, 64))),
 ])
 def test_paged_forward_refusals(lib, want, case):
