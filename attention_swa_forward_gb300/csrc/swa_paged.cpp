@@ -11,7 +11,6 @@ using namespace swa;
 
 namespace {
 
-constexpr int64_t kSms = 152;  // SMs of the part this library is built for; sizes grids only
 constexpr int64_t kMaxKv = int64_t(1) << 28;
 constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is below 2^40 bytes
 // Keys one CTA of the few-row kernel takes at most, so that one long sequence
@@ -448,6 +447,30 @@ struct ForwardPlan {
 };
 bool few_rows(int64_t q_len, int64_t group) { return q_len * group <= kRowsTile; }
 
+// Tensor map of q: boxes of the tile's tokens x heads x 64 columns, heads
+// innermost, as the rows of a tile go.  *usable = 0 where the row stride is not
+// a multiple of the head stride past all heads (the kernel then gathers rows).
+swa_status_t query_map(CUtensorMap* m, int32_t* usable, const void* q, const swa_strides_t& s,
+                       const swa_paged_params_t* p, const Part& tile) {
+  const int64_t row = p->T_q > 1 ? s.row : p->N * p->D;
+  const int64_t head = p->N > 1 ? s.head : row;
+  *usable = row % head == 0 && row / head >= (p->N > 1 ? p->N : 1) ? 1 : 0;
+  if (!*usable) return SWA_OK;
+  auto fn = encode_fn();
+  if (!fn) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t d[3] = {static_cast<cuuint64_t>(p->D), static_cast<cuuint64_t>(p->N),
+                           static_cast<cuuint64_t>(p->T_q)};
+  const cuuint64_t st[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(row) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tile.gs), static_cast<cuuint32_t>(tile.tok)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(m, p->dtype == SWA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        3, const_cast<void*>(q), d, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed with %d", (int)r);
+  return SWA_OK;
+}
+
 swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   swa_status_t st = paged_plan(p, f.seq);
   if (st != SWA_OK) return st;
@@ -475,7 +498,7 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       // the items are as many.  Measured (64 items of 8192 keys): 49 us in 128
       // CTAs, 48 in 256, 60 in 320, which start a second wave; 8 items of
       // 131072 keys: 83 us in 152, 92 in 304.
-      part.par = std::min(ceil_div(kSms, items), steps);
+      part.par = std::min(ceil_div(int64_t(kSms), items), steps);
       part.cap = kRowsMostKeys / step + 2;
       part.least = 1;
       // Up to 8 splits are one cluster, which joins them without a second
@@ -515,7 +538,7 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
 
 template <int CAP>
 cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
-                     const CUtensorMap& mk, const CUtensorMap& mv, bool joins, cudaStream_t s) {
+                     const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, bool joins, cudaStream_t s) {
   const bool few = &part == &f.rows;
   a.gs = static_cast<int32_t>(part.gs);
   a.gs_magic = static_cast<uint32_t>(ceil_div(65536, part.gs));
@@ -535,7 +558,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     cudaError_t e = cudaSuccess;
     if (joins) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
     else if (few) e = launch_paged_rows(a, tab, s);
-    else e = launch_paged_tile(a, tab, mk, mv, s);
+    else e = launch_paged_tile(a, tab, mk, mv, mq, s);
     a.item_base += tab.n_items;
     a.clear_err = 0;
     return e;
@@ -794,7 +817,7 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     a.n_stats = less_slack(p->T_q * p->N);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    CUtensorMap mk{}, mv{};
+    CUtensorMap mk{}, mv{}, mq{};
     if (f.tile.items > 0) {
       const int64_t low = p->page_size & -p->page_size;
       a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
@@ -803,6 +826,7 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
       if (st == SWA_OK)
         st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
                       a.box_rows, "v_pages");
+      if (st == SWA_OK) st = query_map(&mq, &a.q_tma, q, qs, p, f.tile);
       if (st != SWA_OK) return st;
     }
     if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
@@ -810,8 +834,8 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
     auto run = [&](const Part& part, bool joins) {
       if (part.items == 0 || e != cudaSuccess || (joins && (part.splits <= 1 || part.cluster))) return;
-      e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, joins, s)
-                : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, joins, s);
+      e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, mq, joins, s)
+                : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, mq, joins, s);
       a.clear_err = 0;
     };
     // A batch of both kinds whose tables fit one launch each: the few-row kernel

@@ -108,6 +108,7 @@ struct PagedArgs {
   int32_t stall;      // test hook (kStallPaged)
   int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128
   PageDims kd, vd;
+  int32_t q_tma;      // tile kernel: Q comes through a tensor map
   int64_t q_row, q_head;
   const void* q;
   const void* k_pages;
@@ -143,20 +144,20 @@ SWA_PAGED_HD PagedItem resolve_paged(const PagedTable<CAP>& tab, int groups, int
   const PagedDesc& d = tab.d[lo];
   const int local = k - d.item_begin;
   PagedItem it;
-  // sequence, then head group, then tile: the CTAs in flight share a
-  // sequence's pages (its head groups) and a head group's keys (its tiles)
-  const int hg = local / d.tiles;
-  it.tile = d.tiles - 1 - (local - hg * d.tiles);  // the latest tokens, which see most, first
-  it.q_len = d.q_len;
+  // sequence, then tile (the latest tokens, which see most, first), then head
+  // group: items go by falling weight, and those in flight share pages
+  const int per = d.tiles * groups;
+  int x = local, seq = 0;
   if (d.b < 0) {
-    it.b = hg / groups;
-    it.vh = hg - it.b * groups;
-    it.q_start = it.b * d.q_len;
-  } else {
-    it.b = d.b;
-    it.vh = hg;
-    it.q_start = d.q_start;
+    seq = local / per;
+    x = local - seq * per;
   }
+  const int rank = x / groups;
+  it.vh = x - rank * groups;
+  it.tile = d.tiles - 1 - rank;
+  it.q_len = d.q_len;
+  it.b = d.b < 0 ? seq : d.b;
+  it.q_start = d.b < 0 ? seq * d.q_len : d.q_start;
   return it;
 }
 
@@ -187,6 +188,7 @@ SWA_PAGED_HD void paged_split(int steps, int par, int cap, int least, int s, int
   *end = *begin + per < steps ? *begin + per : steps;
 }
 
+constexpr int kSms = 152;         // SMs of the part this library is built for; sizes grids only
 constexpr int kRowsTile = 16;     // rows of a tile of the few-row kernel
 constexpr int kRowsStep = 64;     // keys per step of the few-row kernel (4 warps x 16)
 constexpr int kPagedTileRows = 128;  // rows of a tile of the tensor-memory kernel
@@ -196,7 +198,7 @@ template <int CAP>
 cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream);
 template <int CAP>
 cudaError_t launch_paged_tile(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk,
-                              const CUtensorMap& mv, cudaStream_t stream);
+                              const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t stream);
 // Join the splits' partial results; `step_keys` as of the kernel that wrote them.
 template <int CAP>
 cudaError_t launch_paged_join(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream);

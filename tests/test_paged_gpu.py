@@ -124,6 +124,11 @@ def test_strided_queries_and_pages():
                                 lens.to(DEV))
         for a, b in zip(ref, out):
             assert torch.equal(a, b)
+        # heads outermost
+        heads_first = q.transpose(0, 1).contiguous().to(DEV).transpose(0, 1)
+        out = run(geom, heads_first, kp, vp, table, lens)
+        for a, b in zip(ref, out):
+            assert torch.equal(a, b)
 
 
 def test_statistics_may_be_left_out():
