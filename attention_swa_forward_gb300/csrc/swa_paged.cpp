@@ -162,12 +162,15 @@ void set_split(RopeArgs& a, int dtype, int64_t rows) {
   a.tok_inner = a.src_r[x] < a.src_h[x] ? 1 : 0;
   // Tokens per CTA: the fewest token times over all rounds of resident CTAs,
   // a CTA costing about one token beside its own; a CTA's tokens stay within
-  // 80 KB.  32768 tokens of 40 heads in BNSD: 106 us with 8 (7 rounds), 112
-  // with 16, 116 with 4.
+  // 80 KB, or 112 KB for an append, whose start is longer (length, then block
+  // table).  32768 tokens of 40 heads in BNSD: 106 us with 8 (7 rounds), 112
+  // with 16, 116 with 4; an append of 6739 tokens of 48 heads of 96: 21.7 us
+  // with 9 (one round), 25.4 with 3; TND rotation 103 us under 80 KB, 106 above.
+  const int64_t most_bytes = (a.heads[2] ? 112 : 80) * 1024;
   const int64_t slots = kSms * (a.heads[2] ? kAppendResident : kRopeResident);
   const int64_t bytes = int64_t(a.H) * a.D * (dtype == SWA_DTYPE_FP32 ? 4 : 2);
   int64_t best = 0;
-  for (int tok = 1; tok <= (a.tok_inner ? 8 : kRopeMaxTok) && (tok == 1 || tok * bytes <= 80 * 1024);
+  for (int tok = 1; tok <= (a.tok_inner ? 8 : kRopeMaxTok) && (tok == 1 || tok * bytes <= most_bytes);
        tok += a.tok_inner ? tok : 1) {
     const int64_t cost = ceil_div(ceil_div(rows, tok), slots) * (tok + 1);
     if (best == 0 || cost < best) {
