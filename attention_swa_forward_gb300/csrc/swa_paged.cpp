@@ -347,7 +347,6 @@ swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, cons
   g.D = static_cast<int32_t>(p->D);
   g.page_size = static_cast<int32_t>(p->page_size);
   g.num_pages = static_cast<int32_t>(p->num_pages);
-  g.max_pages = static_cast<int32_t>(p->max_pages);
   g.kv_limit = static_cast<int32_t>(plan.max_kv);
   g.table_stride = table_stride;
   g.table = table;
@@ -842,7 +841,7 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
       a.clear_err = 0;
     };
     // A batch of both kinds whose tables fit one launch each: the few-row kernel
-    // runs beside the other's last wave.  The joins come last: each waits for
+    // takes the SMs that the other leaves.  The joins come last: each waits for
     // the grid before it, and that one for the tiles.
     const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable;
     a.signal = both ? 1 : 0;

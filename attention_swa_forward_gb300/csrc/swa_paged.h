@@ -12,9 +12,9 @@
 
 namespace swa {
 
-// Sequences of one launch, passed as a kernel parameter.  b < 0: one entry
-// stands for `tiles`-many equal sequences (b = q_start = 0, 1, ... times
-// q_len), which is what a decoding step of any batch size is.
+// Sequences of one launch, passed as a kernel parameter.  b < 0: the one entry
+// stands for all sequences, whose chunks have the same length q_len (sequence
+// b's starts at b * q_len), as in a decoding step of any batch size.
 struct PagedDesc {
   int32_t q_start, q_len, b;
   int32_t tiles;       // row tiles per head group (attention)
@@ -30,7 +30,7 @@ struct PagedTable {
 // The cache and the chunk as a kernel sees them.
 struct PagedGeom {
   int32_t N, N_kv, D;
-  int32_t page_size, num_pages, max_pages;
+  int32_t page_size, num_pages;
   int32_t kv_limit;  // largest valid kv_lens[b]
   int64_t table_stride;
   int64_t k_page, k_head, k_slot;  // strides in elements
@@ -121,7 +121,7 @@ struct PagedArgs {
   int32_t item_base;  // items of earlier launches of the call
   int32_t* err;
   int32_t clear_err;
-  int32_t signal;     // tile kernel: let the next grid start with the last wave
+  int32_t signal;     // tile kernel: let the next grid start on the SMs that it leaves
   int32_t overlap;    // few-row kernel: that next grid
   int32_t* page_err;  // per CTA of the call, [items][splits]
   int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build

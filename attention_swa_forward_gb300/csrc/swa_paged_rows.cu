@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Behind the tile kernel of the same call (overlap), whose CTAs signalled
   // after their own wait, every earlier grid has completed: this one may run
-  // beside that kernel's last wave, and its first CTA waits for it at the end.
+  // beside that kernel, and its first CTA waits for it at the end.
   if (!a.overlap) griddep_wait();
   griddep_launch_dependents();
   const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
@@ -478,10 +478,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 // Join the splits of a row tile: WPR warps per row over its splits (each reads
 // a partial row with one load per lane), then over their sums in shared
 // memory; one warp up to 8 splits, eight past that.  Reads the active partial
-// rows once; a few microseconds
-// behind the kernel that wrote them, launched so that its prologue overlaps
-// that tail.  (One warp per row took 30 us for the 152 splits of one
-// 131072-token sequence.)
+// rows once, a few microseconds behind the kernel that wrote them, launched so
+// that its prologue overlaps that tail.  (One warp per row took 30 us for the
+// 152 splits that one 131072-token sequence had.)
 constexpr int kJoinWarps = 8;
 template <int DP, bool F16, int WPR, int CAP>
 __global__ void __launch_bounds__(kJoinWarps * 32)
