@@ -79,6 +79,12 @@ CASES = {
     "one_long_among_many": ([1] * 40, [20000] + [30] * 39, 64, dict(N=4, N_kv=4, D=16)),
     "page_144": ([1, 150], [1000, 700], 144, dict(N=4, N_kv=2, D=64, sparse_mode=4, next_tokens=0,
                                                   cache_layout="TND")),
+    # more row tiles than SMs: a CTA walks several, some without keys
+    "many_tiles": ([200, 40, 0, 130, 300, 17], [200, 0, 5, 400, 310, 900], 48,
+                   dict(N=48, N_kv=48, D=64, sparse_mode=4, pre_tokens=150, next_tokens=0)),
+    "many_tiles_fp16": ([700, 33, 129], [700, 20, 600], 16,
+                        dict(N=40, N_kv=8, D=128, dtype="fp16", sparse_mode=4, next_tokens=0, cache_layout="TND")),
+    "many_tiles_equal": ([70] * 6, [70, 0, 300, 71, 129, 200], 32, dict(N=32, N_kv=32, D=40)),
     "chunk_split": ([160], [4000], 64, dict(N=2, N_kv=1, D=128, sparse_mode=4, next_tokens=0)),
 }
 

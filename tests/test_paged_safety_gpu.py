@@ -214,7 +214,8 @@ def test_a_page_shared_by_two_sequences():
         assert_within(x, r, b, "shared prefix")
 
 
-@pytest.mark.parametrize("name", ["token_long_split", "tokens_ragged", "chunk_split", "chunk_mixed"])
+@pytest.mark.parametrize("name", ["token_long_split", "tokens_ragged", "chunk_split", "chunk_mixed", "many_tiles",
+                                  "many_tiles_fp16"])
 def test_same_bits_from_run_to_run(name):
     geom, _, cache, q, _, _ = problem(name)
     first, _ = forward(geom, cache, q)
@@ -222,6 +223,21 @@ def test_same_bits_from_run_to_run(name):
         again, _ = forward(geom, cache, q)
         for a, b in zip(first, again):
             assert torch.equal(a, b)
+
+
+def test_a_bad_length_among_many_tiles_harms_no_other():
+    geom, kv_lens, cache, q, _, _ = problem("many_tiles")
+    good, _ = forward(geom, cache, q)
+    lens = cache[5].clone()
+    lens[3] = -1
+    got, ws = forward(geom, (*cache[:5], lens), q)
+    with pytest.raises(swa.SwaError) as e:
+        swa.check_paged_forward(geom, ws)
+    assert e.value.status == swa.SWA_ERR_PAGE
+    a, b = 240, 370  # the fourth sequence's rows
+    assert (got[0][a:b] == 0).all() and torch.isneginf(got[1][a:b]).all()
+    for x, y in zip(got, good):
+        assert torch.equal(x[:a], y[:a]) and torch.equal(x[b:], y[b:])
 
 
 @pytest.mark.parametrize("q_lens", [[1, 1], [150, 1]])
