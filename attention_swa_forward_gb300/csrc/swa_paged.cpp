@@ -20,7 +20,7 @@ constexpr int64_t kRowsMostKeys = 16384;
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
 constexpr double kLog2e = 1.4426950408889634;
-constexpr double kTwoPi = 6.283185307179586;
+constexpr double kTurnsPerRadian = 0.15915494309189535;
 
 template <typename... A>
 swa_status_t fail(swa_status_t st, const char* fmt, A... a) {
@@ -142,7 +142,7 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
     const int32_t ax = p->pair_axis ? p->pair_axis[i] : 0;
     if (ax < 0 || ax >= p->n_axes)
       return fail(SWA_ERR_PARAM_INVALID, "pair_axis[%lld] = %d is outside [0, n_axes)", (long long)i, ax);
-    const double turns = f / kTwoPi;
+    const double turns = f * kTurnsPerRadian;
     double frac = turns - std::floor(turns);
     if (frac >= 1.0) frac = 0.0;  // a tiny negative angle rounds up to a whole turn
     a.freq[i] = static_cast<uint64_t>(frac * 18446744073709551616.0);  // 2^64, exact

@@ -78,8 +78,8 @@ def test_far_positions_keep_their_accuracy():
     pos = pos.to(torch.int32)
     y, _ = swa.rope(geom, q.to(DEV), k.to(DEV), pos.to(DEV))
     ref, err = rope_ref(geom, q, pos)
-    # angles up to 2^31 radians: inv_freq (a unit in the last place), 2 pi, their
-    # quotient and the reference's own product each round by 2^-53, the first
+    # angles up to 2^31 radians: inv_freq (a unit in the last place), 1 / (2 pi), their
+    # product and the reference's own product each round by 2^-53, the first
     # by twice that: 6 * 2^-53 * 2^31 radians on |a| + |b|
     slack = 6 * 2.0 ** -22 * 2 * q.abs().amax().double()
     assert_within(y, ref, err + slack, "far")
