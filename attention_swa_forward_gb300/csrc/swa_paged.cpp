@@ -19,6 +19,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is b
 constexpr int64_t kRowsMostKeys = 16384;
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
+constexpr int64_t kTailSteps = 12;  // key tiles that splitting a last round must save (0.76 us each)
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kTurnsPerRadian = 0.15915494309189535;
 
@@ -437,8 +438,10 @@ size_t append_bytes(const swa_paged_params_t* p) { return kHeaderBytes + round25
 struct Part {
   int64_t gs = 1, tok = 1, rows = 0;  // heads and tokens of a tile, rows of a partial
   int64_t items = 0, splits = 1, par = 1, cap = 1, least = 1, step = 1;
+  int64_t whole = 0;  // items that are one unit each (tiles); the others are split
   bool cluster = false;
   size_t status_at = 0, ml_at = 0, o_at = 0;  // workspace offsets
+  int64_t units() const { return whole + (items - whole) * splits; }
 };
 struct ForwardPlan {
   PagedPlan seq;
@@ -516,17 +519,36 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
         part.cluster = true;
       }
     } else {
-      // A CTA costs ~7 us beside its steps of 0.78 us, and a split writes and
-      // reads 64 KB more: only where SMs would stay empty
+      // A split writes and reads 64 KB and needs the join (a few us): only
+      // where SMs would stay empty.  That is all items when they are fewer than
+      // half the SMs, and the items of a last round that fills less than half
+      // of them, if they are long: a tile of the longest sequence has the
+      // cache behind the chunk to itself, as far as the window reaches.
+      // Measured with the last round split and whole (32 / 8 heads): 2048
+      // tokens (512 items) under a window of 4096 116.5 and 122.7 us, 640
+      // tokens (160 items) 55.5 and 65.5, under a window of 8192 85 and 115.
       part.least = 4;
-      part.par = items > kSms / 2 ? 1 : std::min(kSms / items, ceil_div(steps, part.least));
       part.cap = steps;
+      int64_t longest = 0;
+      for (int64_t n : f.seq.len) longest = std::max(longest, few_rows(n, G) ? 0 : n);
+      const int64_t sure = std::min(keys, std::max<int64_t>(f.seq.max_kv - longest, 0)) / step;
+      const int64_t last = part.items % kSms;
+      const bool one_launch = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedLargeTable;
+      if (part.items <= kSms / 2) {
+        part.par = std::min(kSms / items, ceil_div(steps, part.least));
+      } else if (one_launch && part.items > kSms && last > 0 && last <= kSms / 2) {
+        const int64_t ways = std::min(kSms / last, ceil_div(sure, 2 * part.least));
+        if (ways > 1 && sure - ceil_div(sure, ways) >= kTailSteps) {
+          part.par = ways;
+          part.whole = part.items - last;
+        }
+      }
     }
     part.splits = std::max(part.par, ceil_div(steps, part.cap));
     part.status_at = f.total;
-    f.total += round256(part.items * part.splits * 4);
+    f.total += round256(part.units() * 4);
     if (part.splits > 1 && !part.cluster) {
-      const size_t rows = static_cast<size_t>(part.items) * part.splits * part.rows;
+      const size_t rows = static_cast<size_t>(part.items - part.whole) * part.splits * part.rows;
       part.ml_at = f.total;
       part.o_at = part.ml_at + round256(rows * 8);
       f.total = part.o_at + round256(rows * DP * 4);
@@ -546,6 +568,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   a.gs_magic = static_cast<uint32_t>(ceil_div(65536, part.gs));
   a.tok = static_cast<int32_t>(part.tok);
   a.groups = static_cast<int32_t>(p->N / part.gs);
+  a.whole = static_cast<int32_t>(part.whole);
   a.splits = static_cast<int32_t>(part.splits);
   a.par = static_cast<int32_t>(part.par);
   a.cap = static_cast<int32_t>(part.cap);
@@ -870,7 +893,7 @@ swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* w
     if (st != SWA_OK) return st;
     st = swa_workspace_status(workspace, stream);
     for (const Part* part : {&f.rows, &f.tile})
-      if (st == SWA_OK) st = read_pages(part->items * part->splits, workspace, part->status_at);
+      if (st == SWA_OK) st = read_pages(part->units(), workspace, part->status_at);
     return st;
   });
 }

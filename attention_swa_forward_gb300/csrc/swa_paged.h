@@ -101,7 +101,8 @@ struct PagedArgs {
   int32_t sparse_mode;
   int32_t pre, next;  // clamped so that position sums stay inside int32
   float scale_log2;
-  int32_t splits;     // CTAs per item along the keys, at most
+  int32_t whole;      // tile kernel: the first items of the launch, one unit each; the others are split
+  int32_t splits;     // CTAs (units) per split item along the keys, at most
   int32_t par, cap, least;  // paged_split
   int32_t cluster;    // few-row kernel: the splits are a cluster, which joins them itself
   int32_t rows_pad;   // rows of a partial tile
@@ -116,14 +117,14 @@ struct PagedArgs {
   void* out;
   float* smax;        // may be NULL
   float* ssum;        // may be NULL
-  float* part_o;      // [items][splits][rows_pad][DP] (splits > 1)
-  float2* part_ml;    // [items][splits][rows_pad]: maximum (log2 units), sum
-  int32_t item_base;  // items of earlier launches of the call
+  float* part_o;      // [items - whole][splits][rows_pad][DP] (splits > 1)
+  float2* part_ml;    // [items - whole][splits][rows_pad]: maximum (log2 units), sum
+  int32_t item_base;  // items of earlier launches of the call (0 where whole > 0)
   int32_t* err;
   int32_t clear_err;
   int32_t signal;     // tile kernel: let the next grid start on the SMs that it leaves
   int32_t overlap;    // few-row kernel: that next grid
-  int32_t* page_err;  // per CTA of the call, [items][splits]
+  int32_t* page_err;  // per unit of the call: [whole], then [items - whole][splits]
   int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build
 };
 

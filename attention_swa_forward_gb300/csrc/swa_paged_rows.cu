@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __shared__ float s_acc[WPR][DP], s_l[WPR], s_m[WPR];
   const PagedGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
+  const PagedItem w = resolve_paged(tab, a.groups, a.whole + static_cast<int>(blockIdx.x));
   const int r = blockIdx.y * (kJoinWarps / WPR) + warp / WPR, part = warp % WPR;
   const int tok0 = w.tile * a.tok;
   const int n_tok = min(a.tok, w.q_len - tok0);
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (r >= n_tok * a.gs) return;  // (with WPR > 1 a CTA is one row: all of it returns)
   static_assert(WPR == 1 || WPR == kJoinWarps, "a CTA is one row or one row per warp");
   if (active <= 1) return;  // written by the CTA that had the keys
-  const int64_t item = a.item_base + static_cast<int64_t>(blockIdx.x);
+  const int64_t item = a.item_base + static_cast<int64_t>(blockIdx.x);  // among the split ones
   const int64_t p0 = item * a.splits * a.rows_pad + r;
   // each warp: its splits' maximum, then their sum relative to it
   float M = -INFINITY;
@@ -612,9 +612,9 @@ template <int DP, bool F16, int CAP>
 cudaError_t launch_join_t(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream) {
   const int rows = a.tok * a.gs;
   if (a.splits <= 8)
-    return launch_pdl(swa_paged_join_kernel<DP, F16, 1, CAP>, dim3(tab.n_items, (rows + kJoinWarps - 1) / kJoinWarps),
+    return launch_pdl(swa_paged_join_kernel<DP, F16, 1, CAP>, dim3(tab.n_items - a.whole, (rows + kJoinWarps - 1) / kJoinWarps),
                       dim3(kJoinWarps * 32), 0, stream, a, tab, step_keys);
-  return launch_pdl(swa_paged_join_kernel<DP, F16, kJoinWarps, CAP>, dim3(tab.n_items, rows), dim3(kJoinWarps * 32), 0,
+  return launch_pdl(swa_paged_join_kernel<DP, F16, kJoinWarps, CAP>, dim3(tab.n_items - a.whole, rows), dim3(kJoinWarps * 32), 0,
                     stream, a, tab, step_keys);
 }
 

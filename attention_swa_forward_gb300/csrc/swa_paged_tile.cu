@@ -17,8 +17,9 @@
 //    from one to the next: the lengths, block table entries, K, V and Q of the
 //    next tile arrive while this one is computed.  (One CTA per row tile paid
 //    about 7 us each for its start and end: prompt of 8192 tokens 430 us, now
-//    390; 2048 tokens under a 4096 window 128, now 123; 8192 under it 349, now
-//    315.)  Tiles go by falling weight, in rounds of alternating direction.
+//    390; 2048 tokens under a 4096 window 128, now 123, and 117 with the last
+//    round's tiles split; 8192 under it 349, now 315.)  Tiles go by falling
+//    weight, in rounds of alternating direction.
 //    At a boundary the softmax warps still wait for the last product and store
 //    their rows (~5000 cycles).  Handing the stores to four more warps needed
 //    setmaxnreg and waits without calls, and gained nothing (392 us);
@@ -145,10 +146,14 @@ struct UnitWalk {
   int k, u_next, kv_next;
   PagedItem w_next;
 
+  // The first `whole` units are whole items, the others splits of the rest.
+  static __device__ __forceinline__ int item_of(const PagedArgs& a, int u) {
+    return u < a.whole ? u : (a.splits > 1 ? a.whole + (u - a.whole) / a.splits : u);
+  }
   __device__ __forceinline__ void fetch(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units) {
     u_next = unit_index(k, n_units);
     if (u_next < 0) return;
-    w_next = resolve_paged(tab, a.groups, a.splits > 1 ? u_next / a.splits : u_next);
+    w_next = resolve_paged(tab, a.groups, item_of(a, u_next));
     kv_next = in_bounds(w_next.b, 1, a.g.n_lens, a.err) ? a.g.kv_lens[w_next.b] : 0;
   }
   __device__ __forceinline__ void start(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units) {
@@ -157,10 +162,10 @@ struct UnitWalk {
   }
   __device__ __forceinline__ bool next(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units, Unit& x) {
     if (u_next < 0) return false;
-    const int item = a.splits > 1 ? u_next / a.splits : u_next;
+    const bool whole = u_next < a.whole;
     x.w = w_next;
-    x.split = u_next - item * a.splits;
-    x.slot_id = (a.item_base + static_cast<int64_t>(item)) * a.splits + x.split;
+    x.split = whole ? 0 : (u_next - a.whole) - (item_of(a, u_next) - a.whole) * a.splits;
+    x.slot_id = static_cast<int64_t>(a.item_base) * a.splits + u_next;
     const int raw = kv_next;
     ++k;
     fetch(a, tab, n_units);
@@ -173,7 +178,13 @@ struct UnitWalk {
     const int t_first = x.lo >> 7;
     const int steps = x.lo <= x.hi ? (x.hi >> 7) - t_first + 1 : 0;
     int st0, st1, active;
-    paged_split(steps, a.par, a.cap, a.least, x.split, &st0, &st1, &active);
+    if (whole) {
+      st0 = 0;
+      st1 = steps;
+      active = 1;
+    } else {
+      paged_split(steps, a.par, a.cap, a.least, x.split, &st0, &st1, &active);
+    }
     x.direct = active <= 1;
     x.idle = x.split > 0 && x.split >= active;
     x.kv_t0 = t_first + st0;
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.signal) griddep_launch_dependents();
   if (a.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
   const PagedGeom& g = a.g;
-  const int n_units = tab.n_items * a.splits;
+  const int n_units = a.whole + (tab.n_items - a.whole) * a.splits;
   UnitWalk<CAP> walk;
   walk.start(a, tab, n_units);
   Unit x;
@@ -616,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mul = !x.direct ? f : (l > 0.f || l != l ? 1.f / l : 0.f);
       const int h = x.w.vh * a.gs + (r - i * a.gs);
       const int64_t row = static_cast<int64_t>(x.w.q_start + x.tok0 + i) * g.N + h;
-      const int64_t pr = x.slot_id * a.rows_pad + r;
+      const int64_t pr = (x.slot_id - a.whole) * a.rows_pad + r;
 #pragma unroll
       for (int ch = 0; ch < D / 32; ++ch) {
         if (ch * 32 >= g.D) break;
@@ -657,7 +668,7 @@ cudaError_t launch_tile_t(const PagedArgs& a, const PagedTable<CAP>& tab, const 
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = set_smem_limit(swa_paged_tile_kernel<D, F16, CAP>, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int units = tab.n_items * a.splits;
+  const int units = a.whole + (tab.n_items - a.whole) * a.splits;
   return launch_pdl(swa_paged_tile_kernel<D, F16, CAP>, dim3(units < kSms ? units : kSms), dim3(kThreads), smem, stream,
                     a, tab, mk, mv, mq);
 }

@@ -86,6 +86,12 @@ CASES = {
                         dict(N=40, N_kv=8, D=128, dtype="fp16", sparse_mode=4, next_tokens=0, cache_layout="TND")),
     "many_tiles_equal": ([70] * 6, [70, 0, 300, 71, 129, 200], 32, dict(N=32, N_kv=32, D=40)),
     "chunk_split": ([160], [4000], 64, dict(N=2, N_kv=1, D=128, sparse_mode=4, next_tokens=0)),
+    # a last round of few row tiles, which are split over their keys
+    "last_round_split": ([1300], [4700], 48, dict(N=16, N_kv=1, D=32, sparse_mode=4, next_tokens=0)),
+    "last_round_split_ragged": ([33, 1, 1200, 60, 0], [40, 900, 5000, 3, 0], 32,
+                                dict(N=16, N_kv=2, D=40, dtype="fp16", sparse_mode=4, pre_tokens=3500, next_tokens=0,
+                                     cache_layout="TND")),
+    "last_round_split_equal": ([200] * 4, [3200, 190, 2500, 2300], 16, dict(N=40, N_kv=40, D=16)),
 }
 
 
