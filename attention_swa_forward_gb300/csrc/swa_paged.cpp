@@ -96,6 +96,26 @@ swa_status_t tensor_strides(const swa_strides_t* given, int32_t layout, int64_t 
   return SWA_OK;
 }
 
+// The rows of a result must not overlap: in ascending order, each stride is past
+// all that the smaller ones span.
+swa_status_t check_apart(const swa_strides_t& s, int32_t layout, int64_t B, int64_t S, int64_t N, int64_t D,
+                         const char* name) {
+  const bool tnd = layout == SWA_LAYOUT_TND;
+  struct Dim {
+    int64_t n, stride;
+  } d[3] = {{tnd ? 1 : B, s.batch}, {tnd ? B * S : S, s.row}, {N, s.head}};
+  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t span = D;
+  for (const Dim& x : d) {
+    if (x.n <= 1) continue;
+    if (x.stride < span)
+      return fail(SWA_ERR_PARAM_INVALID, "%s: stride %lld overlaps rows, which span %lld elements", name,
+                  (long long)x.stride, (long long)span);
+    span += (x.n - 1) * x.stride;
+  }
+  return SWA_OK;
+}
+
 // No C++ exception leaves a C entry point.
 template <typename F>
 swa_status_t guarded(F&& body) noexcept {
@@ -214,6 +234,7 @@ swa_status_t rope_call(const swa_rope_params_t* p, const void* q, const swa_stri
     a.src_h[x] = s.head;
     a.n_src[x] = less_slack(n);
     st = tensor_strides(ds[x], p->layout, p->B, p->S, heads[x], p->D, true, names[2 + x], &s, &n);
+    if (st == SWA_OK) st = check_apart(s, p->layout, p->B, p->S, heads[x], p->D, names[2 + x]);
     if (st != SWA_OK) return st;
     a.dst[x] = dst[x];
     a.dst_b[x] = s.batch;
@@ -734,6 +755,7 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
       swa_strides_t s;
       int64_t n;
       st = tensor_strides(q_out_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q_out", &s, &n);
+      if (st == SWA_OK) st = check_apart(s, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, "q_out");
       if (st != SWA_OK) return st;
       a.dst_r[0] = s.row;
       a.dst_h[0] = s.head;

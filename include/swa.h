@@ -282,7 +282,9 @@ SWA_API swa_status_t swa_dropout_mask(const swa_params_t *p, uint8_t *mask, size
  * elements, between batches, rows (tokens) and heads; a NULL stands for the
  * dense layout.  The D elements of a head row are contiguous; tensors start
  * on 16 bytes and strides are multiples of 8 elements (q and k may so be
- * slices of one fused projection). */
+ * slices of one fused projection).  Inputs may repeat rows (stride 0); the
+ * strides of a result, in ascending order, are each past all that the smaller
+ * ones span. */
 typedef struct {
   int64_t batch, row, head; /* elements; batch is unused for TND */
 } swa_strides_t;

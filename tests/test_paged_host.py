@@ -82,6 +82,9 @@ S = swa.SwaStrides
     (BAD, dict(change=dict(inv_freq=[float("nan")] * 32))), (BAD, dict(change=dict(inv_freq=[2.0 ** 21] * 32))),
     (BAD, dict(qs=S(0, 257, 64))), (BAD, dict(ks=S(0, -128, 64))), (BAD, dict(qos=S(0, 0, 64))),
     (BAD, dict(kos=S(0, 128, 8))), (BAD, dict(qs=S(0, 1 << 39, 64))),
+    # rows of a result that overlap
+    (BAD, dict(qos=S(0, 64, 64))), (BAD, dict(qos=S(0, 248, 64))), (BAD, dict(kos=S(0, 64, 1016))),
+    (BAD, dict(change=dict(layout="BNSD", B=2, S=8), qos=S(2040, 64, 512))),
 ])
 @pytest.mark.parametrize("backward", [False, True])
 def test_rope_refusals(lib, want, case, backward):
@@ -191,6 +194,7 @@ def append_status(lib, p=None, rope=None, **args):
     (BAD, dict(rope=dict(S=8))), (BAD, dict(rope=dict(N=8))), (BAD, dict(rope=dict(N_kv=4))), (BAD, dict(rope=dict(D=72))),
     (BAD, dict(rope=dict(dtype="fp16"))), (BAD, dict(rope=dict(layout="BNSD"))),
     (BAD, dict(ks=S(0, 100, 64))), (BAD, dict(rope={}, q=FAKE, qo=FAKE, qos=S(0, 0, 64))),
+    (BAD, dict(rope={}, q=FAKE, qo=FAKE, qos=S(0, 192, 64))),
     (BAD, dict(kps=PS(2048, 0, 64))), (BAD, dict(ts=3)),
 ])
 def test_paged_append_refusals(lib, want, case):
