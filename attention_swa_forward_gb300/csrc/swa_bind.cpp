@@ -117,11 +117,19 @@ const int32_t* block_table(const at::Tensor& t, const swa_paged_params_t& p, int
   return static_cast<const int32_t*>(t.data_ptr());
 }
 
-const int32_t* positions(const at::Tensor& t, int64_t numel, int device) {
-  if (t.scalar_type() != at::kInt || !t.is_cuda() || t.get_device() != device || t.numel() != numel ||
-      !t.is_contiguous())
-    refuse(t, "positions", {numel}, at::kInt, device, " (contiguous)");
+// [n_axes, rows], the rows in any shape; one axis may leave its dimension out.
+const int32_t* positions(const at::Tensor& t, int64_t n_axes, int64_t rows, int device) {
+  if (t.scalar_type() != at::kInt || !t.is_cuda() || t.get_device() != device || t.numel() != n_axes * rows ||
+      (n_axes > 1 && (t.dim() < 2 || t.size(0) != n_axes)) || !t.is_contiguous())
+    refuse(t, "positions", {n_axes, rows}, at::kInt, device, " (contiguous)");
   return static_cast<const int32_t*>(t.data_ptr());
+}
+
+const at::Tensor& workspace(PyObject* o, int device) {
+  const at::Tensor& t = tensor(o, "workspace");
+  if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous())
+    throw Refused("workspace must be contiguous and on the device of the tensors");
+  return t;
 }
 
 int device_of(const at::Tensor& t) {
@@ -192,7 +200,7 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x[i] = arg(*t[i], names[i], shape, type, dev);
       }
     }
-    const int32_t* pos = positions(tensor(a[4], "positions"), p.n_axes * p.B * p.S, dev);
+    const int32_t* pos = positions(tensor(a[4], "positions"), p.n_axes, p.B * p.S, dev);
     const On on(dev, a[7]);
     return fn(&p, x[0].ptr, x[0].strides(), x[1].ptr, x[1].strides(), pos, x[2].ptr, x[2].strides(), x[3].ptr,
               x[3].strides(), on.stream);
@@ -220,12 +228,11 @@ PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *pos = tensor_or_none(a[9], "positions"), *q = tensor_or_none(a[10], "q");
     const at::Tensor* qo = tensor_or_none(a[11], "q_out");
     if (pos && !rope) throw Refused("positions are taken with rope only");
-    const int32_t* pp = pos ? positions(*pos, rope->n_axes * rope->B * rope->S, dev) : nullptr;
+    const int32_t* pp = pos ? positions(*pos, rope->n_axes, rope->B * rope->S, dev) : nullptr;
     Arg xq, xo;
     if (q) xq = arg(*q, "q", qs, type, dev);
     if (qo) xo = arg(*qo, "q_out", qs, type, dev);
-    const at::Tensor& ws = tensor(a[12], "workspace");
-    if (device_of(ws) != dev) throw Refused("workspace is on another device");
+    const at::Tensor& ws = workspace(a[12], dev);
     const On on(dev, a[13]);
     return fn(&p, xk.ptr, xk.strides(), xv.ptr, xv.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
               static_cast<const int32_t*>(l.data_ptr()), rope, pp, xq.ptr, xq.strides(), xo.ptr, xo.strides(),
@@ -253,8 +260,7 @@ PyObject* bind_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect_dense(out, "out", qs, type, dev);
     expect_dense(sm, "softmax_max", stats, at::kFloat, dev);
     expect_dense(ss, "softmax_sum", stats, at::kFloat, dev);
-    const at::Tensor& ws = tensor(a[10], "workspace");
-    if (device_of(ws) != dev) throw Refused("workspace is on another device");
+    const at::Tensor& ws = workspace(a[10], dev);
     const On on(dev, a[11]);
     return fn(&p, xq.ptr, xq.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
               static_cast<const int32_t*>(l.data_ptr()), out.data_ptr(), static_cast<float*>(sm.data_ptr()),

@@ -158,6 +158,20 @@ def test_statistics_may_be_left_out():
     assert torch.equal(out, ref)
 
 
+def test_a_workspace_in_pieces_is_refused():
+    """Its bytes must lie behind one another."""
+    geom = geometry([1, 40], [5, 60], 16, N=2, N_kv=1, D=64)
+    _, _, kp, vp, table, lens = (x.to(DEV) if torch.is_tensor(x) else x for x in draw_cache(geom, [5, 60], 3))
+    q = torch.zeros(geom.T_q, 2, 64, dtype=torch.bfloat16, device=DEV)
+    need = swa.swa_paged_forward_workspace_size(swa.PagedParams(geom))
+    whole = torch.empty(2 * need, dtype=torch.uint8, device=DEV)
+    for ws in (whole[::2], whole[:1].expand(need), whole[:need].cpu()):
+        with pytest.raises(ValueError):
+            swa.paged_forward(geom, q, kp, vp, table, lens, workspace=ws)
+        with pytest.raises(ValueError):
+            swa.paged_append(geom, q[:, :1], q[:, :1], kp, vp, table, lens, workspace=ws)
+
+
 def test_rows_behind_the_outputs_are_left_alone():
     geom = geometry([1, 0, 130], [40, 0, 200], 16, N=4, N_kv=2, D=64, sparse_mode=4, next_tokens=0)
     _, _, kp, vp, table, lens = draw_cache(geom, [40, 0, 200], 2)

@@ -151,3 +151,16 @@ def test_captured_rotation_replays():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(yq, want[0]) and torch.equal(yk, want[1])
+
+
+def test_positions_of_another_shape_are_refused():
+    """[rows, n_axes] holds as many numbers as [n_axes, rows]."""
+    geom = RopeGeometry("TND", 1, 12, 2, 64, sections=[16, 16])
+    q, k, pos = (t.to(DEV) for t in draw(geom, 2))
+    for bad in (pos.T.contiguous(), pos.flatten(), pos.T):
+        with pytest.raises(ValueError):
+            swa.rope(geom, q, k, bad)
+    one = RopeGeometry("TND", 1, 12, 2, 64)
+    a = swa.rope(one, q, k, pos[0])
+    b = swa.rope(one, q, k, pos[:1])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
