@@ -215,7 +215,7 @@ def test_a_page_shared_by_two_sequences():
 
 
 @pytest.mark.parametrize("name", ["token_long_split", "tokens_ragged", "chunk_split", "chunk_mixed", "many_tiles",
-                                  "many_tiles_fp16"])
+                                  "many_tiles_fp16", "last_round_split_ragged"])
 def test_same_bits_from_run_to_run(name):
     geom, _, cache, q, _, _ = problem(name)
     first, _ = forward(geom, cache, q)
