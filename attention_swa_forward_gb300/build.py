@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -74,15 +75,38 @@ def build_bind(verbose: bool = False) -> str:
     return BIND_PATH
 
 
+def _bind_failure(verbose: bool):
+    """Build the extension; the exception where that fails, None where it does not."""
+    try:
+        build_bind(verbose)
+    except Exception as e:
+        return e
+    return None
+
+
+def _report(failure) -> None:
+    if failure is None:
+        return
+    if is_stale(BIND_PATH) and os.path.exists(BIND_PATH):
+        os.remove(BIND_PATH)  # its structs may not be the library's
+    warnings.warn(f"the Python calls of the rotary and paged operators are not available: {failure}", RuntimeWarning,
+                  stacklevel=3)
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """Compile every translation unit for sm_103a and link libswa.so (or,
-    with `checked`, the bounds-checked libswa_checked.so); returns its path."""
+    with `checked`, the bounds-checked libswa_checked.so); returns its path.
+
+    The library needs nvcc alone.  The CPython extension is built beside it and
+    needs PyTorch's C++ headers: where that fails the library is complete, a
+    RuntimeWarning says why, and the calls that go through the extension raise
+    ImportError."""
     lib_path = CHECKED_LIB_PATH if checked else LIB_PATH
     build_dir = CHECKED_BUILD_DIR if checked else BUILD_DIR
     bind = force or is_stale(BIND_PATH)
     if not force and not is_stale(lib_path):
         if bind:
-            build_bind(verbose)
+            _report(_bind_failure(verbose))
         return lib_path
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
@@ -99,16 +123,16 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        pending = ex.submit(build_bind, verbose) if bind else None
+        pending = ex.submit(_bind_failure, verbose) if bind else None
         objs = list(ex.map(compile_one, SOURCES))
-        if pending is not None:
-            pending.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if pending is not None:
+        _report(pending.result())
     return lib_path
 
 
