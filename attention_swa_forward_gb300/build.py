@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,7 +24,6 @@ CHECKED_BUILD_DIR = os.path.join(PKG, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libswa_checked.so")
 # the CPython extension that calls the rotary and paged-cache entry points on torch tensors
 BIND_SOURCE = "swa_bind.cpp"
-BIND_PATH = os.path.join(PKG, "_swa_bind.so")
 SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_pair.cu", "swa_bwd_dkv.cu", "swa_bwd_dq.cu", "swa_aux.cu",
            "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged_tile.cu", "swa_paged.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -50,16 +50,29 @@ def is_stale(lib_path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def bind_path() -> str:
+    """Where the CPython extension of the installed torch and the running Python
+    is: it is linked against the C++ ABI of both, so after an upgrade of either it
+    counts as not built."""
+    try:
+        import torch
+
+        version = torch.__version__
+    except ImportError:
+        version = "none"
+    return os.path.join(PKG, f"_swa_bind.torch-{version}{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
+
+
 def build_bind(verbose: bool = False) -> str:
     """Compile the CPython extension against the installed torch; returns its path."""
-    import sysconfig
-
     import torch
+
+    path = bind_path()
 
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
@@ -71,8 +84,8 @@ def build_bind(verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND_PATH)
-    return BIND_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def _bind_failure(verbose: bool):
@@ -87,8 +100,9 @@ def _bind_failure(verbose: bool):
 def _report(failure) -> None:
     if failure is None:
         return
-    if is_stale(BIND_PATH) and os.path.exists(BIND_PATH):
-        os.remove(BIND_PATH)  # its structs may not be the library's
+    path = bind_path()
+    if is_stale(path) and os.path.exists(path):
+        os.remove(path)  # its structs may not be the library's
     warnings.warn(f"the Python calls of the rotary and paged operators are not available: {failure}", RuntimeWarning,
                   stacklevel=3)
 
@@ -103,7 +117,7 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     ImportError."""
     lib_path = CHECKED_LIB_PATH if checked else LIB_PATH
     build_dir = CHECKED_BUILD_DIR if checked else BUILD_DIR
-    bind = force or is_stale(BIND_PATH)
+    bind = force or is_stale(bind_path())
     if not force and not is_stale(lib_path):
         if bind:
             _report(_bind_failure(verbose))

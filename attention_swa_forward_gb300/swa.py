@@ -17,7 +17,6 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libswa.so")
 CHECKED_LIB_PATH = os.path.join(_PKG, "libswa_checked.so")
-BIND_PATH = os.path.join(_PKG, "_swa_bind.so")
 
 SWA_OK = 0
 SWA_ERR_PARAM_NULLPTR = 161001
@@ -566,9 +565,12 @@ def _bind():
 
 def _load_bind():
     global _bind_module
-    if not os.path.exists(BIND_PATH):
-        raise ImportError(f"{BIND_PATH} is missing: build it with attention_swa_forward_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("_swa_bind", BIND_PATH)
+    from .build import bind_path
+
+    path = bind_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with attention_swa_forward_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_swa_bind", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     _bind_module = module
