@@ -6,6 +6,7 @@
 #include <memory>
 
 #include "swa_paged.h"
+#include "swa_turn.h"
 
 using namespace swa;
 
@@ -21,7 +22,6 @@ constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
 constexpr int64_t kTailSteps = 12;  // key tiles that splitting a last round must save (0.76 us each)
 constexpr double kLog2e = 1.4426950408889634;
-constexpr double kTurnsPerRadian = 0.15915494309189535;
 
 template <typename... A>
 swa_status_t fail(swa_status_t st, const char* fmt, A... a) {
@@ -163,10 +163,7 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
     const int32_t ax = p->pair_axis ? p->pair_axis[i] : 0;
     if (ax < 0 || ax >= p->n_axes)
       return fail(SWA_ERR_PARAM_INVALID, "pair_axis[%lld] = %d is outside [0, n_axes)", (long long)i, ax);
-    const double turns = f * kTurnsPerRadian;
-    double frac = turns - std::floor(turns);
-    if (frac >= 1.0) frac = 0.0;  // a tiny negative angle rounds up to a whole turn
-    a.freq[i] = static_cast<uint64_t>(frac * 18446744073709551616.0);  // 2^64, exact
+    a.freq[i] = turn_fraction(f);
     a.axis[i] = static_cast<uint8_t>(ax);
   }
   return SWA_OK;

@@ -3,11 +3,11 @@
 //
 // One kernel: a CTA takes up to 16 tokens, all heads of q, k (and v) of each.
 // Pair i of a row at position p turns by p * inv_freq[i].  The angle is kept as
-// a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1)):
-// p * F_i mod 2^64 is the angle modulo a turn, exact but for the rounding of
-// inv_freq itself, for any int32 p, by one integer multiply; rounded to
-// fp32 it goes through sincospif.  A token's R/2 angles are computed once, into shared
-// memory, for all its heads.
+// a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1))
+// (swa_turn.h): p * F_i mod 2^64 is the angle modulo a turn by one integer
+// multiply, off by |p| 2^-65 turns, at most 2^-34 for any int32 p; rounded to
+// fp32 it goes through sincospif.  A token's R/2 angles are computed once, into
+// shared memory, for all its heads.
 //
 // Bound by HBM: every element is read and written once.  Each thread keeps one
 // place in the head row (VEC elements and their partners) and walks over

@@ -275,8 +275,10 @@ SWA_API swa_status_t swa_dropout_mask(const swa_params_t *p, uint8_t *mask, size
  * Pair i is elements (i, i + R/2), or (2i, 2i + 1) when interleaved = 1.
  * Elements past R are copied.  The backward turns by -t (the transpose of the
  * rotation).  The angle is formed as pos * inv_freq / 2 pi modulo 1 in 64-bit
- * fixed point, so positions anywhere in the int32 range keep the accuracy of
- * small ones; the products are fp32 and rounded once to the element type.
+ * fixed point, with inv_freq / 2 pi modulo 1 rounded once to 2^-64, so positions
+ * anywhere in the int32 range keep the accuracy of small ones (within 2^-34
+ * turns, for the inv_freq that is given); the products are fp32 and rounded once
+ * to the element type.
  *
  * Every tensor may be strided: a swa_strides_t gives the distances, in
  * elements, between batches, rows (tokens) and heads; a NULL stands for the
