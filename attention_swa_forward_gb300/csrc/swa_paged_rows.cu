@@ -127,8 +127,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Behind the tile kernel of the same call (overlap), whose CTAs signalled
   // after their own wait, every earlier grid has completed: this one may run
-  // beside that kernel, and its first CTA waits for it at the end.
-  if (!a.overlap) griddep_wait();
+  // beside that kernel, and its first CTA waits for it at the end.  Its other
+  // CTAs do not wait for a grid, which would make what earlier grids wrote
+  // visible to them: the fence does, so that no line which their SM's L1 holds
+  // from a call before is taken for q, a length or a block table entry (K and V
+  // are read from L2).  Reading all of those from L2 instead cost the calls
+  // without overlap, whose warps share them in L1: 131072 keys 86.1 us for
+  // 83.4, one token 6.7 for 6.3.
+  if (a.overlap) __threadfence();
+  else griddep_wait();
   griddep_launch_dependents();
   const PagedItem w = resolve_paged(tab, a.groups, static_cast<int>(blockIdx.x));
   const int split = blockIdx.y;
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
       const int entry = j / g.page_size;
       my_slot = j - entry * g.page_size;
       const int64_t e = w.b * g.table_stride + entry;
-      const int page = in_bounds(e, 1, g.n_table, a.err) ? __ldg(g.table + e) : -1;
+      const int page = in_bounds(e, 1, g.n_table, a.err) ? g.table[e] : -1;
       if (page >= 0 && page < g.num_pages) my_page = page;
       else bad = kPageErrEntry;
     }
@@ -494,8 +501,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int r = blockIdx.y * (kJoinWarps / WPR) + warp / WPR, part = warp % WPR;
   const int tok0 = w.tile * a.tok;
   const int n_tok = min(a.tok, w.q_len - tok0);
-  // (the lengths come from grids before the one that wrote the partial rows)
-  int kv_len = in_bounds(w.b, 1, g.n_lens, a.err) ? g.kv_lens[w.b] : 0;
+  // (the lengths come from grids before the one that wrote the partial rows:
+  // there is nothing to wait for, and L2 has them)
+  int kv_len = in_bounds(w.b, 1, g.n_lens, a.err) ? __ldcg(g.kv_lens + w.b) : 0;
   if (kv_len < 0 || kv_len > g.kv_limit) kv_len = 0;
   int lo, hi, st0, st1, active;
   paged_key_range(a.sparse_mode, a.pre, a.next, kv_len, w.q_len, tok0, n_tok, &lo, &hi);
