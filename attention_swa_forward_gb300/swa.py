@@ -581,21 +581,24 @@ def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
-    """A tensor of the stream the call runs on: what is freed when the call
-    returns (a workspace) is then not handed out again before it has run."""
+def _empty(shape, dtype, beside, name, stream):
+    """A tensor on the device of `beside` (argument `name`), of the stream the call
+    runs on: what is freed when the call returns (a workspace) is then not handed
+    out again before it has run."""
+    if not isinstance(beside, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor")
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=beside.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=beside.device)
 
 
 def _rope_call(name, geom, q, k, positions, q_out, k_out, stream):
     p = geom if type(geom) is RopeParams else _rope_params(geom)
     if q_out is None and q is not None:
-        q_out = _empty(p.q_shape, p.torch_dtype, q.device, stream)
+        q_out = _empty(p.q_shape, p.torch_dtype, q, "q", stream)
     if k_out is None and k is not None:
-        k_out = _empty(p.k_shape, p.torch_dtype, k.device, stream)
+        k_out = _empty(p.k_shape, p.torch_dtype, k, "k", stream)
     status = _bind().rope(lib().entries[name], p.addr, q, k, positions, q_out, k_out, _handle(stream))
     if status != SWA_OK:
         _check(status)
@@ -645,9 +648,9 @@ def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, 
     p = geom if type(geom) is PagedParams else _paged_params(geom)
     r = rope if rope is None or type(rope) is RopeParams else _rope_params(rope)
     if q is not None and q_out is None:
-        q_out = _empty(p.q_shape, p.torch_dtype, q.device, stream)
+        q_out = _empty(p.q_shape, p.torch_dtype, q, "q", stream)
     if workspace is None:
-        workspace = _empty(swa_paged_append_workspace_size(p), torch.uint8, k.device, stream)
+        workspace = _empty(swa_paged_append_workspace_size(p), torch.uint8, k, "k", stream)
     status = _bind().paged_append(lib().entries["swa_paged_append"], p.addr, k, v, k_pages, v_pages, block_table,
                                   kv_lens, 0 if r is None else r.addr, positions, q, q_out, workspace,
                                   _handle(stream))
@@ -662,13 +665,13 @@ def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, sof
     the paged cache; returns (out, softmax_max, softmax_sum)."""
     p = geom if type(geom) is PagedParams else _paged_params(geom)
     if out is None:
-        out = _empty(p.q_shape, p.torch_dtype, q.device, stream)
+        out = _empty(p.q_shape, p.torch_dtype, q, "q", stream)
     if softmax_max is None:
-        softmax_max = _empty(p.stat_shape, torch.float32, q.device, stream)
+        softmax_max = _empty(p.stat_shape, torch.float32, q, "q", stream)
     if softmax_sum is None:
-        softmax_sum = _empty(p.stat_shape, torch.float32, q.device, stream)
+        softmax_sum = _empty(p.stat_shape, torch.float32, q, "q", stream)
     if workspace is None:
-        workspace = _empty(swa_paged_forward_workspace_size(p), torch.uint8, q.device, stream)
+        workspace = _empty(swa_paged_forward_workspace_size(p), torch.uint8, q, "q", stream)
     status = _bind().paged_forward(lib().entries["swa_paged_forward"], p.addr, q, k_pages, v_pages, block_table,
                                    kv_lens, out, softmax_max, softmax_sum, workspace, _handle(stream))
     if status != SWA_OK:
