@@ -156,6 +156,17 @@ T address(PyObject* o) {
   return reinterpret_cast<T>(PyLong_AsVoidPtr(o));
 }
 
+// The library's part of a call, without the interpreter's lock: a launch waits
+// while the stream's queue is full, and other threads run meanwhile.  Whatever
+// comes from a Python object is taken before.
+template <typename F, typename... A>
+swa_status_t unlocked(F* fn, A... a) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const swa_status_t st = fn(a...);
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
   if (got != want) {
@@ -202,8 +213,8 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const int32_t* pos = positions(tensor(a[4], "positions"), p.n_axes, p.B * p.S, dev);
     const On on(dev, a[7]);
-    return fn(&p, x[0].ptr, x[0].strides(), x[1].ptr, x[1].strides(), pos, x[2].ptr, x[2].strides(), x[3].ptr,
-              x[3].strides(), on.stream);
+    return unlocked(fn, &p, x[0].ptr, x[0].strides(), x[1].ptr, x[1].strides(), pos, x[2].ptr, x[2].strides(),
+                    x[3].ptr, x[3].strides(), on.stream);
   });
 }
 
@@ -234,9 +245,9 @@ PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (qo) xo = arg(*qo, "q_out", qs, type, dev);
     const at::Tensor& ws = workspace(a[12], dev);
     const On on(dev, a[13]);
-    return fn(&p, xk.ptr, xk.strides(), xv.ptr, xv.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
-              static_cast<const int32_t*>(l.data_ptr()), rope, pp, xq.ptr, xq.strides(), xo.ptr, xo.strides(),
-              ws.data_ptr(), ws.nbytes(), on.stream);
+    return unlocked(fn, &p, xk.ptr, xk.strides(), xv.ptr, xv.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table,
+                    row, static_cast<const int32_t*>(l.data_ptr()), rope, pp, xq.ptr, xq.strides(), xo.ptr, xo.strides(),
+                    ws.data_ptr(), ws.nbytes(), on.stream);
   });
 }
 
@@ -262,9 +273,9 @@ PyObject* bind_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect_dense(ss, "softmax_sum", stats, at::kFloat, dev);
     const at::Tensor& ws = workspace(a[10], dev);
     const On on(dev, a[11]);
-    return fn(&p, xq.ptr, xq.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
-              static_cast<const int32_t*>(l.data_ptr()), out.data_ptr(), static_cast<float*>(sm.data_ptr()),
-              static_cast<float*>(ss.data_ptr()), ws.data_ptr(), ws.nbytes(), on.stream);
+    return unlocked(fn, &p, xq.ptr, xq.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
+                    static_cast<const int32_t*>(l.data_ptr()), out.data_ptr(), static_cast<float*>(sm.data_ptr()),
+                    static_cast<float*>(ss.data_ptr()), ws.data_ptr(), ws.nbytes(), on.stream);
   });
 }
 

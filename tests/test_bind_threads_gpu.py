@@ -1,0 +1,59 @@
+"""While a rotary or paged call is inside the library (a launch waits when the
+stream's queue is full), other Python threads run, as with the dense calls."""
+import ctypes
+import subprocess
+import threading
+import time
+
+import pytest
+import torch
+
+from attention_swa_forward_gb300 import swa
+from tests.test_paged_refusals_gpu import APPEND_ROPE, D, N, N_KV, T, append_args, forward_args, geometry, zeros
+
+pytestmark = pytest.mark.gpu
+WAIT = 0.4  # seconds
+
+
+@pytest.fixture(scope="module")
+def slow_entry(tmp_path_factory):
+    """The address of an entry point that takes WAIT seconds and does nothing."""
+    d = tmp_path_factory.mktemp("slow")
+    (d / "slow.c").write_text(f"#include <unistd.h>\nint slow() {{ usleep({int(WAIT * 1e6)}); return 0; }}\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(d / "slow.c"), "-o", str(d / "slow.so")], check=True)
+    lib = ctypes.CDLL(str(d / "slow.so"))
+    return ctypes.cast(lib.slow, ctypes.c_void_p).value
+
+
+def test_other_threads_run_during_a_call(slow_entry, monkeypatch):
+    geom, args, more = geometry(), forward_args(), append_args()
+    q, k, pos = zeros(T, N, D), zeros(T, N_KV, D), zeros(2, T, dtype=torch.int32)
+    calls = {
+        "rope": lambda: swa.rope(APPEND_ROPE, q, k, pos),
+        "append": lambda: swa.paged_append(geom, rope=APPEND_ROPE, **more),
+        "forward": lambda: swa.paged_forward(geom, **args),
+    }
+    for call in calls.values():
+        call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(swa.lib(), "entries", dict.fromkeys(swa.lib().entries, slow_entry))
+    for name, call in calls.items():
+        ticks, done = [], threading.Event()
+
+        def watch():
+            while not done.is_set():
+                ticks.append(time.monotonic())
+                time.sleep(0.01)
+
+        other = threading.Thread(target=watch)
+        other.start()
+        try:
+            t0 = time.monotonic()
+            call()
+            t1 = time.monotonic()
+        finally:
+            done.set()
+            other.join()
+        assert t1 - t0 >= WAIT * 0.9
+        # a thread that sleeps 10 ms at a time ran through the middle of the call
+        assert sum(t0 + 0.25 * WAIT < t < t0 + 0.75 * WAIT for t in ticks) >= 3, name
