@@ -137,6 +137,18 @@ int device_of(const at::Tensor& t) {
   return static_cast<int>(t.get_device());
 }
 
+// An integer as a pointer.  Anything else is refused: the NULL that the
+// conversion gives in its place would be taken for an answer.
+template <typename T>
+T address(PyObject* o, const char* name) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refused(std::string(name) + ": expected an address as an integer");
+  }
+  return reinterpret_cast<T>(p);
+}
+
 // Makes `device` current if it is not, and picks the stream.
 struct On {
   std::optional<c10::cuda::CUDAGuard> guard;
@@ -147,14 +159,9 @@ struct On {
       stream = reinterpret_cast<swa_stream_t>(
           c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
     else
-      stream = static_cast<swa_stream_t>(PyLong_AsVoidPtr(s));
+      stream = address<swa_stream_t>(s, "stream");  // (0 is the default stream)
   }
 };
-
-template <typename T>
-T address(PyObject* o) {
-  return reinterpret_cast<T>(PyLong_AsVoidPtr(o));
-}
 
 // The library's part of a call, without the interpreter's lock: a launch waits
 // while the stream's queue is full, and other threads run meanwhile.  Whatever
@@ -174,9 +181,7 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
     return nullptr;
   }
   try {
-    const swa_status_t st = body();
-    if (PyErr_Occurred()) return nullptr;
-    return PyLong_FromLong(st);
+    return PyLong_FromLong(body());
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const std::exception& e) {
@@ -188,8 +193,8 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
 // rope(fn, params, q, k, positions, q_out, k_out, stream)
 PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> swa_status_t {
-    const auto fn = address<decltype(&swa_rope_forward)>(a[0]);
-    const swa_rope_params_t& p = *address<const swa_rope_params_t*>(a[1]);
+    const auto fn = address<decltype(&swa_rope_forward)>(a[0], "entry point");
+    const swa_rope_params_t& p = *address<const swa_rope_params_t*>(a[1], "parameters");
     const at::Tensor *q = tensor_or_none(a[2], "q"), *k = tensor_or_none(a[3], "k");
     const at::Tensor *qo = tensor_or_none(a[5], "q_out"), *ko = tensor_or_none(a[6], "k_out");
     if (!q && !k) throw Refused("q or k is required");
@@ -222,9 +227,9 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //              workspace, stream)
 PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> swa_status_t {
-    const auto fn = address<decltype(&swa_paged_append)>(a[0]);
-    const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1]);
-    const auto* rope = address<const swa_rope_params_t*>(a[8]);
+    const auto fn = address<decltype(&swa_paged_append)>(a[0], "entry point");
+    const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1], "parameters");
+    const auto* rope = address<const swa_rope_params_t*>(a[8], "rope");
     const at::Tensor& k = tensor(a[2], "k");
     const int dev = device_of(k);
     const at::ScalarType type = scalar_type(p.dtype);
@@ -254,8 +259,8 @@ PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // paged_forward(fn, params, q, k_pages, v_pages, block_table, kv_lens, out, softmax_max, softmax_sum, workspace, stream)
 PyObject* bind_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> swa_status_t {
-    const auto fn = address<decltype(&swa_paged_forward)>(a[0]);
-    const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1]);
+    const auto fn = address<decltype(&swa_paged_forward)>(a[0], "entry point");
+    const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1], "parameters");
     const at::Tensor& q = tensor(a[2], "q");
     const int dev = device_of(q);
     const at::ScalarType type = scalar_type(p.dtype);

@@ -57,3 +57,16 @@ def test_other_threads_run_during_a_call(slow_entry, monkeypatch):
         assert t1 - t0 >= WAIT * 0.9
         # a thread that sleeps 10 ms at a time ran through the middle of the call
         assert sum(t0 + 0.25 * WAIT < t < t0 + 0.75 * WAIT for t in ticks) >= 3, name
+
+
+def test_a_stream_that_is_no_handle_enqueues_nothing():
+    out = torch.full((T, N, D), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    args = {**forward_args(), "out": out}
+
+    class Odd:
+        cuda_stream = "no handle"
+
+    with pytest.raises(ValueError, match="stream"):
+        swa.paged_forward(geometry(), **args, workspace=swa.paged_forward_workspace(geometry(), "cuda:0"), stream=Odd())
+    torch.cuda.synchronize()
+    assert (out == 7).all()
