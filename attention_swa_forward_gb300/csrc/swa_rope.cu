@@ -5,8 +5,8 @@
 // Pair i of a row at position p turns by p * inv_freq[i].  The angle is kept as
 // a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1))
 // (swa_turn.h): p * F_i mod 2^64 is the angle modulo a turn by one integer
-// multiply, off by |p| 2^-65 turns, at most 2^-34 for any int32 p; rounded to
-// fp32 it goes through sincospif.  A token's R/2 angles are computed once, into
+// multiply, off by |p| 2^-65 turns, at most 2^-34 for any int32 p; its distance
+// from the nearest quarter turn goes through sincospif.  A token's R/2 angles are computed once, into
 // shared memory, for all its heads.
 //
 // Bound by HBM: every element is read and written once.  Each thread keeps one
@@ -165,10 +165,22 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
         p = rope_in_bounds(e, 1, a.n_axes * a.n_pos, a.err) ? a.positions[e] : 0;
       }
       const uint64_t turn64 = static_cast<uint64_t>(static_cast<int64_t>(p)) * a.freq[i];
-      // the angle in half turns, [-1, 1): as a signed number, 2^63 is half a turn
-      const float ht = __ll2float_rn(static_cast<int64_t>(turn64)) * 1.0842021724855044e-19f;  // 2^-63
+      // its nearest quarter turn and the distance from there, in half turns within
+      // a quarter: rounded to fp32, that is off by 2^-24 of itself, where the
+      // whole angle was by 2^-25 half turns, much of a sine near its zeros
+      const int quarter = static_cast<int>((turn64 + (uint64_t(1) << 61)) >> 62);
+      const int64_t rest = static_cast<int64_t>(turn64 - (static_cast<uint64_t>(quarter) << 62));
       float sn, cs;
-      sincospif(ht, &sn, &cs);
+      sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63
+      if (quarter & 1) {
+        const float x = sn;
+        sn = cs;
+        cs = -x;
+      }
+      if (quarter & 2) {
+        sn = -sn;
+        cs = -cs;
+      }
       s.cs[tk][i] = cs;
       s.sn[tk][i] = a.inverse ? -sn : sn;
     }
