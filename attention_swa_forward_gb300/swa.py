@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import importlib.util
+import math
 import os
 import threading
 
@@ -497,8 +498,11 @@ class RopeParams:
         if geom.inv_freq is not None and len(geom.inv_freq) != half:
             raise ValueError(f"inv_freq names {len(geom.inv_freq)} pairs, rotary_dim has {half}")
         freq = geom.inv_freq
-        if freq is None and c.base > 0:  # the library's default, formed once here instead of in every call
-            freq = [c.base ** (-2.0 * i / (2 * half)) for i in range(half)]
+        if freq is None and 0 < c.base < math.inf:  # the library's default, formed once here instead of in every call
+            try:
+                freq = [c.base ** (-2.0 * i / (2 * half)) for i in range(half)]
+            except OverflowError:
+                pass  # the library refuses it
         if freq is not None:
             self._freq = (ctypes.c_double * max(half, 1))(*[float(x) for x in freq])
             c.inv_freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))

@@ -8,6 +8,10 @@ from fractions import Fraction
 
 import pytest
 
+from attention_swa_forward_gb300 import build as B
+from attention_swa_forward_gb300 import swa
+from attention_swa_forward_gb300.workloads import RopeGeometry
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "attention_swa_forward_gb300", "csrc")
 # 60 decimals of 2 pi
 TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
@@ -51,3 +55,15 @@ def test_an_opposite_frequency_turns_as_far_back(fraction_of):
     fs = frequencies()
     for a, b in zip(fraction_of(fs), fraction_of([-f for f in fs])):
         assert (a + b) % 2 ** 64 == 0
+
+
+@pytest.mark.parametrize("base", [math.inf, math.nan, 0.0, -1.0, 1e-320, 1e-300])
+def test_a_base_without_frequencies_is_refused_from_python_too(base):
+    """RopeParams forms the default frequencies; the refusal is the library's.
+    (Positions off their alignment, checked after the parameters, keep any call
+    from being made.)"""
+    B.build()
+    p = swa.RopeParams(RopeGeometry("TND", 1, 16, 4, 64, base=base))
+    st = swa.lib().swa_rope_forward(p.ref(), 1 << 20, None, None, None, (1 << 20) + 2, 1 << 20, None, None, None, None)
+    assert st == swa.SWA_ERR_PARAM_INVALID
+    assert "base" in swa.swa_last_error() or "inv_freq" in swa.swa_last_error()
