@@ -459,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = walk.next(a, tab, n_units, x), more_after;
     Unit after;  // formed while the last product of this unit runs
     for (; ok && more; x = after, more = more_after) {
+      // A unit begins with instructions of the whole warp (tensor memory loads and
+      // stores): lanes of rows past the last tile's, which stored nothing, wait
+      // here for the others.
+      __syncwarp();
       if (x.idle) {
         more_after = walk.next(a, tab, n_units, after);
         continue;
@@ -620,41 +624,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 32; ++y) acc[ch][y] = 0u;
       }
-      if (row_valid) {
-        // relative to the true maximum from here on
-        const bool empty = m_true == -INFINITY;
-        const float f = empty ? 0.f : ex2_approx(m_use - m_true);
-        const float mul = !x.direct ? f : (l > 0.f || l != l ? 1.f / l : 0.f);
-        const int h = x.w.vh * a.gs + (r - i * a.gs);
-        const int64_t row = static_cast<int64_t>(x.w.q_start + x.tok0 + i) * g.N + h;
-        const int64_t pr = (x.slot_id - a.whole) * a.rows_pad + r;
+      if (!row_valid) continue;
+      // relative to the true maximum from here on
+      const bool empty = m_true == -INFINITY;
+      const float f = empty ? 0.f : ex2_approx(m_use - m_true);
+      const float mul = !x.direct ? f : (l > 0.f || l != l ? 1.f / l : 0.f);
+      const int h = x.w.vh * a.gs + (r - i * a.gs);
+      const int64_t row = static_cast<int64_t>(x.w.q_start + x.tok0 + i) * g.N + h;
+      const int64_t pr = (x.slot_id - a.whole) * a.rows_pad + r;
 #pragma unroll
-        for (int ch = 0; ch < D / 32; ++ch) {
-          if (ch * 32 >= g.D) break;
-          float o[32];
+      for (int ch = 0; ch < D / 32; ++ch) {
+        if (ch * 32 >= g.D) break;
+        float o[32];
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(acc[ch][y]) * mul;
+        for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(acc[ch][y]) * mul;
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const int col = ch * 32 + q4 * 8;
-            if (col >= g.D) continue;
-            if (!x.direct) {
-              store8<F16>(a.part_o, pr * D + col, &o[q4 * 8], true);
-            } else if (in_bounds(row * g.D + col, 8, a.n_out, a.err)) {
-              store8<F16>(a.out, row * g.D + col, &o[q4 * 8], false);
-            }
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const int col = ch * 32 + q4 * 8;
+          if (col >= g.D) continue;
+          if (!x.direct) {
+            store8<F16>(a.part_o, pr * D + col, &o[q4 * 8], true);
+          } else if (in_bounds(row * g.D + col, 8, a.n_out, a.err)) {
+            store8<F16>(a.out, row * g.D + col, &o[q4 * 8], false);
           }
         }
-        if (!x.direct) {
-          a.part_ml[pr] = make_float2(m_true, l * f);
-        } else if (in_bounds(row, 1, a.n_stats, a.err)) {
-          if (a.smax) a.smax[row] = empty ? -INFINITY : m_true * kLn2;
-          if (a.ssum) a.ssum[row] = l * f;
-        }
       }
-      // The next unit begins with instructions of the whole warp (tensor memory
-      // loads and stores): a warp with rows past the tile's joins again here.
-      __syncwarp();
+      if (!x.direct) {
+        a.part_ml[pr] = make_float2(m_true, l * f);
+      } else if (in_bounds(row, 1, a.n_stats, a.err)) {
+        if (a.smax) a.smax[row] = empty ? -INFINITY : m_true * kLn2;
+        if (a.ssum) a.ssum[row] = l * f;
+      }
     }
   }
   __syncwarp();  // (the roles of one lane: its warp waits here, not inside the barrier)
