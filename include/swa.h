@@ -373,7 +373,9 @@ typedef struct {
   int64_t max_pages;           /* block table columns, 1..2^24 */
   int64_t max_kv_len;          /* largest kv_lens[b] of any (re)play of this call, up to 2^28; 0 (the
                                   default): max_pages * page_size.  How the keys are split over the GPU
-                                  follows from it */
+                                  follows from it, whatever the lengths are: without a window, up to 16
+                                  query rows of a sequence and key/value head take a CTA, and up to 8 KB
+                                  of workspace, per 16384 keys of this bound */
   double scale;                /* score scale, default 1.0 */
   int64_t pre_tokens;          /* BAND, around each token's position; defaults 2147483647 */
   int64_t next_tokens;
@@ -398,7 +400,8 @@ SWA_API void swa_paged_params_default(swa_paged_params_t *p);
  *   positions     device, int32 [n_axes, T_q], or NULL: every axis at the
  *                 token's position in its sequence (0 where that is negative)
  *   q, q_out      NULL, or (with rope only) queries [T_q, N, D] rotated along
- *                 with k into q_out, in the same launch
+ *                 with k into q_out, in the same launch; q_out may be q itself
+ *                 with the same strides
  *   workspace     device, >= swa_paged_append_workspace_size bytes, 256-byte
  *                 aligned; holds the status only
  * Errors: as swa_rope_forward, plus SWA_ERR_WORKSPACE. */
@@ -417,7 +420,10 @@ SWA_API swa_status_t swa_paged_append(const swa_paged_params_t *p, const void *k
  * p = kv_lens[b] - q_len_b + i, which sees key j iff p - pre_tokens <= j <=
  * p + next_tokens and 0 <= j < kv_lens[b] (mode 4), or every key (mode 0).  A
  * row that sees no key gets out = 0, softmax_max = -inf, softmax_sum = 0.
- *   q             device, p->dtype, [T_q, N, D], may be strided
+ * Scores, statistics and sums are fp32; exp(scale q.k - maximum) is rounded to
+ * p->dtype before the product with V, as in swa_forward, and out once more.
+ *   q             device, p->dtype, [T_q, N, D], may be strided, its rows and
+ *                 heads apart (no stride 0)
  *   k_pages, v_pages, block_table, table_stride, kv_lens
  *                 as for swa_paged_append; read only
  *   out           device, p->dtype, dense [T_q, N, D]

@@ -82,3 +82,20 @@ def test_queries_with_gaps(name, dtype):
         assert torch.equal(view, turned), (row, head)
         view.copy_(q)
         assert torch.equal(torch.nan_to_num(store, nan=7.0), torch.nan_to_num(before, nan=7.0))  # nothing between
+
+
+def test_append_rotates_queries_in_place():
+    q_lens, kv_lens = CHUNKS["mixed"]
+    geom = geometry(q_lens, kv_lens, 16, N=6, N_kv=3, D=72)
+    _, _, kp, vp, table, lens = (t.to(DEV) if torch.is_tensor(t) else t for t in draw_cache(geom, kv_lens, 5))
+    g = torch.Generator().manual_seed(6)
+    fused = torch.randn(geom.T_q, 12, 72, generator=g).bfloat16().to(DEV)  # q, k and v of one projection
+    rope = RopeGeometry("TND", 1, geom.T_q, 6, 72, N_kv=3, rotary_dim=40)
+    pages = [t.clone() for t in (kp, vp)]
+    want = swa.paged_append(geom, fused[:, 6:9], fused[:, 9:], kp, vp, table, lens, rope=rope, q=fused[:, :6])
+    keep = fused[:, 6:].clone()
+    got = swa.paged_append(geom, fused[:, 6:9], fused[:, 9:], *pages, table, lens, rope=rope, q=fused[:, :6],
+                           q_out=fused[:, :6])
+    assert got.data_ptr() == fused.data_ptr() and torch.equal(got, want) and torch.equal(fused[:, 6:], keep)
+    for a, b in zip(pages, (kp, vp)):
+        assert torch.equal(torch.nan_to_num(a, nan=7.0), torch.nan_to_num(b, nan=7.0))
