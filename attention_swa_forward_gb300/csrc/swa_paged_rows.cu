@@ -18,9 +18,16 @@
 // soon as they are in registers, and no per-row tests inside the visible run,
 // a CTA draws 46 GB/s (32 before).  Measured: 256 sequences x 1024-key windows
 // 137 us (the copy rate's own time), 64 x 4096 145 us (0.96 of it), 24
-// sequences of up to 8192 keys, 16 heads of 64, 81 us (0.88), one sequence of
-// 131072 keys 84 us (0.94).  The warps' results are joined in shared memory at
+// sequences of up to 8192 keys, 16 heads of 64, 80 us (0.89), one sequence of
+// 131072 keys 83 us (0.95).  The warps' results are joined in shared memory at
 // the end.
+//
+// The probabilities are rounded to the element type for the second product, as
+// in the dense forward: half a step (2^-8 in bf16, 2^-11 in fp16) of each, which
+// leaves the output 1.4 times as far from exact as its own rounding does
+// (relative 2.3e-3 and 1.7e-3 in bf16).  With what the rounding leaves out in a
+// second product it was at its own rounding, 3 to 5 % slower (64 x 4096 keys
+// 150.5 us for 144.1, 131072 keys 85.9 for 82.2): not kept.
 //
 // A 16-key group lies in one page (page sizes are multiples of 16).  Keys no
 // row of the tile sees are never read: their chunks are zero-filled, so a NaN

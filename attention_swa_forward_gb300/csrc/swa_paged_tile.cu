@@ -3,8 +3,9 @@
 // key/value head), key tiles of 128.
 //
 // Per row (include/swa.h): O = sum_j softmax_j(scale q.k_j) v_j over visible
-// keys, softmax_max, softmax_sum; online softmax in fp32 (log2 units), P
-// rounded to the element type for the second product.
+// keys, softmax_max, softmax_sum; online softmax in fp32 (log2 units).  P is
+// rounded to the element type, which the second product's operands have (as in
+// swa_fwd.cu; swa_paged_rows.cu says what that does to the result).
 //
 // Bound by the tensor pipe and its hand-offs to the softmax, like the dense
 // forward, whose roles it keeps (swa_fwd.cu): one thread per row in warps 0-3,
@@ -16,10 +17,11 @@
 //  * One CTA per SM walks several row tiles, every ring and barrier running on
 //    from one to the next: the lengths, block table entries, K, V and Q of the
 //    next tile arrive while this one is computed.  (One CTA per row tile paid
-//    about 7 us each for its start and end: prompt of 8192 tokens 430 us, now
-//    390; 2048 tokens under a 4096 window 128, now 123, and 117 with the last
-//    round's tiles split; 8192 under it 349, now 315.)  Tiles go by falling
-//    weight, in rounds of alternating direction.
+//    about 7 us each for its start and end.  On the same inputs again and again:
+//    prompt of 8192 tokens 430 us, then 390; 2048 tokens under a 4096 window 128,
+//    then 123, and 117 with the last round's tiles split; 8192 under it 349, then
+//    315.  One call among others on inputs of its own: prompt 423, 2048 tokens
+//    120.)  Tiles go by falling weight, in rounds of alternating direction.
 //    At a boundary the softmax warps still wait for the last product and store
 //    their rows (~5000 cycles).  Handing the stores to four more warps needed
 //    setmaxnreg and waits without calls, and gained nothing (392 us);

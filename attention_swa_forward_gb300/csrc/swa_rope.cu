@@ -12,7 +12,7 @@
 // Bound by HBM: every element is read and written once.  Each thread keeps one
 // place in the head row (VEC elements and their partners) and walks over
 // (token, head) rows, four in flight through registers.  671 MB (32768 tokens,
-// 32 + 8 heads of 128) take 108 us, 0.92 of the measured copy rate.  Walking
+// 32 + 8 heads of 128) take 106 us, 0.93 of the measured copy rate.  Walking
 // the heads of a token first in BNSD, 256 bytes at a time, took 122 us; 16
 // tokens per CTA 112, 4 tokens 116; all rows staged through shared memory by
 // cp.async, 4 tokens per CTA, 130: what is left are instructions, not bytes in

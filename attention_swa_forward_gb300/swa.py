@@ -374,8 +374,9 @@ def swa_debug_schedule(params: "Params", pass_: int):
 
 
 def swa_debug_stall(kernels: int):
-    """Test hook: kernels (bit 0 forward, 1 key-major, 2 query-major) whose
-    compute warps first wait on a barrier nothing completes; 0 turns it off."""
+    """Test hook: kernels (bit 0 forward, 1 key-major, 2 query-major, 3 paged
+    attention's row tiles) whose compute warps first wait on a barrier nothing
+    completes; 0 turns it off."""
     lib().swa_debug_stall(int(kernels))
 
 
