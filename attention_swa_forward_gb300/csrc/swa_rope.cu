@@ -6,8 +6,8 @@
 // a 64-bit fraction of a turn, F_i = round(2^64 * (inv_freq_i / 2 pi mod 1))
 // (swa_turn.h): p * F_i mod 2^64 is the angle modulo a turn by one integer
 // multiply, off by |p| 2^-65 turns, at most 2^-34 for any int32 p; its distance
-// from the nearest quarter turn goes through sincospif.  A token's R/2 angles are computed once, into
-// shared memory, for all its heads.
+// from the nearest quarter turn goes through sincospif.  A token's R/2 angles
+// are computed once, into shared memory, for all its heads.
 //
 // Bound by HBM: every element is read and written once.  Each thread keeps one
 // place in the head row (VEC elements and their partners) and walks over

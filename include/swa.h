@@ -433,7 +433,9 @@ SWA_API swa_status_t swa_paged_append(const swa_paged_params_t *p, const void *k
  *                 aligned: status, and the partial results of keys split over
  *                 several CTAs.  Needs no initialisation; a workspace may be
  *                 reused by later calls on the same stream, but not by calls
- *                 (or replays of graphs) running concurrently
+ *                 (or replays of graphs) running concurrently, nor by calls that
+ *                 several threads make at once, on one stream either (a call is
+ *                 several launches)
  * Errors: as swa_forward.  The results do not depend on how the keys were
  * split beyond fp32 rounding, and are the same bits from run to run. */
 SWA_API swa_status_t swa_paged_forward_workspace_size(const swa_paged_params_t *p, size_t *bytes);

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from attention_swa_forward_gb300 import swa
+from tests.test_paged_order_gpu import MIXED, Serving
 from tests.test_paged_refusals_gpu import APPEND_ROPE, D, N, N_KV, T, append_args, forward_args, geometry, zeros
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +71,46 @@ def test_a_stream_that_is_no_handle_enqueues_nothing():
         swa.paged_forward(geometry(), **args, workspace=swa.paged_forward_workspace(geometry(), "cuda:0"), stream=Odd())
     torch.cuda.synchronize()
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("one_stream", [True, False])
+def test_threads_that_call_at_once_match_serial_calls(one_stream):
+    """Mixed batches, whose calls are up to four launches, from four threads: their
+    launches interleave, on one stream or on four; each has its own workspaces."""
+    names = ["40_tiles_split", "40_few_rows_joined", "40_last_round_split", "17_tiles_of_a_round"]
+    work = []
+    for i, name in enumerate(names):
+        s = Serving(*MIXED[name](), 23 + i)
+        s.feed()
+        s.step()
+        work.append((s, s.check(name)))
+    torch.cuda.synchronize()
+    shared = torch.cuda.Stream()
+    got, errors = [[] for _ in work], []
+    start = threading.Barrier(len(work))
+
+    def run(i):
+        try:
+            s = work[i][0]
+            with torch.cuda.stream(shared if one_stream else torch.cuda.Stream()):
+                start.wait()
+                for _ in range(40):
+                    for t in (s.rq, s.out, s.sm, s.ss):
+                        t.fill_(7.0)
+                    s.step()
+                    got[i].append([t.clone() for t in (s.out, s.sm, s.ss)])
+        except Exception as e:  # noqa: BLE001 (raised below, in the test's thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for (s, want), res in zip(work, got):
+        assert len(res) == 40
+        for again in res:
+            for a, b in zip(want, again):
+                assert torch.equal(a, b)
