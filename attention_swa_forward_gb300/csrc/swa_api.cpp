@@ -123,6 +123,8 @@ swa_status_t make_plan(const swa_params_t* p, Plan& plan) {
     const long double s = (long double)p->pre_tokens + (long double)p->next_tokens;
     if (s < 0) return fail(SWA_ERR_PARAM_INVALID, "pre_tokens + next_tokens < 0: every row would be empty");
   }
+  if (p->sink_tokens < 0)
+    return fail(SWA_ERR_PARAM_INVALID, "sink_tokens must be >= 0, got %lld", (long long)p->sink_tokens);
 
   plan = Plan();
   plan.B = p->B;
@@ -203,6 +205,7 @@ swa_status_t make_plan(const swa_params_t* p, Plan& plan) {
   const int64_t lim = max_len + 1;
   g.pre = static_cast<int32_t>(std::min(std::max(p->pre_tokens, -lim), lim));
   g.next = static_cast<int32_t>(std::min(std::max(p->next_tokens, -lim), lim));
+  g.sinks = p->sparse_mode == 4 ? static_cast<int32_t>(std::min(p->sink_tokens, lim)) : 0;
   return SWA_OK;
 }
 
@@ -221,7 +224,7 @@ SeqInfo info_of(const Seq& s) {
 int64_t fwd_tile_cost(const Geometry& g, const Seq& s, int64_t t) {
   int t0, n;
   key_tiles_of_query_tile(g, info_of(s), static_cast<int>(t), &t0, &n);
-  return n;
+  return n + sink_tiles_before(g, info_of(s), static_cast<int>(t), t0);
 }
 int64_t bwd_tile_cost(const Geometry& g, const Seq& s, int64_t t) {
   int t0, n;
@@ -229,24 +232,62 @@ int64_t bwd_tile_cost(const Geometry& g, const Seq& s, int64_t t) {
   return n;
 }
 
-// Work entries of one launch family, heaviest first.
+// A key tile with sinks is seen by every query behind it.  It is cut into
+// pieces (a CTA each, which writes 128 KB to be joined) of as many steps as the
+// longest other tile of its sequence, or as half an SM's share of the pass where
+// that is more: the pieces start first, and none then ends last.  BNSD
+// 1x16x32768x128, 4 key/value heads, window of 4096: a tile has 132 steps, one
+// with sinks 1024, an SM 898 in all.
+constexpr int64_t kPieceSteps = 8, kMostPieces = 4096, kPieceSms = 152;
+
+// Work entries of one launch family, heaviest first (after the pieces of key
+// tiles with sinks, in the key-major pass).
 std::vector<SeqDesc> build_descs(const Plan& plan, bool forward) {
   const Geometry& g = plan.g;
   struct Entry {
     SeqDesc d;
     int64_t weight;
   };
-  std::vector<Entry> entries;
+  std::vector<Entry> entries, pieces;
+  int64_t share = 0;  // half an SM's steps of the key-major pass
+  if (!forward && g.sinks > 0) {
+    for (const Seq& s : plan.seqs)
+      for (int64_t t = 0; t * kTileN < s.kv_len; ++t) share += g.group * bwd_tile_cost(g, s, t);
+    share = share * g.N_kv / (2 * kPieceSms);
+  }
   auto fill = [&](const Seq& s, int32_t b, int32_t heads) {
     const int64_t rows = forward ? s.q_len : s.kv_len;
     if (rows <= 0) return;
-    const int64_t tiles = (rows + kTileM - 1) / kTileM;
-    int64_t wmax = 0;
-    for (int64_t t = 0; t < tiles; ++t)
+    int64_t tiles = (rows + kTileM - 1) / kTileM, tile0 = 0;
+    const int64_t with_sinks = forward ? 0 : std::min<int64_t>((g.sinks + kTileN - 1) / kTileN, tiles);
+    int64_t wmax = 0, wsink = 0;
+    for (int64_t t = 0; t < with_sinks; ++t) wsink = std::max(wsink, bwd_tile_cost(g, s, t));
+    for (int64_t t = with_sinks; t < tiles; ++t)
       wmax = std::max(wmax, forward ? fwd_tile_cost(g, s, t) : bwd_tile_cost(g, s, t));
-    const int64_t c0 = forward ? fwd_tile_cost(g, s, 0) : bwd_tile_cost(g, s, 0);
-    const int64_t c1 = forward ? fwd_tile_cost(g, s, tiles - 1) : bwd_tile_cost(g, s, tiles - 1);
+    const int64_t per = std::max({kPieceSteps, g.group * wmax, share});
+    const int64_t n_pieces = std::min((g.group * wsink + per - 1) / per, kMostPieces);
+    if (n_pieces > 1) {
+      SeqDesc d{};
+      d.q_start = static_cast<int32_t>(s.q_start);
+      d.q_len = static_cast<int32_t>(s.q_len);
+      d.kv_start = static_cast<int32_t>(s.kv_start);
+      d.kv_len = static_cast<int32_t>(s.kv_len);
+      d.mask_base = s.mask_base;
+      d.b = b;
+      d.tiles = static_cast<int32_t>(with_sinks);
+      d.heads = heads;
+      d.pieces = static_cast<uint16_t>(n_pieces);
+      pieces.push_back(Entry{d, (wsink + n_pieces - 1) / n_pieces});
+      tile0 = with_sinks;
+      tiles -= with_sinks;
+      if (tiles == 0) return;
+    } else {
+      wmax = std::max(wmax, wsink);
+    }
+    const int64_t c0 = forward ? fwd_tile_cost(g, s, tile0) : bwd_tile_cost(g, s, tile0);
+    const int64_t c1 = forward ? fwd_tile_cost(g, s, tile0 + tiles - 1) : bwd_tile_cost(g, s, tile0 + tiles - 1);
     SeqDesc d{};
+    d.tile0 = static_cast<uint16_t>(tile0);
     d.q_start = static_cast<int32_t>(s.q_start);
     d.q_len = static_cast<int32_t>(s.q_len);
     d.kv_start = static_cast<int32_t>(s.kv_start);
@@ -265,13 +306,22 @@ std::vector<SeqDesc> build_descs(const Plan& plan, bool forward) {
     fill(plan.seqs[0], -1, static_cast<int32_t>(plan.B * nh));
   } else {
     for (int64_t b = 0; b < plan.B; ++b) fill(plan.seqs[b], static_cast<int32_t>(b), nh);
-    std::stable_sort(entries.begin(), entries.end(),
-                     [](const Entry& x, const Entry& y) { return x.weight > y.weight; });
+    for (std::vector<Entry>* v : {&entries, &pieces})
+      std::stable_sort(v->begin(), v->end(), [](const Entry& x, const Entry& y) { return x.weight > y.weight; });
   }
   std::vector<SeqDesc> out;
-  out.reserve(entries.size());
+  out.reserve(pieces.size() + entries.size());
+  for (auto& e : pieces) out.push_back(e.d);
   for (auto& e : entries) out.push_back(e.d);
   return out;
+}
+
+// Work items of an entry, and those of a list that are pieces.
+int64_t items_of(const SeqDesc& d) { return int64_t(d.tiles) * d.heads * (d.pieces > 1 ? d.pieces : 1); }
+int64_t piece_items(const SeqDesc* d, size_t n) {
+  int64_t items = 0;
+  for (size_t i = 0; i < n; ++i) items += d[i].pieces > 1 ? items_of(d[i]) : 0;
+  return items;
 }
 
 // Split the entries into launches of at most CAP entries and run `launch` on each table.
@@ -287,7 +337,7 @@ cudaError_t for_each_table(const std::vector<SeqDesc>& descs, size_t begin, size
     for (size_t i = 0; i < n; ++i) {
       tab.d[i] = descs[c + i];
       tab.d[i].item_begin = static_cast<int32_t>(items);
-      items += static_cast<int64_t>(descs[c + i].tiles) * descs[c + i].heads;
+      items += items_of(descs[c + i]);
     }
     tab.count = static_cast<int32_t>(n);
     tab.n_items = static_cast<int32_t>(items);
@@ -379,7 +429,7 @@ FwdLayout fwd_layout(const Plan& plan) {
 }
 
 struct BwdLayout {
-  size_t lse2, dsum, q16, k16, v16, dy16, out16, total;
+  size_t lse2, dsum, q16, k16, v16, dy16, out16, part, total;
 };
 BwdLayout bwd_layout(const Plan& plan) {
   const size_t rows = static_cast<size_t>(plan.q_rows) * plan.g.N;
@@ -394,6 +444,11 @@ BwdLayout bwd_layout(const Plan& plan) {
     l.dy16 = l.v16 + round256(kv_elems(plan) * 2);
     l.out16 = l.dy16 + round256(q_elems(plan) * 2);
     l.total = l.out16 + round256(q_elems(plan) * 2);
+  }
+  if (plan.g.sinks > 0) {
+    const std::vector<SeqDesc> descs = build_descs(plan, false);
+    l.part = l.total;
+    l.total += static_cast<size_t>(piece_items(descs.data(), descs.size())) * 2 * kTileN * (plan.g.D <= 64 ? 64 : 128) * 4;
   }
   return l;
 }
@@ -607,12 +662,16 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
   a.dk = dk;
   a.dv = dv;
   a.err = reinterpret_cast<int32_t*>(ws);
-  // key-major pass: dK, dV (one work item per key tile)
+  a.part = reinterpret_cast<float*>(ws + lay.part);
+  // key-major pass: dK, dV (one work item per key tile, or per piece of one)
   const std::vector<SeqDesc> kv_descs = build_descs(plan, false);
   if (t_ev[2]) cudaEventRecord(t_ev[2], s);
-  e = run_tables(
-      kv_descs, [&](const SeqTable<kSmallTable>& t) { return launch_backward_dkv(a, t, mq, mk, mv, mdy, s); },
-      [&](const SeqTable<kLargeTable>& t) { return launch_backward_dkv(a, t, mq, mk, mv, mdy, s); });
+  auto key_major = [&](const auto& t) {
+    const cudaError_t le = launch_backward_dkv(a, t, mq, mk, mv, mdy, s);
+    a.part_base += piece_items(t.d, t.count);
+    return le;
+  };
+  e = run_tables(kv_descs, key_major, key_major);
   if (t_ev[3]) cudaEventRecord(t_ev[3], s);
   if (e != cudaSuccess) return cuda_fail(e, "backward dK/dV launch");
   // query-major pass: dQ (one work item per query tile)
@@ -623,6 +682,16 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
       [&](const SeqTable<kLargeTable>& t) { return launch_backward_dq(a, t, mq, mk, mv, mdy, s); });
   if (t_ev[5]) cudaEventRecord(t_ev[5], s);
   if (e != cudaSuccess) return cuda_fail(e, "backward dQ launch");
+  // (behind the query-major pass, which ends after the key-major one)
+  a.part_base = 0;
+  auto join = [&](const auto& t) {
+    const int64_t n = piece_items(t.d, t.count);
+    const cudaError_t le = n > 0 ? launch_backward_join(a, t, static_cast<int>(n), s) : cudaSuccess;
+    a.part_base += n;
+    return le;
+  };
+  e = run_tables(kv_descs, join, join);
+  if (e != cudaSuccess) return cuda_fail(e, "backward dK/dV join launch");
   return SWA_OK;
 }
 
@@ -685,16 +754,29 @@ swa_status_t swa_debug_schedule(const swa_params_t* p, int32_t pass, int32_t* it
       if (pass == 0) key_tiles_of_query_tile(plan.g, it.s, it.tile, &t0, &cnt);
       else if (pass == 1) query_tiles_of_key_tile(plan.g, it.s, it.tile, &t0, &cnt);
       else key_tiles_of_query_pair(plan.g, it.s, it.tile, &t0, &cnt);
-      if (items && n < capacity) {
-        int32_t* r = items + 6 * n;
-        r[0] = launch;
-        r[1] = it.b;
-        r[2] = it.n;
-        r[3] = it.tile;
-        r[4] = t0;
-        r[5] = cnt;
+      auto row = [&](int first, int partners) {
+        if (items && n < capacity) {
+          int32_t* r = items + 6 * n;
+          r[0] = launch;
+          r[1] = it.b;
+          r[2] = it.n;
+          r[3] = it.tile;
+          r[4] = first;
+          r[5] = partners;
+        }
+        ++n;
+      };
+      int sinks = 0;
+      if (pass == 0) sinks = sink_tiles_before(plan.g, it.s, it.tile, t0);
+      for (int h = 0; pass == 2 && h < 2; ++h) {
+        const int qt = 2 * it.tile + h;
+        int h0, hn;
+        if (qt * kTileM >= it.s.q_len) continue;
+        key_tiles_of_query_tile(plan.g, it.s, qt, &h0, &hn);
+        sinks = std::max(sinks, std::min(sink_tiles_before(plan.g, it.s, qt, h0), t0));
       }
-      ++n;
+      if (sinks > 0) row(0, sinks);
+      row(t0, cnt);
     }
     ++launch;
     return cudaSuccess;

@@ -211,7 +211,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // key/value head (one head without grouping): step it is query tile
   // q_t0 + it % n_q of query head w.n * group + it / n_q, and dK / dV sum
   // over all of them in TMEM.
-  const int n_it = g.group * n_q;
+  // A tile with sinks, which every later query sees, may be cut into pieces,
+  // runs of those steps for a CTA each: step it is then step it0 + it.
+  int it0 = 0, n_it = g.group * n_q;
+  if (w.pieces > 1) {
+    const int per = steps_per_piece(n_it, w.pieces);
+    it0 = min(w.piece * per, n_it);
+    n_it = min(per, n_it - it0);
+  }
 
   // The producer's lane initialises the barriers and issues the loads of K,
   // V and the first Q and dY tiles before the CTA-wide barrier, so their
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar[kBarDrainKv], 1);
     mbar_init(&bar[kBarNever], 1);
     fence_mbar_init();
-    if (n_q > 0) {
+    if (n_it > 0) {
       tma_prefetch_desc(&mq);
       tma_prefetch_desc(&mk);
       tma_prefetch_desc(&mv);
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&bar[kBarKvFull], 2 * kTileBytes);
       tma_rows<D>(s.k(), &mk, &bar[kBarKvFull], g, w.b, w.n, sq.kv_start, j0);
       tma_rows<D>(s.v(), &mv, &bar[kBarKvFull], g, w.b, w.n, sq.kv_start, j0);
-      const int i0 = q_t0 * kTileM, qn = w.n * g.group;  // step 0
+      const int i0 = (q_t0 + it0 % n_q) * kTileM, qn = w.n * g.group + it0 / n_q;  // step 0
       mbar_arrive_expect_tx(&bar[kBarQFull], kTileBytes);
       tma_rows<D>(s.q(0), &mq, &bar[kBarQFull], g, w.b, qn, sq.q_start, i0);
       mbar_arrive_expect_tx(&bar[kBarDyFull], kTileBytes);
@@ -271,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the per-query statistics below come from the preprocess grid; every
     // lane waits for it (so this grid also completes only after it has)
     griddep_wait();
-    if (n_q > 0) {
+    if (n_it > 0) {
       int q_issued = 0, dy_issued = 0;
       for (int it = 0; it < n_it; ++it) {
-        const int i0 = (q_t0 + it % n_q) * kTileM;
-        const int qn = w.n * g.group + it / n_q;  // query head of this step
+        const int i0 = (q_t0 + (it0 + it) % n_q) * kTileM;
+        const int qn = w.n * g.group + (it0 + it) / n_q;  // query head of this step
         const int qs = it % kQS;
         // Q(it) reuses the stage of Q(it - kQS), free once dK of that tile is done
         if (it >= kQS &&
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ----------------------------------------------------- tcgen05 issuer --
-    if (lane == 0 && n_q > 0) {
+    if (lane == 0 && n_it > 0) {
       constexpr uint32_t kIdT = idesc_f16_f32(kTileN, kTileM, false, false, F16);  // S^T, dP^T
       const uint32_t k_addr = smem_u32(s.k()), v_addr = smem_u32(s.v());
       const int nk = d_steps(g);
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 10) {
     // ------------------------------------------------- dV / dK issuer --
-    if (lane == 0 && n_q > 0) {
+    if (lane == 0 && n_it > 0) {
       constexpr uint32_t kIdKV = idesc_f16_f32(kTileN, D, false, true, F16);  // A = P^T / dS^T in TMEM
       for (int it = 0; it < n_it; ++it) {
         const int st = it & 1, qs = it % kQS;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int qlo = 0, qhi = sq.q_len - 1;
     if (g.sparse_mode == 4) {
       qlo = max(qlo, j - g.next);
-      qhi = min(qhi, j + g.pre);
+      if (j >= g.sinks) qhi = min(qhi, j + g.pre);
     }
     if (j >= sq.kv_len) {
       qlo = 1;
@@ -461,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // read (row r's four words, as the producer fills them from a mask).
     auto gen_tile_bits = [&](int it2) {
       const int stage = it2 & 1;
-      const int qn = w.n * g.group + it2 / n_q;
-      const int row_i = (q_t0 + it2 % n_q) * kTileM + r;
+      const int qn = w.n * g.group + (it0 + it2) / n_q;
+      const int row_i = (q_t0 + (it0 + it2) % n_q) * kTileM + r;
       uint32_t words[2];
       gen_keep_words<2>(g, stat_index(g, sq, w.b, qn, row_i), (j0 + cbase) >> 4, words);
       if constexpr (DROP) {
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (DM == 2 && n_it > 0) gen_tile_bits(0);
     for (int it = 0; ok && it < n_it; ++it) {
       const int st = it & 1;
-      const int i0 = (q_t0 + it % n_q) * kTileM;
+      const int i0 = (q_t0 + (it0 + it) % n_q) * kTileM;
       const bool full = tile_fully_visible(g, sq, i0, j0);
       const uint32_t col = tmem + lane_off + region(it) + cbase;
       if (!compute_wait(&bar[kBarSFull + region_of<kR>(it)], region_phase<kR>(it), a.err)) { ok = false; break; }
@@ -619,11 +626,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before_sync();
       mbar_arrive(&bar[kBarDsFull + region_of<kR>(it)]);
     }
-    if (ok && n_q > 0) ok = compute_wait(&bar[kBarMmaDone], 0, a.err);  // every MMA done
+    if (ok && n_it > 0) ok = compute_wait(&bar[kBarMmaDone], 0, a.err);  // every MMA done
     // The eight compute warps agree on whether to write the epilogue: its
     // staging barrier below must see all eight or none.
     ok = named_barrier_and(1, kComputeThreads, ok);
-    if (ok) {
+    if (ok && w.pieces > 1) {
+      // a piece: fp32 rows for the join (one without steps has none)
+      tc_fence_after_sync();
+      if (n_it > 0) {
+        const float mul = h == 0 ? g.inv_keep : g.scale * g.inv_keep;
+        float* dst = a.part + (((a.part_base + blockIdx.x) * 2 + h) * kTileN + r) * D;
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t t32[32];
+          tmem_ld_32x32b_x32(tmem + lane_off + (h == 0 ? kColDV : kColDK) + ch * 32, t32);
+          tmem_ld_wait(t32);
+#pragma unroll
+          for (int t = 0; t < 32; t += 4)
+            *reinterpret_cast<float4*>(dst + ch * 32 + t) =
+                make_float4(__uint_as_float(t32[t]) * mul, __uint_as_float(t32[t + 1]) * mul,
+                            __uint_as_float(t32[t + 2]) * mul, __uint_as_float(t32[t + 3]) * mul);
+        }
+      }
+    } else if (ok) {
       tc_fence_after_sync();
       // epilogue: thread r owns key row j0 + r; warps 0-3 write dV, 4-7 dK
       const bool kv_valid = j < sq.kv_len;
@@ -638,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ch = 0; ch < D / 32; ++ch) {
         if (ch * 32 >= g.D) break;  // columns past D are padding
         float o[32];
-        if (n_q > 0) {
+        if (n_it > 0) {
           uint32_t t32[32];
           tmem_ld_32x32b_x32(tmem + lane_off + dcol + ch * 32, t32);
           tmem_ld_wait(t32);
@@ -685,6 +710,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// dK and dV of the key tiles whose steps were cut into pieces: the pieces'
+// fp32 rows, summed in their order.  The CTA of piece x takes every pieces-th
+// row from x on; a few MB, read once, behind a pass of milliseconds.
+constexpr int kJoinThreads = 256;
+template <int D, bool F16, int CAP>
+__global__ void __launch_bounds__(kJoinThreads)
+    swa_bwd_join_kernel(const BwdArgs a, const __grid_constant__ SeqTable<CAP> tab) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Geometry& g = a.g;
+  const Item w = resolve_item(tab, g, static_cast<int>(blockIdx.x), g.N_kv);
+  int q_t0, n_q;
+  query_tiles_of_key_tile(g, w.s, w.tile, &q_t0, &n_q);
+  const int n_it = g.group * n_q, per = steps_per_piece(n_it, w.pieces);
+  const int live = n_it > 0 ? (n_it + per - 1) / per : 0;  // pieces with steps
+  const float* part = a.part + (a.part_base + blockIdx.x - w.piece) * 2 * kTileN * D;
+  constexpr int kChunks = D / 8;
+  const int n_rows = min(kTileN, w.s.kv_len - w.tile * kTileN);
+  const int mine = n_rows > w.piece ? (n_rows - w.piece + w.pieces - 1) / w.pieces : 0;  // rows of this CTA
+  for (int x = threadIdx.x; x < 2 * mine * kChunks; x += kJoinThreads) {
+    const int c = x % kChunks, y = x / kChunks;
+    const int h = y & 1, r = w.piece + (y >> 1) * w.pieces;
+    if (c * 8 >= g.D) continue;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < live; ++p) {
+      const float4* src = reinterpret_cast<const float4*>(part + ((p * 2 + h) * kTileN + r) * D + c * 8);
+      const float4 u = src[0], v = src[1];
+      o[0] += u.x; o[1] += u.y; o[2] += u.z; o[3] += u.w;
+      o[4] += v.x; o[5] += v.y; o[6] += v.z; o[7] += v.w;
+    }
+    const int64_t e = kv_elem(g, w.s, w.b, w.n, w.tile * kTileN + r) + c * 8;
+    if (in_bounds(e, 8, g.n_kv_elems, a.err)) store8<F16>(h == 0 ? a.dv : a.dk, e, o, g.out_f32);
+  }
+}
+
 template <int D, int DM, bool F16, int CAP>
 cudaError_t launch_dkv_t(const BwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq, const CUtensorMap& mk,
                          const CUtensorMap& mv, const CUtensorMap& mdy, cudaStream_t stream) {
@@ -720,6 +781,15 @@ cudaError_t launch_backward_dkv(const BwdArgs& a, const SeqTable<CAP>& tab, cons
   }
 }
 
+template <int CAP>
+cudaError_t launch_backward_join(const BwdArgs& a, const SeqTable<CAP>& tab, int n_pieces, cudaStream_t stream) {
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(n_pieces), dim3(kJoinThreads), 0, stream, a, tab); };
+  if (a.g.D <= 64) return a.g.f16 ? go(swa_bwd_join_kernel<64, true, CAP>) : go(swa_bwd_join_kernel<64, false, CAP>);
+  return a.g.f16 ? go(swa_bwd_join_kernel<128, true, CAP>) : go(swa_bwd_join_kernel<128, false, CAP>);
+}
+
+template cudaError_t launch_backward_join<kSmallTable>(const BwdArgs&, const SeqTable<kSmallTable>&, int, cudaStream_t);
+template cudaError_t launch_backward_join<kLargeTable>(const BwdArgs&, const SeqTable<kLargeTable>&, int, cudaStream_t);
 template cudaError_t launch_backward_dkv<kSmallTable>(const BwdArgs&, const SeqTable<kSmallTable>&,
                                                       const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                                       const CUtensorMap&, cudaStream_t);

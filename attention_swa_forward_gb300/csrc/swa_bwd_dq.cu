@@ -80,6 +80,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // key tiles touched by this query tile
   int kv_t0, n_kv;
   key_tiles_of_query_tile(g, sq, w.tile, &kv_t0, &n_kv);
+  // step j is sink tile j, then the window's run
+  const int n_sink = sink_tiles_before(g, sq, w.tile, kv_t0);
+  n_kv += n_sink;
+  kv_t0 -= n_sink;
+  auto key_tile = [&](int j) { return j < n_sink ? j : kv_t0 + j; };
 
   // The producer's lane initialises the barriers and issues the loads of Q,
   // dY and the first K and V tiles before the CTA-wide barrier, so their
@@ -116,9 +121,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_rows<D>(s.q, &mq, &s.qdy_full, g, w.b, w.n, sq.q_start, q0);
       tma_rows<D>(s.dy, &mdy, &s.qdy_full, g, w.b, w.n, sq.q_start, q0);
       mbar_arrive_expect_tx(&s.k_full[0], kTileBytes);
-      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, kv_t0 * kTileN);
+      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, key_tile(0) * kTileN);
       mbar_arrive_expect_tx(&s.v_full[0], kTileBytes);
-      tma_rows<D>(s.v[0], &mv, &s.v_full[0], g, w.b, hk, sq.kv_start, kv_t0 * kTileN);
+      tma_rows<D>(s.v[0], &mv, &s.v_full[0], g, w.b, hk, sq.kv_start, key_tile(0) * kTileN);
     }
   }
   if (warp == 9) {
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && n_kv > 0) {
       int k_issued = 1, v_issued = 1;  // Q, dY, K(0) and V(0) went out before the CTA-wide barrier
       for (int j = 1; j < n_kv; ++j) {
-        const int jr = (kv_t0 + j) * kTileN;
+        const int jr = key_tile(j) * kTileN;
         const int kb = j % 3, vb = j & 1;
         // K(j) reuses the stage of K(j-3), free once dQ(j-3) is done
         if (j >= 3 && !mbar_wait(&s.k_empty[kb], ((j / 3) - 1) & 1, a.err, kErrBwdLoad)) break;
@@ -250,12 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       kb0 = kb1 = 0xFFFFFFFFu;
       if (DM == 1 && row_valid) {
         uint32_t bits[4];
-        load_keep_bits(a.mask, sq, w.n, i, (kv_t0 + j) * kTileN, bits, g.n_mask_bytes, a.err);
+        load_keep_bits(a.mask, sq, w.n, i, key_tile(j) * kTileN, bits, g.n_mask_bytes, a.err);
         kb0 = h ? bits[2] : bits[0];
         kb1 = h ? bits[3] : bits[1];
       } else if (DM == 2) {
         uint32_t bits[2];
-        gen_keep_words<2>(g, stat_index(g, sq, w.b, w.n, i), ((kv_t0 + j) * kTileN + cbase) >> 4, bits);
+        gen_keep_words<2>(g, stat_index(g, sq, w.b, w.n, i), (key_tile(j) * kTileN + cbase) >> 4, bits);
         kb0 = bits[0];
         kb1 = bits[1];
       }
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t u = (j >> 1) & 1;
       const uint32_t kb0 = n_kb0, kb1 = n_kb1;
       if (DM != 0 && j + 1 < n_kv) fetch_bits(j + 1, n_kb0, n_kb1);
-      const int jb = (kv_t0 + j) * kTileN;
+      const int jb = key_tile(j) * kTileN;
       const bool full = tile_fully_visible(g, sq, q0, jb);
 
       // ---- S -> P (kept in registers)
@@ -300,11 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[t + 1] = ex2_approx(x1);
           }
         } else {
-          const int lo_t = wlo - (jb + cbase), hi_t = whi - (jb + cbase);  // visible t in [lo_t, hi_t]
+          const int lo_t = wlo - (jb + cbase), hi_t = whi - (jb + cbase);  // visible t in [lo_t, hi_t],
+          const int sink_t = g.sinks - (jb + cbase);                       // and sinks
 #pragma unroll
           for (int t = 0; t < 64; ++t) {
             const float e = ex2_approx(__uint_as_float(t < 32 ? s0[t] : s1[t - 32]) * c - lse2);
-            p[t] = ((t >= lo_t) & (t <= hi_t)) ? e : 0.f;
+            p[t] = (((t >= lo_t) | (t < sink_t)) & (t <= hi_t)) ? e : 0.f;
           }
         }
       }

@@ -60,7 +60,7 @@ __device__ __forceinline__ int64_t ws_stat_index(const Geometry& g, const SeqInf
                        : static_cast<int64_t>(n) * g.T_q + (s.q_start + i);
 }
 
-// Keys visible to local query row i: [lo, hi] (empty when lo > hi).
+// Keys visible to local query row i: [lo, hi] (empty when lo > hi), and the sinks up to hi.
 // sparse_mode 4 (BAND): i - pre <= j <= i + next; rows past the sequence see nothing.
 __device__ __forceinline__ void key_window(const Geometry& g, const SeqInfo& s, int i, int& lo, int& hi) {
   lo = 0;
@@ -70,8 +70,8 @@ __device__ __forceinline__ void key_window(const Geometry& g, const SeqInfo& s, 
     hi = min(hi, i + g.next);
   }
   if (i >= s.q_len) {
-    lo = 1;
-    hi = 0;
+    lo = 0;
+    hi = -1;
   }
 }
 
@@ -84,7 +84,7 @@ __device__ __forceinline__ int d_steps(const Geometry& g) { return (g.D + 15) >>
 __device__ __forceinline__ bool tile_fully_visible(const Geometry& g, const SeqInfo& s, int q0, int j0) {
   if (q0 + 127 >= s.q_len || j0 + 127 >= s.kv_len) return false;
   if (g.sparse_mode != 4) return true;
-  return j0 >= q0 + 127 - g.pre && j0 + 127 <= q0 + g.next;
+  return (j0 >= q0 + 127 - g.pre || j0 + 127 < g.sinks) && j0 + 127 <= q0 + g.next;
 }
 
 // TMA load of 128 rows x D columns starting at local row `row0` of (b, n) into

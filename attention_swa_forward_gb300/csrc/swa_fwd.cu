@@ -70,6 +70,11 @@ __global__ void __launch_bounds__(224, 1)
   // key tiles touched by this query tile
   int kv_t0, n_kv;
   key_tiles_of_query_tile(g, sq, w.tile, &kv_t0, &n_kv);
+  // step it is sink tile it, then the window's run
+  const int n_sink = sink_tiles_before(g, sq, w.tile, kv_t0);
+  n_kv += n_sink;
+  kv_t0 -= n_sink;
+  auto key_tile = [&](int it) { return it < n_sink ? it : kv_t0 + it; };
 
   // The producer's lane initialises the barriers and issues the loads of Q
   // and the first K tile before the CTA-wide barrier, so their latency runs
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(224, 1)
       mbar_arrive_expect_tx(&s.q_full, kTileBytes);
       tma_rows<D>(s.q, &mq, &s.q_full, g, w.b, w.n, sq.q_start, q0);
       mbar_arrive_expect_tx(&s.k_full[0], kTileBytes);
-      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, kv_t0 * kTileN);
+      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, key_tile(0) * kTileN);
     }
   }
   if (warp == 5) {
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(224, 1)
       for (int it = 0; it < n_kv; ++it) {
         const int st = it % kStages;
         const uint32_t use = it / kStages;
-        const int j0 = (kv_t0 + it) * kTileN;
+        const int j0 = key_tile(it) * kTileN;
         if (it > 0) {
           if (it >= kStages && !mbar_wait(&s.k_empty[st], (use - 1) & 1, a.err, kErrFwdLoad)) break;
           mbar_arrive_expect_tx(&s.k_full[st], kTileBytes);
@@ -204,14 +209,14 @@ __global__ void __launch_bounds__(224, 1)
     // Keep bits read from the mask are fetched one tile ahead, so their
     // global-load latency is not on the softmax's path.
     uint32_t next_bits[4] = {0u, 0u, 0u, 0u};
-    if (DM == 1 && n_kv > 0 && row_valid) load_keep_bits(a.mask, sq, w.n, i, kv_t0 * kTileN, next_bits, g.n_mask_bytes, a.err);
+    if (DM == 1 && n_kv > 0 && row_valid) load_keep_bits(a.mask, sq, w.n, i, key_tile(0) * kTileN, next_bits, g.n_mask_bytes, a.err);
     for (int it = 0; ok && it < n_kv; ++it) {
       const int sb = it & 1;
       uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
       if (DM == 1) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) bits[u] = next_bits[u];
-        if (it + 1 < n_kv && row_valid) load_keep_bits(a.mask, sq, w.n, i, (kv_t0 + it + 1) * kTileN, next_bits, g.n_mask_bytes, a.err);
+        if (it + 1 < n_kv && row_valid) load_keep_bits(a.mask, sq, w.n, i, key_tile(it + 1) * kTileN, next_bits, g.n_mask_bytes, a.err);
       }
       // warp-uniform outcome: the tcgen05.ld below is warp-collective
       if (!s_ready && !__all_sync(0xFFFFFFFFu, mbar_wait(&s.s_full[sb], (it >> 1) & 1, a.err, kErrFwdSoftmax))) {
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(224, 1)
       const bool p_free = it < 2 || mbar_test(&s.o_done[sb], ((it >> 1) - 1) & 1);
       auto X = [&](int t) -> float { return __uint_as_float(xr[t]); };
 
-      const int j0 = (kv_t0 + it) * kTileN;
+      const int j0 = key_tile(it) * kTileN;
       // With a positive scale the maximum is taken on the raw scores and the
       // scale folds into one packed FMA per pair, p = exp2(x*c - m); keys
       // outside the window (partial tiles only) become -inf first, and
@@ -259,10 +264,10 @@ __global__ void __launch_bounds__(224, 1)
 #pragma unroll
           for (int t = 0; t < kTileN; t += 2) m8[(t >> 1) & 7] = fmax3(m8[(t >> 1) & 7], X(t), X(t + 1));
         } else {
-          const int lo_t = wlo - j0, hi_t = whi - j0;  // visible t in [lo_t, hi_t]
+          const int lo_t = wlo - j0, hi_t = whi - j0, sink_t = g.sinks - j0;  // visible t in [lo_t, hi_t], and sinks
 #pragma unroll
           for (int t = 0; t < kTileN; ++t) {
-            const bool vis = (t >= lo_t) & (t <= hi_t);
+            const bool vis = ((t >= lo_t) | (t < sink_t)) & (t <= hi_t);
             const float v = vis ? (fold ? X(t) : X(t) * c) : -INFINITY;  // selects, not branches
             xr[t] = __float_as_uint(v);
             m8[t & 7] = fmaxf(m8[t & 7], v);

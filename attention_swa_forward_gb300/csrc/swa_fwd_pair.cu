@@ -52,13 +52,17 @@ constexpr float kPairLn2 = 0.6931471805599453f;
 // Rescale O only when the running max grows by more than 2^8 (log2 units).
 constexpr float kPairRescale = 8.0f;
 
-// The key tiles [t0, t0 + n) of query tile qt, or none if the tile does not exist.
+// The key tiles [t0, t0 + n) of query tile qt and its sink tiles [0, sinks)
+// before them, or none if the tile does not exist.
 struct HalfRange {
-  int t0, n;
+  int t0, n, sinks;
 };
 __device__ __forceinline__ HalfRange half_range(const Geometry& g, const SeqInfo& s, int qt) {
-  HalfRange r{0, 0};
-  if (qt * kTileM < s.q_len) key_tiles_of_query_tile(g, s, qt, &r.t0, &r.n);
+  HalfRange r{0, 0, 0};
+  if (qt * kTileM < s.q_len) {
+    key_tiles_of_query_tile(g, s, qt, &r.t0, &r.n);
+    r.sinks = sink_tiles_before(g, s, qt, r.t0);
+  }
   return r;
 }
 
@@ -84,12 +88,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const SeqInfo sq = w.s;
   const HalfRange ra = half_range(g, sq, 2 * w.tile), rb = half_range(g, sq, 2 * w.tile + 1);
   const bool has_b = (2 * w.tile + 1) * kTileM < sq.q_len;
-  // the key tiles either half visits: [u0, u0 + n_u)
+  // the key tiles either half visits: the sink tiles before [u0, u0 + n_u), and those
   int u0, n_u;
   key_tiles_of_query_pair(g, sq, w.tile, &u0, &n_u);
+  const int u_sink = min(max(ra.sinks, rb.sinks), u0);
+  u0 -= u_sink;
+  n_u += u_sink;
+  auto union_tile = [&](int it) { return it < u_sink ? it : u0 + it; };
   auto uses = [&](int h, int j) {
     const HalfRange& r = h ? rb : ra;
-    return j >= r.t0 && j < r.t0 + r.n;
+    return (j >= r.t0 || j < r.sinks) && j < r.t0 + r.n;
   };
 
   // The producer's lane initialises the barriers and issues the loads of
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tma_rows<D>(s.q[0], &mq, &s.q_full, g, w.b, w.n, sq.q_start, 2 * w.tile * kTileM);
       if (has_b) tma_rows<D>(s.q[1], &mq, &s.q_full, g, w.b, w.n, sq.q_start, (2 * w.tile + 1) * kTileM);
       mbar_arrive_expect_tx(&s.k_full[0], kTileBytes);
-      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, u0 * kTileN);
+      tma_rows<D>(s.k[0], &mk, &s.k_full[0], g, w.b, hk, sq.kv_start, union_tile(0) * kTileN);
     }
   }
   if (warp == 9) {
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int it = 0; it < n_u; ++it) {
         const int st = it % kPairStages;
         const uint32_t use = it / kPairStages;
-        const int j0 = (u0 + it) * kTileN;
+        const int j0 = union_tile(it) * kTileN;
         if (it > 0) {
           if (it >= kPairStages && !mbar_wait(&s.k_empty[st], (use - 1) & 1, a.err, kErrFwdLoad)) break;
           mbar_arrive_expect_tx(&s.k_full[st], kTileBytes);
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int issued[2] = {0, 0};  // S tiles issued per half
       bool ok = mbar_wait(&s.q_full, 0, a.err, kErrFwdMma);
       for (int it = 0; ok && it < n_u; ++it) {
-        const int st = it % kPairStages, j = u0 + it;
+        const int st = it % kPairStages, j = union_tile(it);
         if (!mbar_wait(&s.k_full[st], (it / kPairStages) & 1, a.err, kErrFwdMma)) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int issued[2] = {0, 0};  // PV tiles issued per half
       bool ok = true;
       for (int it = 0; ok && it < n_u; ++it) {
-        const int st = it % kPairStages, j = u0 + it;
+        const int st = it % kPairStages, j = union_tile(it);
         if (!mbar_wait(&s.v_full[st], (it / kPairStages) & 1, a.err, kErrFwdMma)) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -233,7 +241,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------------------------- softmax + epilogue of one half --
     const int h = warp >> 2;  // 0: half A, 1: half B
     const HalfRange rh = h ? rb : ra;
-    const int n_kv = rh.n, kv_t0 = rh.t0;
+    const int n_kv = rh.sinks + rh.n, kv_t0 = rh.t0 - rh.sinks;
+    auto key_tile = [&](int it) { return it < rh.sinks ? it : kv_t0 + it; };
     const int q0 = (2 * w.tile + h) * kTileM;
     const int r = (warp & 3) * 32 + lane;  // TMEM lane == row of the half's tile
     const int i = q0 + r;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
       if (DM == 1) {
         bits[0] = bits[1] = bits[2] = bits[3] = 0u;
-        if (row_valid) load_keep_bits(a.mask, sq, w.n, i, (kv_t0 + it) * kTileN, bits, g.n_mask_bytes, a.err);
+        if (row_valid) load_keep_bits(a.mask, sq, w.n, i, key_tile(it) * kTileN, bits, g.n_mask_bytes, a.err);
       }
       // warp-uniform outcome: the tcgen05.ld below is warp-collective
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s.s_full[h], it & 1, a.err, kErrFwdSoftmax))) {
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const bool pv_done = it < 1 || mbar_test(&s.o_done[h], (it - 1) & 1);
       auto X = [&](int t) -> float { return __uint_as_float(xr[t]); };
 
-      const int j0 = (kv_t0 + it) * kTileN;
+      const int j0 = key_tile(it) * kTileN;
       // Positive scale: maximum on the raw scores, the scale folded into one
       // packed FMA per pair, p = exp2(x*c - m); keys outside the window
       // (partial tiles only) become -inf first.  A scale <= 0 takes scale,
@@ -305,10 +314,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int t = 0; t < kTileN; t += 2) m8[(t >> 1) & 7] = fmax3(m8[(t >> 1) & 7], X(t), X(t + 1));
         } else {
-          const int lo_t = wlo - j0, hi_t = whi - j0;  // visible t in [lo_t, hi_t]
+          const int lo_t = wlo - j0, hi_t = whi - j0, sink_t = g.sinks - j0;  // visible t in [lo_t, hi_t], and sinks
 #pragma unroll
           for (int t = 0; t < kTileN; ++t) {
-            const bool vis = (t >= lo_t) & (t <= hi_t);
+            const bool vis = ((t >= lo_t) | (t < sink_t)) & (t <= hi_t);
             const float v = vis ? (fold ? X(t) : X(t) * c) : -INFINITY;  // selects, not branches
             xr[t] = __float_as_uint(v);
             m8[t & 7] = fmaxf(m8[t & 7], v);

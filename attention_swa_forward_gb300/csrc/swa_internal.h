@@ -42,7 +42,8 @@ struct SeqDesc {
   int32_t tiles;       // 128-row tiles per head
   int32_t heads;       // N (TND) or B*N (BNSD)
   int32_t descending;
-  int32_t pad;
+  uint16_t pieces;     // > 1 (key-major pass): the entry's tiles are split into this many runs of steps each
+  uint16_t tile0;      // first tile of the entry
 };
 static_assert(sizeof(SeqDesc) == 48, "SeqDesc layout");
 
@@ -109,6 +110,7 @@ struct Geometry {
   int32_t S_q, S_kv;  // BNSD (per-batch lengths)
   int32_t sparse_mode;
   int32_t pre, next;  // clamped into +-(max sequence length + 1)
+  int32_t sinks;      // BAND: keys below this one stay visible behind the window (0 without BAND)
   float scale;        // score scale
   float scale_log2;   // scale * log2(e)
   float inv_keep;     // 1 / keep_prob
@@ -151,6 +153,9 @@ struct BwdArgs {
   void* dk;   // written by the key-major pass
   void* dv;
   int32_t* err;
+  // key-major pass, key tiles with sinks: the pieces' dK and dV, [piece][dV, dK][128][64 or 128 columns]
+  float* part;
+  int64_t part_base;  // pieces of the launches before this one
 };
 
 struct PrepArgs {
@@ -199,6 +204,9 @@ template <int CAP>
 cudaError_t launch_backward_dq(const BwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq,
                                const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdy,
                                cudaStream_t stream);
+// Sum the pieces of the launch's first `n_pieces` items, which hold every entry with pieces > 1.
+template <int CAP>
+cudaError_t launch_backward_join(const BwdArgs& a, const SeqTable<CAP>& tab, int n_pieces, cudaStream_t stream);
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream);
 // fp32 -> bf16 (round to nearest even) of n elements, n a multiple of 8, both 16-byte aligned.
 cudaError_t launch_to_bf16(const float* in, __nv_bfloat16* out, int64_t n, cudaStream_t stream);

@@ -25,6 +25,7 @@ namespace swa {
 // geometry of its sequence.
 struct Item {
   int b, n, tile;
+  int piece, pieces;  // key-major pass: run `piece` of `pieces` of the tile's steps
   SeqInfo s;
 };
 
@@ -39,11 +40,18 @@ SWA_HD Item resolve_item(const SeqTable<CAP>& tab, const Geometry& g, int k, int
     if (tab.d[mid].item_begin <= k) lo = mid; else hi = mid - 1;
   }
   const SeqDesc& d = tab.d[lo];
-  const int local = k - d.item_begin;
+  int local = k - d.item_begin;
+  Item it;
+  it.pieces = d.pieces;
+  it.piece = 0;
+  if (d.pieces > 1) {
+    const int whole = local / d.pieces;
+    it.piece = local - whole * d.pieces;
+    local = whole;
+  }
   const int h = local / d.tiles;  // head by head: the CTAs in flight share a head's tiles in L2
   const int rank = local - h * d.tiles;
-  Item it;
-  it.tile = d.descending ? d.tiles - 1 - rank : rank;
+  it.tile = d.tile0 + (d.descending ? d.tiles - 1 - rank : rank);
   if (d.b < 0) {
     it.b = h / nh;
     it.n = h - it.b * nh;
@@ -60,7 +68,17 @@ SWA_HD Item resolve_item(const SeqTable<CAP>& tab, const Geometry& g, int k, int
   return it;
 }
 
-// Key tiles [*t0, *t0 + *n) that query tile `tile` of sequence s touches.
+// Key tiles that hold a sink (a key below g.sinks) which query row q_last sees.
+SWA_HD int sink_tiles(const Geometry& g, const SeqInfo& s, int q_last) {
+  int hi = g.sinks - 1;
+  hi = q_last + g.next < hi ? q_last + g.next : hi;
+  hi = s.kv_len - 1 < hi ? s.kv_len - 1 : hi;
+  return hi >= 0 ? hi / kTileN + 1 : 0;
+}
+
+// Key tiles [*t0, *t0 + *n) that query tile `tile` of sequence s touches; the
+// sink tiles are among them where they reach the window's run, else before it
+// (sink_tiles_before).
 SWA_HD void key_tiles_of_query_tile(const Geometry& g, const SeqInfo& s, int tile, int* t0, int* n) {
   const int q0 = tile * kTileM;
   const int q_last = q0 + kTileM - 1 < s.q_len - 1 ? q0 + kTileM - 1 : s.q_len - 1;
@@ -75,6 +93,21 @@ SWA_HD void key_tiles_of_query_tile(const Geometry& g, const SeqInfo& s, int til
     *t0 = lo / kTileN;
     *n = hi / kTileN - *t0 + 1;
   }
+  if (g.sinks > 0) {
+    const int sinks = sink_tiles(g, s, q_last);
+    if (sinks >= *t0) {
+      *n = *t0 + *n > sinks ? *t0 + *n : sinks;
+      *t0 = 0;
+    }
+  }
+}
+
+// Sink tiles [0, .) that query tile `tile` touches before its run, which begins at t0.
+SWA_HD int sink_tiles_before(const Geometry& g, const SeqInfo& s, int tile, int t0) {
+  if (g.sinks <= 0) return 0;
+  const int q0 = tile * kTileM;
+  const int sinks = sink_tiles(g, s, q0 + kTileM - 1 < s.q_len - 1 ? q0 + kTileM - 1 : s.q_len - 1);
+  return sinks < t0 ? sinks : 0;
 }
 
 // Key tiles [*u0, *u0 + *n) that query tiles 2p and 2p + 1 of sequence s
@@ -100,14 +133,14 @@ SWA_HD void key_tiles_of_query_pair(const Geometry& g, const SeqInfo& s, int p, 
 }
 
 // Query tiles [*t0, *t0 + *n) that see key tile `tile` of sequence s:
-// i - pre <= j <= i + next  <=>  j - next <= i <= j + pre.
+// i - pre <= j <= i + next  <=>  j - next <= i <= j + pre; a sink is seen by every i >= j - next.
 SWA_HD void query_tiles_of_key_tile(const Geometry& g, const SeqInfo& s, int tile, int* t0, int* n) {
   const int j0 = tile * kTileN;
   const int j_last = j0 + kTileN - 1 < s.kv_len - 1 ? j0 + kTileN - 1 : s.kv_len - 1;
   int lo = 0, hi = s.q_len - 1;
   if (g.sparse_mode == 4) {
     lo = j0 - g.next > lo ? j0 - g.next : lo;
-    hi = j_last + g.pre < hi ? j_last + g.pre : hi;
+    if (j0 >= g.sinks) hi = j_last + g.pre < hi ? j_last + g.pre : hi;
   }
   *t0 = 0;
   *n = 0;
@@ -116,5 +149,8 @@ SWA_HD void query_tiles_of_key_tile(const Geometry& g, const SeqInfo& s, int til
     *n = hi / kTileM - *t0 + 1;
   }
 }
+
+// Steps of each piece but the last of a key tile's n_it steps.
+SWA_HD int steps_per_piece(int n_it, int pieces) { return n_it > 0 ? (n_it + pieces - 1) / pieces : 1; }
 
 }  // namespace swa

@@ -62,6 +62,7 @@ class SwaParams(ctypes.Structure):
         ("dropout_seed", ctypes.c_uint64),
         ("dropout_offset", ctypes.c_uint64),
         ("dtype", ctypes.c_int32),
+        ("sink_tokens", ctypes.c_int64),
     ]
 
 
@@ -281,6 +282,7 @@ class Params:
         c.dropout_seed = int(getattr(geom, "dropout_seed", 0) or 0) & (2**64 - 1)
         c.dropout_offset = int(getattr(geom, "dropout_offset", 0) or 0) & (2**64 - 1)
         c.dtype = DTYPES[getattr(geom, "dtype", "bf16") or "bf16"]
+        c.sink_tokens = int(getattr(geom, "sink_tokens", 0) or 0)
 
     def ref(self):
         return ctypes.byref(self.c)

@@ -44,6 +44,7 @@ class Geometry:
     dropout_seed: int = 0
     dropout_offset: int = 0
     dtype: str = "bf16"  # element type of q, k, v, dy (and of out and the gradients): "bf16" or "fp16"
+    sink_tokens: int = 0  # BAND: keys of a sequence's start that stay visible behind the window
 
     def as_dict(self) -> dict:
         return asdict(self)

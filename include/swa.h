@@ -20,6 +20,7 @@
  *   0  no mask: query i sees every key of its sequence;
  *   4  BAND: query i sees key j iff  i - pre_tokens <= j <= i + next_tokens
  *      (indices local to the sequence, top-left aligned when Sq != Skv).
+ * With sink_tokens the first keys of a sequence stay visible behind the window.
  * A query row that sees no key gets out = 0, softmax_max = -inf,
  * softmax_sum = 0 and a zero dq row; it contributes nothing to dk / dv.
  *
@@ -133,6 +134,10 @@ typedef struct {
                                    (rounded to nearest even, made in the workspace), every
                                    accumulation is fp32 as for the other types, and the
                                    outputs are stored in fp32 */
+  int64_t sink_tokens;          /* BAND: the first sink_tokens keys of a sequence stay visible behind
+                                   the window: query i sees key j iff j <= i + next_tokens and
+                                   (j >= i - pre_tokens or j < sink_tokens).  Default 0; no effect
+                                   without BAND (an addition of this library) */
 } swa_params_t;
 
 typedef enum { SWA_DTYPE_BF16 = 0, SWA_DTYPE_FP16 = 1, SWA_DTYPE_FP32 = 2 } swa_dtype_t;
@@ -165,7 +170,9 @@ SWA_API swa_status_t swa_forward(const swa_params_t *p, const void *q, const voi
 /* Device workspace bytes that swa_backward needs: a status word, and per
  * query row D = rowsum(dY*O) and the log2-sum-exp of the forward statistics
  * (8 bytes per query row and head); with fp32 inputs also bf16 copies of q,
- * k, v, dy and out. */
+ * k, v, dy and out; with sink_tokens also fp32 partial dk and dv rows of the
+ * 128-key tiles that hold sinks, whose queries are split over several CTAs
+ * (64 KB at D <= 64, else 128 KB, per CTA; the sums have a fixed order). */
 SWA_API swa_status_t swa_backward_workspace_size(const swa_params_t *p, size_t *bytes);
 
 /* Backward (PyPTO-Gym "反向公式"; aclnnFlashAttentionUnpaddingScoreGradV2
@@ -493,7 +500,10 @@ SWA_API void swa_set_timing_events(void *const *events);
  *            from the first start to the last end of the two tiles' runs
  *   items    host, 6 int32 per item in launch order: launch index, batch,
  *            head, tile, first partner tile, partner tile count; at most
- *            `capacity` items are written (items may be NULL to count)
+ *            `capacity` items are written (items may be NULL to count).
+ *            With sink_tokens, an item that also visits sink tiles before its
+ *            run has a row for those, before the run's; a key tile whose steps
+ *            are split over several CTAs (pass 1) has its row once per CTA
  *   count    host, receives the number of items
  * Errors: the size query's, SWA_ERR_PARAM_NULLPTR (count), and
  * SWA_ERR_PARAM_INVALID (pass).

@@ -106,6 +106,7 @@ class Problem:
     dropout_seed: int = 0
     dropout_offset: int = 0
     dtype: str = "bf16"  # the inputs' element type; the oracle reads their exact values in fp64
+    sink_tokens: int = 0  # not in the oracle: a problem with sinks is refused
 
     @property
     def n_kv(self) -> int:
@@ -171,6 +172,8 @@ class _Call:
             pr.keep_prob,
             pr.n_kv,
         )
+        if pr.sink_tokens:
+            raise ValueError("the oracle has no sinks")
         if pr.n_kv < 1 or pr.N % pr.n_kv:
             raise ValueError(f"N={pr.N} is not a multiple of N_kv={pr.n_kv}")
 
