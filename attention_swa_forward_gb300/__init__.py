@@ -6,4 +6,4 @@ hand-written CUDA behind a C ABI (include/swa.h).
 ``workloads`` draws seeded synthetic inputs; ``build`` compiles libswa.so.
 """
 from . import swa  # noqa: F401
-from .swa import SwaError, backward, forward, paged_append, paged_forward, rope, rope_backward  # noqa: F401
+from .swa import SwaError, backward, forward, paged_append, paged_forward, paged_gather, rope, rope_backward  # noqa: F401

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <optional>
 #include <sstream>
@@ -115,6 +116,33 @@ const int32_t* block_table(const at::Tensor& t, const swa_paged_params_t& p, int
     if (p.B > 1) *row = t.stride(0);
   }
   return static_cast<const int32_t*>(t.data_ptr());
+}
+
+at::ScalarType page_type(const swa_paged_params_t& p) {
+  return p.cache_dtype == SWA_CACHE_E4M3 ? at::kFloat8_e4m3fn : scalar_type(p.dtype);
+}
+// The exponents of an 8-bit cache, NULL for None (the library says which it wants).
+int8_t* exponents(PyObject* o, const char* name, const swa_paged_params_t& p, int device) {
+  const at::Tensor* t = tensor_or_none(o, name);
+  if (!t) return nullptr;
+  const int64_t shape[3] = {p.num_pages, p.N_kv ? p.N_kv : p.N, p.page_size};
+  expect_dense(*t, name, shape, at::kChar, device);
+  return static_cast<int8_t*>(t->data_ptr());
+}
+// The bits of a tree, [T_q, words], and the words between rows.
+const uint32_t* tree_rows(const at::Tensor& t, const swa_paged_params_t& p, int device, int64_t* row) {
+  int64_t longest = 0, last = 0;
+  for (int64_t b = 0; b < p.B; ++b) {
+    longest = std::max(longest, p.cu_seqlens_q[b] - last);
+    last = p.cu_seqlens_q[b];
+  }
+  const int64_t words = std::max<int64_t>((longest + 31) / 32, 1);
+  const int64_t shape[2] = {p.T_q, words};
+  if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != p.T_q || t.size(1) < words || !t.is_cuda() ||
+      t.get_device() != device || (t.stride(1) != 1 && t.size(1) > 1) || (t.stride(0) < t.size(1) && p.T_q > 1))
+    refuse(t, "tree", shape, at::kInt, device, " (rows contiguous and apart; more words may follow)");
+  *row = p.T_q > 1 ? t.stride(0) : t.size(1);
+  return static_cast<const uint32_t*>(t.data_ptr());
 }
 
 // [n_axes, rows], the rows in any shape; one axis may leave its dimension out.
@@ -224,10 +252,10 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // paged_append(fn, params, k, v, k_pages, v_pages, block_table, kv_lens, rope params or 0, positions, q, q_out,
-//              workspace, stream)
+//              workspace, stream, k_exponents, v_exponents)
 PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 14, [&]() -> swa_status_t {
-    const auto fn = address<decltype(&swa_paged_append)>(a[0], "entry point");
+  return guarded(n, 16, [&]() -> swa_status_t {
+    const auto fn = address<decltype(&swa_paged_append_ext)>(a[0], "entry point");
     const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1], "parameters");
     const auto* rope = address<const swa_rope_params_t*>(a[8], "rope");
     const at::Tensor& k = tensor(a[2], "k");
@@ -235,8 +263,10 @@ PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = scalar_type(p.dtype);
     const int64_t kv[3] = {p.T_q, p.N_kv ? p.N_kv : p.N, p.D}, qs[3] = {p.T_q, p.N, p.D}, lens[1] = {p.B};
     const Arg xk = arg(k, "k", kv, type, dev), xv = arg(tensor(a[3], "v"), "v", kv, type, dev);
-    const Pages kp = pages(tensor(a[4], "k_pages"), "k_pages", p, type, dev);
-    const Pages vp = pages(tensor(a[5], "v_pages"), "v_pages", p, type, dev);
+    const Pages kp = pages(tensor(a[4], "k_pages"), "k_pages", p, page_type(p), dev);
+    const Pages vp = pages(tensor(a[5], "v_pages"), "v_pages", p, page_type(p), dev);
+    int8_t* const ke = exponents(a[14], "k_exponents", p, dev);
+    int8_t* const ve = exponents(a[15], "v_exponents", p, dev);
     int64_t row;
     const int32_t* table = block_table(tensor(a[6], "block_table"), p, dev, &row);
     const at::Tensor& l = tensor(a[7], "kv_lens");
@@ -250,24 +280,34 @@ PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (qo) xo = arg(*qo, "q_out", qs, type, dev);
     const at::Tensor& ws = workspace(a[12], dev);
     const On on(dev, a[13]);
-    return unlocked(fn, &p, xk.ptr, xk.strides(), xv.ptr, xv.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table,
-                    row, static_cast<const int32_t*>(l.data_ptr()), rope, pp, xq.ptr, xq.strides(), xo.ptr, xo.strides(),
+    return unlocked(fn, &p, xk.ptr, xk.strides(), xv.ptr, xv.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), ke, ve,
+                    table, row, static_cast<const int32_t*>(l.data_ptr()), rope, pp, xq.ptr, xq.strides(), xo.ptr, xo.strides(),
                     ws.data_ptr(), ws.nbytes(), on.stream);
   });
 }
 
-// paged_forward(fn, params, q, k_pages, v_pages, block_table, kv_lens, out, softmax_max, softmax_sum, workspace, stream)
+// paged_forward(fn, params, q, k_pages, v_pages, block_table, kv_lens, out, softmax_max, softmax_sum, workspace, stream,
+//               k_exponents, v_exponents, tree, depth)
 PyObject* bind_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&]() -> swa_status_t {
-    const auto fn = address<decltype(&swa_paged_forward)>(a[0], "entry point");
+  return guarded(n, 16, [&]() -> swa_status_t {
+    const auto fn = address<decltype(&swa_paged_forward_ext)>(a[0], "entry point");
     const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1], "parameters");
     const at::Tensor& q = tensor(a[2], "q");
     const int dev = device_of(q);
     const at::ScalarType type = scalar_type(p.dtype);
     const int64_t qs[3] = {p.T_q, p.N, p.D}, stats[2] = {p.T_q, p.N}, lens[1] = {p.B};
     const Arg xq = arg(q, "q", qs, type, dev);
-    const Pages kp = pages(tensor(a[3], "k_pages"), "k_pages", p, type, dev);
-    const Pages vp = pages(tensor(a[4], "v_pages"), "v_pages", p, type, dev);
+    const Pages kp = pages(tensor(a[3], "k_pages"), "k_pages", p, page_type(p), dev);
+    const Pages vp = pages(tensor(a[4], "v_pages"), "v_pages", p, page_type(p), dev);
+    swa_paged_extra_t extra{};
+    extra.k_exponents = exponents(a[12], "k_exponents", p, dev);
+    extra.v_exponents = exponents(a[13], "v_exponents", p, dev);
+    if (const at::Tensor* t = tensor_or_none(a[14], "tree")) extra.tree = tree_rows(*t, p, dev, &extra.tree_stride);
+    if (const at::Tensor* t = tensor_or_none(a[15], "depth")) {
+      const int64_t tokens[1] = {p.T_q};
+      expect_dense(*t, "depth", tokens, at::kInt, dev);
+      extra.depth = static_cast<const int32_t*>(t->data_ptr());
+    }
     int64_t row;
     const int32_t* table = block_table(tensor(a[5], "block_table"), p, dev, &row);
     const at::Tensor& l = tensor(a[6], "kv_lens");
@@ -278,9 +318,36 @@ PyObject* bind_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect_dense(ss, "softmax_sum", stats, at::kFloat, dev);
     const at::Tensor& ws = workspace(a[10], dev);
     const On on(dev, a[11]);
-    return unlocked(fn, &p, xq.ptr, xq.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(), table, row,
+    return unlocked(fn, &p, xq.ptr, xq.strides(), kp.ptr, kp.strides(), vp.ptr, vp.strides(),
+                    static_cast<const swa_paged_extra_t*>(&extra), table, row,
                     static_cast<const int32_t*>(l.data_ptr()), out.data_ptr(), static_cast<float*>(sm.data_ptr()),
                     static_cast<float*>(ss.data_ptr()), ws.data_ptr(), ws.nbytes(), on.stream);
+  });
+}
+
+// paged_gather(fn, params, k_pages, v_pages, block_table, kv_lens, k, v, workspace, stream, k_exponents, v_exponents)
+PyObject* bind_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> swa_status_t {
+    const auto fn = address<decltype(&swa_paged_gather)>(a[0], "entry point");
+    const swa_paged_params_t& p = *address<const swa_paged_params_t*>(a[1], "parameters");
+    const at::Tensor& k = tensor(a[6], "k");
+    const int dev = device_of(k);
+    const at::ScalarType type = scalar_type(p.dtype);
+    const int64_t kv[3] = {p.T_q, p.N_kv ? p.N_kv : p.N, p.D}, lens[1] = {p.B};
+    const Arg xk = arg(k, "k", kv, type, dev), xv = arg(tensor(a[7], "v"), "v", kv, type, dev);
+    const Pages kp = pages(tensor(a[2], "k_pages"), "k_pages", p, page_type(p), dev);
+    const Pages vp = pages(tensor(a[3], "v_pages"), "v_pages", p, page_type(p), dev);
+    int8_t* const ke = exponents(a[10], "k_exponents", p, dev);
+    int8_t* const ve = exponents(a[11], "v_exponents", p, dev);
+    int64_t row;
+    const int32_t* table = block_table(tensor(a[4], "block_table"), p, dev, &row);
+    const at::Tensor& l = tensor(a[5], "kv_lens");
+    expect_dense(l, "kv_lens", lens, at::kInt, dev);
+    const at::Tensor& ws = workspace(a[8], dev);
+    const On on(dev, a[9]);
+    return unlocked(fn, &p, kp.ptr, kp.strides(), vp.ptr, vp.strides(), ke, ve, table, row,
+                    static_cast<const int32_t*>(l.data_ptr()), xk.ptr, xk.strides(), xv.ptr, xv.strides(), ws.data_ptr(),
+                    ws.nbytes(), on.stream);
   });
 }
 
@@ -289,6 +356,7 @@ PyMethodDef methods[] = {
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_append)), METH_FASTCALL, nullptr},
     {"paged_forward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_forward)), METH_FASTCALL,
      nullptr},
+    {"paged_gather", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_gather)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_swa_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 #include <memory>
+#include <type_traits>
 
 #include "swa_paged.h"
 #include "swa_turn.h"
@@ -22,6 +23,7 @@ constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
 constexpr int64_t kTailSteps = 12;  // key tiles that splitting a last round must save (0.76 us each)
 constexpr double kLog2e = 1.4426950408889634;
+constexpr int64_t kGatherWaves = 8;  // CTAs per SM that a gather spreads its tokens over, before a CTA takes several
 
 template <typename... A>
 swa_status_t fail(swa_status_t st, const char* fmt, A... a) {
@@ -172,9 +174,11 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
 // Split of the tokens over CTAs, and of a CTA over its threads: units of
 // 2 * VEC elements, row_lanes rows at a time.
 void set_split(RopeArgs& a, int dtype, int64_t rows) {
+  const bool q8 = a.pg.k_exp != nullptr;
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
   a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.H - 1) / a.H);
   a.units = static_cast<int32_t>(ceil_div(a.D, 2 * rope_vec(dtype, a.R)));
+  while (q8 && (a.units & (a.units - 1))) ++a.units;  // a row's threads then share a warp
   a.row_lanes = kRopeThreads / a.units;
   const int x = a.heads[0] ? 0 : 1;
   a.tok_inner = a.src_r[x] < a.src_h[x] ? 1 : 0;
@@ -185,7 +189,7 @@ void set_split(RopeArgs& a, int dtype, int64_t rows) {
   // with 16, 116 with 4; an append of 6739 tokens of 48 heads of 96: 21.7 us
   // with 9 (one round), 25.4 with 3; TND rotation 103 us under 80 KB, 106 above.
   const int64_t most_bytes = (a.heads[2] ? 112 : 80) * 1024;
-  const int64_t slots = kSms * (a.heads[2] ? kAppendResident : kRopeResident);
+  const int64_t slots = kSms * (a.heads[2] && !q8 ? kAppendResident : kRopeResident);
   const int64_t bytes = int64_t(a.H) * a.D * (dtype == SWA_DTYPE_FP32 ? 4 : 2);
   int64_t best = 0;
   for (int tok = 1; tok <= (a.tok_inner ? 8 : kRopeMaxTok) && (tok == 1 || tok * bytes <= most_bytes);
@@ -276,6 +280,10 @@ swa_status_t paged_plan(const swa_paged_params_t* p, PagedPlan& plan) {
     return fail(SWA_ERR_PARAM_INVALID, "pre_tokens + next_tokens < 0: every row would be empty");
   if (!std::isfinite(static_cast<float>(p->scale * kLog2e)))
     return fail(SWA_ERR_PARAM_INVALID, "scale is not a finite fp32 number");
+  if (p->sink_tokens < 0)
+    return fail(SWA_ERR_PARAM_INVALID, "sink_tokens must be >= 0, got %lld", (long long)p->sink_tokens);
+  if (p->cache_dtype != SWA_CACHE_SAME && p->cache_dtype != SWA_CACHE_E4M3)
+    return fail(SWA_ERR_PARAM_INVALID, "cache_dtype should be 0 (as dtype) or 1 (e4m3), got %d", p->cache_dtype);
   if (p->cache_layout != SWA_LAYOUT_BNSD && p->cache_layout != SWA_LAYOUT_TND)
     return fail(SWA_ERR_PARAM_INVALID, "cache_layout %d is neither BNSD (0) nor TND (1)", p->cache_layout);
   if (p->num_pages < 1 || p->num_pages > 2147483647)
@@ -350,8 +358,16 @@ swa_status_t page_strides(const swa_page_strides_t* given, const swa_paged_param
 
 swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, const void* k_pages,
                         const swa_page_strides_t* k_s, const void* v_pages, const swa_page_strides_t* v_s,
-                        const int32_t* table, int64_t table_stride, const int32_t* kv_lens, PagedGeom& g) {
+                        const int8_t* k_exp, const int8_t* v_exp, const int32_t* table, int64_t table_stride,
+                        const int32_t* kv_lens, PagedGeom& g) {
   swa_status_t st;
+  const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
+  if (q8) {
+    if ((st = check_pointer(k_exp, "k_exponents")) != SWA_OK || (st = check_pointer(v_exp, "v_exponents")) != SWA_OK)
+      return st;
+  } else if (k_exp || v_exp) {
+    return fail(SWA_ERR_PARAM_INVALID, "exponents are taken with an e4m3 cache only");
+  }
   if ((st = check_pointer(k_pages, "k_pages")) != SWA_OK || (st = check_pointer(v_pages, "v_pages")) != SWA_OK)
     return st;
   if (!table || !kv_lens) return fail(SWA_ERR_PARAM_NULLPTR, "block_table or kv_lens is NULL");
@@ -381,6 +397,13 @@ swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, cons
   g.v_slot = s.slot;
   g.n_k = less_slack(g.n_k);
   g.n_v = less_slack(g.n_v);
+  if (q8) {
+    g.k_exp = const_cast<int8_t*>(k_exp);
+    g.v_exp = const_cast<int8_t*>(v_exp);
+    g.exp_page = plan.N_kv * p->page_size;
+    g.n_exp = less_slack(p->num_pages * g.exp_page);
+    g.wide = (p->D | g.k_page | g.k_head | g.k_slot | g.v_page | g.v_head | g.v_slot) % 16 == 0 ? 1 : 0;
+  }
   g.n_table = (p->B - 1) * table_stride + p->max_pages;
   g.n_lens = p->B;
   return SWA_OK;
@@ -448,7 +471,32 @@ int64_t live_sequences(const PagedPlan& plan) {
   return n;
 }
 
-// Workspace of an append call: the header and one page status per token.
+// Launches over the chunk's tokens, `tok` of them a CTA: go(table, first token, past the last, CTAs).
+template <typename Go>
+cudaError_t over_tokens(const swa_paged_params_t* p, const PagedPlan& plan, int64_t tok, Go&& go) {
+  if (plan.uniform > 0) {
+    PagedTable<kPagedSmallTable> tab{};
+    tab.count = 1;
+    tab.d[0].b = -1;
+    tab.d[0].q_len = static_cast<int32_t>(plan.uniform);
+    return go(tab, 0, p->T_q, static_cast<int>(ceil_div(p->T_q, tok)));
+  }
+  auto take = [&](int b, PagedDesc& d, auto&) {
+    d.q_start = static_cast<int32_t>(plan.start[b]);
+    d.q_len = static_cast<int32_t>(plan.len[b]);
+    d.b = b;
+    return true;
+  };
+  auto one = [&](auto& tab) {
+    const PagedDesc& last = tab.d[tab.count - 1];
+    const int64_t begin = tab.d[0].q_start, end = last.q_start + last.q_len;
+    return go(tab, begin, end, static_cast<int>(ceil_div(end - begin, tok)));
+  };
+  return live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, one)
+                                                  : each_table<kPagedLargeTable>(plan, {}, take, one);
+}
+
+// Workspace of an append or a gather call: the header and one page status per token.
 size_t append_bytes(const swa_paged_params_t* p) { return kHeaderBytes + round256(static_cast<size_t>(p->T_q) * 4); }
 
 // -------------------------------------------------------------- attention --
@@ -510,7 +558,10 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
     // keys a tile can see, in steps (one more: a run may begin inside a step)
     int64_t keys = f.seq.max_kv;
     if (p->sparse_mode == 4) {
-      const long double w = (long double)p->pre_tokens + (long double)p->next_tokens + (long double)part.tok;
+      // (sinks: whole steps of their own)
+      const int64_t sinks = ceil_div(std::min(p->sink_tokens, keys), step) * step;
+      const long double w =
+          (long double)p->pre_tokens + (long double)p->next_tokens + (long double)part.tok + (long double)sinks;
       if (w < (long double)keys) keys = std::max<int64_t>(1, static_cast<int64_t>(w));
     }
     const int64_t steps = ceil_div(keys, step) + 1;
@@ -578,6 +629,9 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   return SWA_OK;
 }
 
+template <PagedKind K>
+using Kind = std::integral_constant<PagedKind, K>;
+
 template <int CAP>
 cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
                      const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, bool joins, cudaStream_t s) {
@@ -590,6 +644,8 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   a.splits = static_cast<int32_t>(part.splits);
   a.par = static_cast<int32_t>(part.par);
   a.cap = static_cast<int32_t>(part.cap);
+  if (a.tree && p->sparse_mode == 4)  // a tile of a tree may see the whole chunk, past the window's keys that the plan counts
+    a.cap += static_cast<int32_t>(ceil_div(*std::max_element(f.seq.len.begin(), f.seq.len.end()), part.step) + 1);
   a.least = static_cast<int32_t>(part.least);
   a.cluster = part.cluster ? 1 : 0;
   a.rows_pad = static_cast<int32_t>(part.rows);
@@ -599,9 +655,15 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   a.part_o = reinterpret_cast<float*>(ws + part.o_at);
   auto go = [&](PagedTable<CAP>& tab) {
     cudaError_t e = cudaSuccess;
+    // calls without sinks, tree and 8-bit cache run the kernels that know nothing of them
+    const PagedKind kind = a.g.k_exp ? PagedKind::kE4m3 : (a.sinks > 0 || a.tree ? PagedKind::kMasks : PagedKind::kPlain);
+    auto launch = [&](auto k) {
+      return few ? launch_paged_rows<k.value>(a, tab, s) : launch_paged_tile<k.value>(a, tab, mk, mv, mq, s);
+    };
     if (joins) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
-    else if (few) e = launch_paged_rows(a, tab, s);
-    else e = launch_paged_tile(a, tab, mk, mv, mq, s);
+    else if (kind == PagedKind::kPlain) e = launch(Kind<PagedKind::kPlain>{});
+    else if (kind == PagedKind::kMasks) e = launch(Kind<PagedKind::kMasks>{});
+    else e = launch(Kind<PagedKind::kE4m3>{});
     a.item_base += tab.n_items;
     a.clear_err = 0;
     return e;
@@ -707,6 +769,19 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
                               const int32_t* positions, const void* q, const swa_strides_t* q_strides, void* q_out,
                               const swa_strides_t* q_out_strides, void* workspace, size_t workspace_bytes,
                               swa_stream_t stream) {
+  return swa_paged_append_ext(p, k, k_strides, v, v_strides, k_pages, k_page_strides, v_pages, v_page_strides, nullptr,
+                              nullptr, block_table, table_stride, kv_lens, rope, positions, q, q_strides, q_out,
+                              q_out_strides, workspace, workspace_bytes, stream);
+}
+
+swa_status_t swa_paged_append_ext(const swa_paged_params_t* p, const void* k, const swa_strides_t* k_strides,
+                                  const void* v, const swa_strides_t* v_strides, void* k_pages,
+                                  const swa_page_strides_t* k_page_strides, void* v_pages,
+                                  const swa_page_strides_t* v_page_strides, int8_t* k_exponents, int8_t* v_exponents,
+                                  const int32_t* block_table, int64_t table_stride, const int32_t* kv_lens,
+                                  const swa_rope_params_t* rope, const int32_t* positions, const void* q,
+                                  const swa_strides_t* q_strides, void* q_out, const swa_strides_t* q_out_strides,
+                                  void* workspace, size_t workspace_bytes, swa_stream_t stream) {
   return guarded([&]() -> swa_status_t {
     PagedPlan plan;
     swa_status_t st = paged_plan(p, plan);
@@ -726,7 +801,8 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
     if ((q == nullptr) != (q_out == nullptr)) return fail(SWA_ERR_PARAM_NULLPTR, "q and q_out come together");
     if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
     if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
-    st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.pg);
+    st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, k_exponents, v_exponents, block_table,
+                    table_stride, kv_lens, a.pg);
     if (st != SWA_OK) return st;
     const size_t need = append_bytes(p);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
@@ -777,32 +853,13 @@ swa_status_t swa_paged_append(const swa_paged_params_t* p, const void* k, const 
     if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
     const bool il = rope && rope->interleaved != 0;
-    if (plan.uniform > 0) {
-      PagedTable<kPagedSmallTable> tab{};
-      tab.count = 1;
-      tab.d[0].b = -1;
-      tab.d[0].q_len = static_cast<int32_t>(plan.uniform);
-      a.rows = p->T_q;
-      e = launch_append(a, tab, p->dtype, il, static_cast<int>(ceil_div(p->T_q, a.tok)), s);
-    } else {
-      auto take = [&](int b, PagedDesc& d, auto&) {
-        d.q_start = static_cast<int32_t>(plan.start[b]);
-        d.q_len = static_cast<int32_t>(plan.len[b]);
-        d.b = b;
-        return true;
-      };
-      auto go = [&](auto& tab) {
-        const PagedDesc& last = tab.d[tab.count - 1];
-        a.tok_begin = tab.d[0].q_start;
-        a.rows = last.q_start + last.q_len;
-        const int n = static_cast<int>(ceil_div(a.rows - a.tok_begin, a.tok));
-        const cudaError_t le = launch_append(a, tab, p->dtype, il, n, s);
-        a.clear_err = 0;
-        return le;
-      };
-      e = live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, go)
-                                                   : each_table<kPagedLargeTable>(plan, {}, take, go);
-    }
+    e = over_tokens(p, plan, a.tok, [&](const auto& tab, int64_t begin, int64_t end, int n_ctas) {
+      a.tok_begin = static_cast<int32_t>(begin);
+      a.rows = end;
+      const cudaError_t le = launch_append(a, tab, p->dtype, il, n_ctas, s);
+      a.clear_err = 0;
+      return le;
+    });
     return e == cudaSuccess ? SWA_OK : cuda_fail(e, "append launch");
   });
 }
@@ -823,16 +880,46 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
                                const swa_page_strides_t* v_page_strides, const int32_t* block_table,
                                int64_t table_stride, const int32_t* kv_lens, void* out, float* softmax_max,
                                float* softmax_sum, void* workspace, size_t workspace_bytes, swa_stream_t stream) {
+  return swa_paged_forward_ext(p, q, q_strides, k_pages, k_page_strides, v_pages, v_page_strides, nullptr, block_table,
+                               table_stride, kv_lens, out, softmax_max, softmax_sum, workspace, workspace_bytes, stream);
+}
+
+swa_status_t swa_paged_forward_ext(const swa_paged_params_t* p, const void* q, const swa_strides_t* q_strides,
+                                   const void* k_pages, const swa_page_strides_t* k_page_strides, const void* v_pages,
+                                   const swa_page_strides_t* v_page_strides, const swa_paged_extra_t* extra,
+                                   const int32_t* block_table, int64_t table_stride, const int32_t* kv_lens, void* out,
+                                   float* softmax_max, float* softmax_sum, void* workspace, size_t workspace_bytes,
+                                   swa_stream_t stream) {
   return guarded([&]() -> swa_status_t {
     ForwardPlan f;
     swa_status_t st = forward_plan(p, f);
     if (st != SWA_OK) return st;
+    const swa_paged_extra_t x = extra ? *extra : swa_paged_extra_t{};
     if ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(out, "out")) != SWA_OK) return st;
     if ((reinterpret_cast<uintptr_t>(softmax_max) | reinterpret_cast<uintptr_t>(softmax_sum)) & 3u)
       return fail(SWA_ERR_PARAM_INVALID, "softmax_max and softmax_sum must be 4-byte aligned");
     PagedArgs a{};
-    st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, block_table, table_stride, kv_lens, a.g);
+    st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, x.k_exponents, x.v_exponents,
+                    block_table, table_stride, kv_lens, a.g);
     if (st != SWA_OK) return st;
+    if (x.tree) {
+      const int64_t words = ceil_div(*std::max_element(f.seq.len.begin(), f.seq.len.end()), 32);
+      const int64_t row = x.tree_stride == 0 ? words : x.tree_stride;
+      if ((reinterpret_cast<uintptr_t>(x.tree) | reinterpret_cast<uintptr_t>(x.depth)) & 3u)
+        return fail(SWA_ERR_PARAM_INVALID, "tree and depth must be 4-byte aligned");
+      if (row < words || row > (int64_t(1) << 40))
+        return fail(SWA_ERR_PARAM_INVALID, "tree_stride %lld is below the %lld words of the longest chunk", (long long)row,
+                    (long long)words);
+      if (p->sparse_mode == 4 && p->next_tokens < 0)
+        return fail(SWA_ERR_PARAM_INVALID, "next_tokens must be >= 0 with a tree, got %lld", (long long)p->next_tokens);
+      a.tree = x.tree;
+      a.tree_row = row;
+      a.depth = x.depth;
+      a.n_tree = less_slack((p->T_q - 1) * row + words);
+      a.n_depth = less_slack(p->T_q);
+    } else if (x.depth || x.tree_stride != 0) {
+      return fail(SWA_ERR_PARAM_INVALID, "depth and tree_stride are taken with a tree only");
+    }
     swa_strides_t qs;
     // the row stride may not fold rows onto each other: tensor maps want it
     st = tensor_strides(q_strides, SWA_LAYOUT_TND, 1, p->T_q, p->N, p->D, true, "q", &qs, &a.n_q);
@@ -845,6 +932,7 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     const int64_t lim = int64_t(1) << 29;  // positions stay within +-2^28: no sum passes int32
     a.pre = static_cast<int32_t>(std::min(std::max(p->pre_tokens, -lim), lim));
     a.next = static_cast<int32_t>(std::min(std::max(p->next_tokens, -lim), lim));
+    a.sinks = p->sparse_mode == 4 ? static_cast<int32_t>(std::min(p->sink_tokens, lim)) : 0;
     a.scale_log2 = static_cast<float>(p->scale * kLog2e);
     a.stall = debug_stall_bits();
     a.q_row = qs.row;
@@ -865,9 +953,10 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     if (f.tile.items > 0) {
       const int64_t low = p->page_size & -p->page_size;
       a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
-      st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
-                    a.box_rows, "k_pages");
-      if (st == SWA_OK)
+      if (!a.g.k_exp)
+        st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
+                      a.box_rows, "k_pages");
+      if (!a.g.k_exp && st == SWA_OK)
         st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
                       a.box_rows, "v_pages");
       if (st == SWA_OK) st = query_map(&mq, &a.q_tma, q, qs, p, f.tile);
@@ -893,6 +982,62 @@ swa_status_t swa_paged_forward(const swa_paged_params_t* p, const void* q, const
     run(f.tile, true);
     run(f.rows, true);
     return e == cudaSuccess ? SWA_OK : cuda_fail(e, "paged attention launch");
+  });
+}
+
+swa_status_t swa_paged_gather(const swa_paged_params_t* p, const void* k_pages, const swa_page_strides_t* k_page_strides,
+                              const void* v_pages, const swa_page_strides_t* v_page_strides, const int8_t* k_exponents,
+                              const int8_t* v_exponents, const int32_t* block_table, int64_t table_stride,
+                              const int32_t* kv_lens, void* k, const swa_strides_t* k_strides, void* v,
+                              const swa_strides_t* v_strides, void* workspace, size_t workspace_bytes,
+                              swa_stream_t stream) {
+  return guarded([&]() -> swa_status_t {
+    PagedPlan plan;
+    swa_status_t st = paged_plan(p, plan);
+    if (st != SWA_OK) return st;
+    if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
+    GatherArgs a{};
+    st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, k_exponents, v_exponents, block_table,
+                    table_stride, kv_lens, a.pg);
+    if (st != SWA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, append_bytes(p))) != SWA_OK) return st;
+    a.src[0] = k_pages;
+    a.src[1] = v_pages;
+    void* dst[2] = {k, v};
+    const swa_strides_t* given[2] = {k_strides, v_strides};
+    const char* names[2] = {"k", "v"};
+    for (int x = 0; x < 2; ++x) {
+      swa_strides_t s;
+      int64_t n;
+      st = tensor_strides(given[x], SWA_LAYOUT_TND, 1, p->T_q, plan.N_kv, p->D, true, names[x], &s, &n);
+      if (st == SWA_OK) st = check_apart(s, SWA_LAYOUT_TND, 1, p->T_q, plan.N_kv, p->D, names[x]);
+      if (st != SWA_OK) return st;
+      a.dst[x] = dst[x];
+      a.dst_r[x] = s.row;
+      a.dst_h[x] = s.head;
+      a.n_dst[x] = less_slack(n);
+    }
+    const int64_t pieces = ceil_div(p->D, a.pg.k_exp ? 16 : 8);  // threads of a row
+    while ((int64_t(1) << a.lane_shift) < pieces) ++a.lane_shift;
+    a.lanes = 1 << a.lane_shift;
+    // few tokens: over the SMs; many: as many per CTA as a thread needs for its rows in flight
+    a.tok = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(p->T_q / (kSms * kGatherWaves), 1), kGatherMostTok));
+    a.err = static_cast<int32_t*>(workspace);
+    a.page_err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    a.clear_err = SWA_CHECKS ? 0 : 1;
+    if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+    const bool f16 = p->dtype == SWA_DTYPE_FP16;
+    e = over_tokens(p, plan, a.tok, [&](const auto& tab, int64_t begin, int64_t end, int n_ctas) {
+      a.tok_begin = static_cast<int32_t>(begin);
+      a.rows = end;
+      const cudaError_t le = launch_gather(a, tab, f16, n_ctas, s);
+      a.clear_err = 0;
+      return le;
+    });
+    return e == cudaSuccess ? SWA_OK : cuda_fail(e, "gather launch");
   });
 }
 

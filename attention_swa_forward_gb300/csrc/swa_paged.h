@@ -37,13 +37,21 @@ struct PagedGeom {
   int64_t v_page, v_head, v_slot;
   const int32_t* table;
   const int32_t* kv_lens;
+  // 8-bit cache: the exponents of its rows, [pages][N_kv][page_size]; exp_page: of a page
+  int8_t *k_exp, *v_exp;
+  int64_t exp_page;
+  int32_t wide;  // 8-bit cache: rows start on 16 bytes and are multiples of 16 long (else of 8)
   // extents of the caller's tensors in elements, for the bounds-checked build
-  int64_t n_k, n_v, n_table, n_lens;
+  int64_t n_k, n_v, n_table, n_lens, n_exp;
 };
+
+// The exponents of an 8-bit row: least (bf16, fp16) and most.  A larger one
+// marks a row with a NaN.
+constexpr int kExpLeastBf16 = -100, kExpLeastF16 = -15, kExpMost = 7, kExpNan = 127;
 
 // ------------------------------------------------------- rotary / append --
 constexpr int kRopeMaxTok = 16;  // rows (tokens) per CTA at most
-constexpr int kRopeResident = 4, kAppendResident = 5;  // CTAs per SM
+constexpr int kRopeResident = 4, kAppendResident = 5;  // CTAs per SM (an append to an 8-bit cache: 4)
 constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
@@ -75,6 +83,24 @@ struct RopeArgs {
   uint8_t axis[64];
 };
 
+// The tokens of a chunk read back from the pages.
+constexpr int kGatherThreads = 256, kGatherMostTok = 16;
+struct GatherArgs {
+  PagedGeom pg;
+  const void* src[2];           // k, v pages
+  void* dst[2];
+  int64_t dst_r[2], dst_h[2];   // strides: row, head
+  int64_t n_dst[2];             // extents, for the bounds-checked build
+  int32_t lanes, lane_shift;    // threads of a row: a power of two
+  int32_t tok, tok_begin;       // tokens per CTA, first token of this launch
+  int64_t rows;                 // last token + 1 of this launch
+  int32_t* err;
+  int32_t clear_err;
+  int32_t* page_err;  // per token
+};
+template <int CAP>
+cudaError_t launch_gather(const GatherArgs& a, const PagedTable<CAP>& tab, bool f16, int n_ctas, cudaStream_t stream);
+
 template <int CAP>
 cudaError_t launch_append(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype, bool interleaved, int n_ctas,
                           cudaStream_t stream);
@@ -100,6 +126,12 @@ struct PagedArgs {
   int32_t f16;
   int32_t sparse_mode;
   int32_t pre, next;  // clamped so that position sums stay inside int32
+  int32_t sinks;      // BAND: keys below this one stay visible behind the window
+  // a chunk that is a tree of drafted tokens: bit c of row t: token t sees token c of its chunk
+  const uint32_t* tree;
+  int64_t tree_row;      // words between rows
+  const int32_t* depth;  // of each token; NULL: its place in the chunk
+  int64_t n_tree, n_depth;  // extents, for the bounds-checked build
   float scale_log2;
   int32_t whole;      // tile kernel: the first items of the launch, one unit each; the others are split
   int32_t splits;     // CTAs (units) per split item along the keys, at most
@@ -162,17 +194,52 @@ SWA_PAGED_HD PagedItem resolve_paged(const PagedTable<CAP>& tab, int groups, int
   return it;
 }
 
-// Keys that some row of the tile sees, [lo, hi] (empty when lo > hi).  Chunk
-// token i has position kv_len - q_len + i.
-SWA_PAGED_HD void paged_key_range(int sparse_mode, int pre, int next, int kv_len, int q_len, int tok0, int n_tok,
-                                  int* lo, int* hi) {
-  *lo = 0;
-  *hi = kv_len - 1;
-  if (sparse_mode == 4) {
-    const int p0 = kv_len - q_len + tok0, p1 = p0 + n_tok - 1;
-    *lo = p0 - pre > 0 ? p0 - pre : 0;
-    *hi = p1 + next < *hi ? p1 + next : *hi;
+// Keys that some row of a tile sees: [lo, hi] (empty when lo > hi), and the
+// sinks [0, sinks) where those end before lo.
+struct PagedKeys {
+  int lo, hi, sinks;
+};
+// Chunk token i has position kv_len - q_len + i; a token of a tree that of its
+// depth, at least that of depth 0, and it may see the whole chunk.  X: there may
+// be sinks or a tree.
+template <bool X>
+SWA_PAGED_HD PagedKeys paged_keys(const PagedArgs& a, int kv_len, int q_len, int tok0, int n_tok) {
+  PagedKeys k{0, kv_len - 1, 0};
+  if (a.sparse_mode == 4) {
+    const bool tree = X && a.tree != nullptr;
+    const int p0 = kv_len - q_len + (tree ? 0 : tok0), p1 = p0 + n_tok - 1;
+    k.lo = p0 - a.pre > 0 ? p0 - a.pre : 0;
+    if (!tree) k.hi = p1 + a.next < k.hi ? p1 + a.next : k.hi;
+    if (X && a.sinks > 0) {
+      const int n = a.sinks < k.hi + 1 ? a.sinks : k.hi + 1;
+      if (k.lo > k.hi) {
+        k.lo = 0;
+        k.hi = n - 1;
+      } else if (n >= k.lo) {
+        k.lo = 0;
+      } else {
+        k.sinks = n;
+      }
+    }
   }
+  return k;
+}
+// The same keys in runs of 2^shift: unit x of `total` is number x < sinks ? x : jump + x.
+struct PagedUnits {
+  int sinks, jump, total;
+  SWA_PAGED_HD int at(int x) const { return x < sinks ? x : jump + x; }
+};
+template <bool X>
+SWA_PAGED_HD PagedUnits paged_units(const PagedKeys& k, int shift) {
+  PagedUnits u{0, k.lo >> shift, 0};
+  if (k.lo > k.hi) return u;
+  if (X && k.sinks > 0) {
+    const int n = ((k.sinks - 1) >> shift) + 1;
+    u.sinks = n < u.jump ? n : u.jump;
+  }
+  u.total = u.sinks + (k.hi >> shift) - u.jump + 1;
+  u.jump -= u.sinks;
+  return u;
 }
 
 // Key steps of split s: [begin, end) of the item's `steps`, in `*active` equal
@@ -195,9 +262,14 @@ constexpr int kRowsStep = 64;     // keys per step of the few-row kernel (4 warp
 constexpr int kPagedTileRows = 128;  // rows of a tile of the tensor-memory kernel
 constexpr int kPagedTileStep = 128;  // keys per step of it
 
-template <int CAP>
+// What a kernel can do beside the window over a 16-bit cache: sinks and trees
+// (extended masks), and those over an 8-bit cache.  Each is a translation unit
+// of its own, and calls that need neither run what they ran without them.
+enum class PagedKind { kPlain, kMasks, kE4m3 };
+
+template <PagedKind KIND, int CAP>
 cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream);
-template <int CAP>
+template <PagedKind KIND, int CAP>
 cudaError_t launch_paged_tile(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk,
                               const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t stream);
 // Join the splits' partial results; `step_keys` as of the kernel that wrote them.

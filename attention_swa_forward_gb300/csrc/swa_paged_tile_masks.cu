@@ -1,0 +1,15 @@
+// swa_paged_tile_masks.cu — attention of a chunk with sinks or a tree, 16-bit cache (swa_paged_tile.cuh).
+#include "swa_paged_tile.cuh"
+
+namespace swa {
+
+template cudaError_t launch_paged_tile<PagedKind::kMasks, kPagedSmallTable>(const PagedArgs&,
+                                                                         const PagedTable<kPagedSmallTable>&,
+                                                                         const CUtensorMap&, const CUtensorMap&,
+                                                                         const CUtensorMap&, cudaStream_t);
+template cudaError_t launch_paged_tile<PagedKind::kMasks, kPagedLargeTable>(const PagedArgs&,
+                                                                         const PagedTable<kPagedLargeTable>&,
+                                                                         const CUtensorMap&, const CUtensorMap&,
+                                                                         const CUtensorMap&, cudaStream_t);
+
+}  // namespace swa

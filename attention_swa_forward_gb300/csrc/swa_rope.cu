@@ -17,8 +17,14 @@
 // tokens per CTA 112, 4 tokens 116; all rows staged through shared memory by
 // cp.async, 4 tokens per CTA, 130: what is left are instructions, not bytes in
 // flight.
+//
+// 8-bit cache (Q8): a key or value row is rotated in fp32, its largest magnitude
+// found by shuffles among the threads that hold it (a power of two of them), and
+// its codes rounded once from fp32; the exponent goes out as a byte per row.
 #include "swa_paged.h"
 #include "swa_device.cuh"
+
+#include <type_traits>
 
 namespace swa {
 namespace {
@@ -50,6 +56,7 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 
 struct RopeSmem {
   int64_t src[kRopeMaxTok][3], dst[kRopeMaxTok][3];  // element offsets of (token, head 0); dst < 0: not stored
+  int64_t ex[kRopeMaxTok];                           // 8-bit cache: offset of the exponent of (token, head 0)
   int32_t pos[kRopeMaxTok];                          // position in its sequence (append)
   alignas(16) float cs[kRopeMaxTok][64], sn[kRopeMaxTok][64];
 };
@@ -89,8 +96,64 @@ __device__ __forceinline__ void turn(T (&a)[VEC], T (&b)[VEC], const float* cs_,
   }
 }
 
-template <typename T, int VEC, bool IL, bool PAGED, int CAP>
-__global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeResident)
+// The rotation of `turn` before its rounding, or without one (R: the pairs turn).
+template <typename T, int VEC, bool IL>
+__device__ __forceinline__ void turn_float(const T (&a)[VEC], const T (&b)[VEC], float (&x)[VEC], float (&y)[VEC],
+                                           const float* cs, const float* sn, bool turns) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    x[i] = to_f(a[i]);
+    y[i] = to_f(b[i]);
+  }
+  if (!turns) return;
+  if constexpr (IL) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+      x[2 * i] = x0 * cs[i] - x1 * sn[i];
+      x[2 * i + 1] = x1 * cs[i] + x0 * sn[i];
+      y[2 * i] = y0 * cs[VEC / 2 + i] - y1 * sn[VEC / 2 + i];
+      y[2 * i + 1] = y1 * cs[VEC / 2 + i] + y0 * sn[VEC / 2 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float u = x[i], v = y[i];
+      x[i] = u * cs[i] - v * sn[i];
+      y[i] = v * cs[i] + u * sn[i];
+    }
+  }
+}
+// Largest magnitude of VEC values as bits, which order like the values (a NaN above infinity).
+template <int VEC>
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[VEC], uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return top;
+}
+// The least exponent e, within its limits, with top <= 448 2^e = 0.875 2^(9 + e).
+__device__ __forceinline__ int row_exponent(uint32_t top, int least) {
+  if (top > 0x7F800000u) return kExpNan;
+  const int e = static_cast<int>(top >> 23) - 126 - 9 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, least), kExpMost);
+}
+// VEC codes of x times 2^-e, nearest even, saturated at 448.
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[VEC], float scale) {
+  uint32_t w[VEC / 4];
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[4 * i + 1] * scale), "f"(x[4 * i] * scale));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[4 * i + 3] * scale), "f"(x[4 * i + 2] * scale));
+    w[i] = lo | static_cast<uint32_t>(hi) << 16;
+  }
+  if constexpr (VEC == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
+template <typename T, int VEC, bool IL, bool PAGED, bool Q8, int CAP>
+__global__ void __launch_bounds__(kRopeThreads, PAGED && !Q8 ? kAppendResident : kRopeResident)
     swa_rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ PagedTable<CAP> tab) {
   using R = typename Raw<T, VEC>::type;
   __shared__ RopeSmem s;
@@ -133,7 +196,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
       }
       const int pos = len - q_len + i;
       s.pos[tid] = pos;
-      int64_t kd = -1, vd = -1;
+      int64_t kd = -1, vd = -1, ex = 0;
       if (pos >= 0) {
         const int entry = pos / a.pg.page_size, slot = pos - entry * a.pg.page_size;
         const int64_t e = b * a.pg.table_stride + entry;
@@ -141,12 +204,14 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
         if (page >= 0 && page < a.pg.num_pages) {
           kd = page * a.pg.k_page + slot * a.pg.k_slot;
           vd = page * a.pg.v_page + slot * a.pg.v_slot;
+          if (Q8) ex = page * a.pg.exp_page + slot;
         } else {
           bad = kPageErrEntry;
         }
       }
       s.dst[tid][1] = kd;
       s.dst[tid][2] = vd;
+      if (Q8) s.ex[tid] = ex;
     }
   }
   if (PAGED && tid < n_tok) a.page_err[t0 + tid] = bad;
@@ -197,7 +262,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
   const int n_rows = a.tok_inner ? a.H << a.tok_shift : n_tok * a.H;
   constexpr int kBatch = PAGED ? 2 : 4;
   struct Place {
-    int tk, sg, ia, ib;
+    int tk, sg, h, ia, ib;
     int64_t src, dst;
   };
   auto locate = [&](int r, Place& w) -> bool {
@@ -222,6 +287,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
       w.ia = 2 * u * VEC;
       w.ib = w.ia + VEC;
     }
+    w.h = h;
     w.src = s.src[w.tk][w.sg] + h * a.src_h[w.sg];
     w.dst = s.dst[w.tk][w.sg];
     if (PAGED && w.dst < 0) return false;
@@ -235,7 +301,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
       Place w;
       if (!locate(r0 + k * a.row_lanes, w)) continue;
       const T* p = static_cast<const T*>(a.src[w.sg]);
-      if (rope_in_bounds(w.src + w.ia, VEC, a.n_src[w.sg], a.err))
+      if ((!Q8 || w.ia < a.D) && rope_in_bounds(w.src + w.ia, VEC, a.n_src[w.sg], a.err))
         ra[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + w.ia));
       if (w.ib < a.D && rope_in_bounds(w.src + w.ib, VEC, a.n_src[w.sg], a.err))
         rb[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + w.ib));
@@ -247,10 +313,30 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
       alignas(16) T xa[VEC], xb[VEC];
       *reinterpret_cast<R*>(xa) = ra[k];
       *reinterpret_cast<R*>(xb) = rb[k];
+      if (Q8 && w.sg != 0) {
+        // (the threads of a row, neighbours in a warp, are all here or none)
+        float fa[VEC], fb[VEC];
+        turn_float<T, VEC, IL>(xa, xb, fa, fb, &s.cs[w.tk][u * VEC], &s.sn[w.tk][u * VEC],
+                               w.sg == 1 && u * 2 * VEC < a.R);
+        uint32_t top = 0;
+        if (w.ia < a.D) top = top_bits<VEC>(fa, top);
+        if (w.ib < a.D) top = top_bits<VEC>(fb, top);
+        const uint32_t row_mask = ((1u << a.units) - 1u) << ((tid & 31) & ~(a.units - 1));
+        for (int d = a.units >> 1; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(row_mask, top, d));
+        const int e = row_exponent(top, std::is_same<T, __half>::value ? kExpLeastF16 : kExpLeastBf16);
+        const float scale = e == kExpNan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        uint8_t* p = static_cast<uint8_t*>(a.dst[w.sg]) + w.dst;
+        if (w.ia < a.D && rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ia, fa, scale);
+        if (w.ib < a.D && rope_in_bounds(w.dst + w.ib, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ib, fb, scale);
+        const int64_t x = s.ex[w.tk] + static_cast<int64_t>(w.h) * a.pg.page_size;
+        if (u == 0 && rope_in_bounds(x, 1, a.pg.n_exp, a.err))
+          (w.sg == 1 ? a.pg.k_exp : a.pg.v_exp)[x] = static_cast<int8_t>(e);
+        continue;
+      }
       // the chunk's pairs: VEC of them, from pair u * VEC on in both forms
       if (w.sg != 2 && u * 2 * VEC < a.R) turn<T, VEC, IL>(xa, xb, &s.cs[w.tk][u * VEC], &s.sn[w.tk][u * VEC]);
       T* p = static_cast<T*>(a.dst[w.sg]);
-      if (rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err))
+      if ((!Q8 || w.ia < a.D) && rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err))
         *reinterpret_cast<R*>(p + w.dst + w.ia) = *reinterpret_cast<R*>(xa);
       if (w.ib < a.D && rope_in_bounds(w.dst + w.ib, VEC, a.n_dst[w.sg], a.err))
         *reinterpret_cast<R*>(p + w.dst + w.ib) = *reinterpret_cast<R*>(xb);
@@ -258,24 +344,24 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED ? kAppendResident : kRopeR
   }
 }
 
-template <bool PAGED, int CAP>
+template <bool PAGED, bool Q8, int CAP>
 cudaError_t launch_any(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype, bool il, int ctas, cudaStream_t st) {
   const bool wide = rope_vec(dtype, a.R) == 8;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(ctas), dim3(kRopeThreads), 0, st, a, tab); };
   if constexpr (!PAGED) {  // a paged cache holds 16-bit elements
     if (dtype == SWA_DTYPE_FP32)
-      return il ? go(swa_rope_kernel<float, 4, true, PAGED, CAP>) : go(swa_rope_kernel<float, 4, false, PAGED, CAP>);
+      return il ? go(swa_rope_kernel<float, 4, true, PAGED, Q8, CAP>) : go(swa_rope_kernel<float, 4, false, PAGED, Q8, CAP>);
   }
   if (dtype == SWA_DTYPE_FP16) {
     if (wide)
-      return il ? go(swa_rope_kernel<__half, 8, true, PAGED, CAP>) : go(swa_rope_kernel<__half, 8, false, PAGED, CAP>);
-    return il ? go(swa_rope_kernel<__half, 4, true, PAGED, CAP>) : go(swa_rope_kernel<__half, 4, false, PAGED, CAP>);
+      return il ? go(swa_rope_kernel<__half, 8, true, PAGED, Q8, CAP>) : go(swa_rope_kernel<__half, 8, false, PAGED, Q8, CAP>);
+    return il ? go(swa_rope_kernel<__half, 4, true, PAGED, Q8, CAP>) : go(swa_rope_kernel<__half, 4, false, PAGED, Q8, CAP>);
   }
   if (wide)
-    return il ? go(swa_rope_kernel<__nv_bfloat16, 8, true, PAGED, CAP>)
-              : go(swa_rope_kernel<__nv_bfloat16, 8, false, PAGED, CAP>);
-  return il ? go(swa_rope_kernel<__nv_bfloat16, 4, true, PAGED, CAP>)
-            : go(swa_rope_kernel<__nv_bfloat16, 4, false, PAGED, CAP>);
+    return il ? go(swa_rope_kernel<__nv_bfloat16, 8, true, PAGED, Q8, CAP>)
+              : go(swa_rope_kernel<__nv_bfloat16, 8, false, PAGED, Q8, CAP>);
+  return il ? go(swa_rope_kernel<__nv_bfloat16, 4, true, PAGED, Q8, CAP>)
+            : go(swa_rope_kernel<__nv_bfloat16, 4, false, PAGED, Q8, CAP>);
 }
 
 }  // namespace
@@ -283,13 +369,14 @@ cudaError_t launch_any(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype,
 cudaError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, cudaStream_t stream) {
   PagedTable<1> none{};
   const int64_t ctas = (a.rows + a.tok - 1) / a.tok;
-  return launch_any<false, 1>(a, none, dtype, interleaved, static_cast<int>(ctas), stream);
+  return launch_any<false, false, 1>(a, none, dtype, interleaved, static_cast<int>(ctas), stream);
 }
 
 template <int CAP>
 cudaError_t launch_append(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype, bool interleaved, int n_ctas,
                           cudaStream_t stream) {
-  return launch_any<true, CAP>(a, tab, dtype, interleaved, n_ctas, stream);
+  return a.pg.k_exp ? launch_any<true, true, CAP>(a, tab, dtype, interleaved, n_ctas, stream)
+                    : launch_any<true, false, CAP>(a, tab, dtype, interleaved, n_ctas, stream);
 }
 template cudaError_t launch_append<kPagedSmallTable>(const RopeArgs&, const PagedTable<kPagedSmallTable>&, int, bool,
                                                      int, cudaStream_t);

@@ -30,6 +30,7 @@ SWA_ERR_BOUNDS = 161104
 SWA_ERR_PAGE = 161105
 LAYOUTS = {"BNSD": 0, "TND": 1}
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+CACHE_DTYPES = {"": 0, "e4m3": 1}
 
 
 class SwaError(RuntimeError):
@@ -118,6 +119,20 @@ class SwaPagedParams(ctypes.Structure):
         ("next_tokens", ctypes.c_int64),
         ("sparse_mode", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
+        ("sink_tokens", ctypes.c_int64),
+        ("cache_dtype", ctypes.c_int32),
+    ]
+
+
+class SwaPagedExtra(ctypes.Structure):
+    """Mirror of swa_paged_extra_t."""
+
+    _fields_ = [
+        ("k_exponents", ctypes.c_void_p),
+        ("v_exponents", ctypes.c_void_p),
+        ("tree", ctypes.c_void_p),
+        ("tree_stride", ctypes.c_int64),
+        ("depth", ctypes.c_void_p),
     ]
 
 
@@ -224,13 +239,21 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.swa_paged_forward_workspace_size.restype = st
     L.swa_paged_forward.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     L.swa_paged_forward.restype = st
+    L.swa_paged_append_ext.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, RP, vp, vp, vp, vp, vp, vp,
+                                       sz, vp]
+    L.swa_paged_append_ext.restype = st
+    L.swa_paged_forward_ext.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.swa_paged_forward_ext.restype = st
+    L.swa_paged_gather.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.swa_paged_gather.restype = st
     L.swa_paged_append_status.argtypes = [PP, vp, vp]
     L.swa_paged_append_status.restype = st
     L.swa_paged_forward_status.argtypes = [PP, vp, vp]
     L.swa_paged_forward_status.restype = st
     # addresses for the extension module, which calls them on tensors
     L.entries = {n: ctypes.cast(getattr(L, n), vp).value
-                 for n in ("swa_rope_forward", "swa_rope_backward", "swa_paged_append", "swa_paged_forward")}
+                 for n in ("swa_rope_forward", "swa_rope_backward", "swa_paged_append_ext", "swa_paged_forward_ext",
+                           "swa_paged_gather")}
     L.swa_last_error.argtypes = []
     L.swa_last_error.restype = ctypes.c_char_p
     return L
@@ -244,7 +267,7 @@ def exported_symbols():
             "swa_debug_extent_slack", "swa_rope_params_default", "swa_rope_forward", "swa_rope_backward",
             "swa_paged_params_default", "swa_paged_append_workspace_size", "swa_paged_append",
             "swa_paged_forward_workspace_size", "swa_paged_forward", "swa_paged_append_status",
-            "swa_paged_forward_status"]
+            "swa_paged_forward_status", "swa_paged_append_ext", "swa_paged_forward_ext", "swa_paged_gather"]
 
 
 def _check(status: int):
@@ -543,9 +566,11 @@ class PagedParams:
         c.scale, c.sparse_mode = float(geom.scale), int(geom.sparse_mode)
         c.pre_tokens, c.next_tokens = int(geom.pre_tokens), int(geom.next_tokens)
         c.dtype = DTYPES[geom.dtype]
+        c.sink_tokens, c.cache_dtype = int(geom.sink_tokens), CACHE_DTYPES[geom.cache_dtype]
         self.torch_dtype = _TORCH_DTYPES[geom.dtype]
         self._ref = ctypes.byref(c)
         self.q_shape = (geom.T_q, geom.N, geom.D)
+        self.kv_shape = (geom.T_q, geom.n_kv, geom.D)
         self.stat_shape = (geom.T_q, geom.N)
         self.addr = ctypes.addressof(c)
 
@@ -648,28 +673,52 @@ def paged_forward_workspace(geom, device="cuda:0"):
 
 
 def paged_append(geom, k, v, k_pages, v_pages, block_table, kv_lens, rope=None, positions=None, q=None, q_out=None,
-                 workspace=None, stream=None):
-    """Enqueue swa_paged_append: the chunk's k and v [T_q, N_kv, D] into the
+                 workspace=None, stream=None, k_exponents=None, v_exponents=None):
+    """Enqueue swa_paged_append_ext: the chunk's k and v [T_q, N_kv, D] into the
     pages; with `rope` (a RopeGeometry / RopeParams) k is rotated on the way, and
-    q too, into q_out.  Returns q_out (None without q)."""
+    q too, into q_out.  An 8-bit cache (cache_dtype "e4m3", pages of
+    torch.float8_e4m3fn) takes the exponents that go with its codes, int8
+    [num_pages, N_kv, page_size].  Returns q_out (None without q)."""
     p = geom if type(geom) is PagedParams else _paged_params(geom)
     r = rope if rope is None or type(rope) is RopeParams else _rope_params(rope)
     if q is not None and q_out is None:
         q_out = _empty(p.q_shape, p.torch_dtype, q, "q", stream)
     if workspace is None:
         workspace = _empty(swa_paged_append_workspace_size(p), torch.uint8, k, "k", stream)
-    status = _bind().paged_append(lib().entries["swa_paged_append"], p.addr, k, v, k_pages, v_pages, block_table,
+    status = _bind().paged_append(lib().entries["swa_paged_append_ext"], p.addr, k, v, k_pages, v_pages, block_table,
                                   kv_lens, 0 if r is None else r.addr, positions, q, q_out, workspace,
-                                  _handle(stream))
+                                  _handle(stream), k_exponents, v_exponents)
     if status != SWA_OK:
         _check(status)
     return q_out
 
 
+def paged_gather(geom, k_pages, v_pages, block_table, kv_lens, k=None, v=None, workspace=None, stream=None,
+                 k_exponents=None, v_exponents=None):
+    """Enqueue swa_paged_gather: the chunk's keys and values [T_q, N_kv, D] back
+    out of the pages; returns (k, v).  The workspace is one of paged_append, and
+    check_paged_append reports."""
+    p = geom if type(geom) is PagedParams else _paged_params(geom)
+    if k is None:
+        k = _empty(p.kv_shape, p.torch_dtype, k_pages, "k_pages", stream)
+    if v is None:
+        v = _empty(p.kv_shape, p.torch_dtype, k_pages, "k_pages", stream)
+    if workspace is None:
+        workspace = _empty(swa_paged_append_workspace_size(p), torch.uint8, k_pages, "k_pages", stream)
+    status = _bind().paged_gather(lib().entries["swa_paged_gather"], p.addr, k_pages, v_pages, block_table, kv_lens, k, v,
+                                  workspace, _handle(stream), k_exponents, v_exponents)
+    if status != SWA_OK:
+        _check(status)
+    return k, v
+
+
 def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, softmax_max=None, softmax_sum=None,
-                  workspace=None, stream=None):
-    """Enqueue swa_paged_forward: attention of the chunk's q [T_q, N, D] over
-    the paged cache; returns (out, softmax_max, softmax_sum)."""
+                  workspace=None, stream=None, k_exponents=None, v_exponents=None, tree=None, depth=None):
+    """Enqueue swa_paged_forward_ext: attention of the chunk's q [T_q, N, D] over
+    the paged cache; returns (out, softmax_max, softmax_sum).  k_exponents and
+    v_exponents as for paged_append.  With `tree` (int32 [T_q, words], bit c of a
+    row: the token sees token c of its chunk) and `depth` (int32 [T_q]) the chunk
+    is a tree of drafted tokens."""
     p = geom if type(geom) is PagedParams else _paged_params(geom)
     if out is None:
         out = _empty(p.q_shape, p.torch_dtype, q, "q", stream)
@@ -679,8 +728,9 @@ def paged_forward(geom, q, k_pages, v_pages, block_table, kv_lens, out=None, sof
         softmax_sum = _empty(p.stat_shape, torch.float32, q, "q", stream)
     if workspace is None:
         workspace = _empty(swa_paged_forward_workspace_size(p), torch.uint8, q, "q", stream)
-    status = _bind().paged_forward(lib().entries["swa_paged_forward"], p.addr, q, k_pages, v_pages, block_table,
-                                   kv_lens, out, softmax_max, softmax_sum, workspace, _handle(stream))
+    status = _bind().paged_forward(lib().entries["swa_paged_forward_ext"], p.addr, q, k_pages, v_pages, block_table,
+                                   kv_lens, out, softmax_max, softmax_sum, workspace, _handle(stream), k_exponents,
+                                   v_exponents, tree, depth)
     if status != SWA_OK:
         _check(status)
     return out, softmax_max, softmax_sum

@@ -137,6 +137,8 @@ class PagedGeometry:
     next_tokens: int = INT32_MAX
     sparse_mode: int = 0
     dtype: str = "bf16"
+    sink_tokens: int = 0  # BAND: tokens of a sequence's start that stay visible behind the window
+    cache_dtype: str = ""  # "": the pages hold dtype; "e4m3": 8-bit codes, with exponents beside them
 
     @property
     def n_kv(self) -> int:
@@ -145,6 +147,9 @@ class PagedGeometry:
     @property
     def T_q(self) -> int:
         return max(self.cu_seqlens_q)
+
+    def exponent_shape(self):
+        return (self.num_pages, self.n_kv, self.page_size)
 
     def page_shape(self):
         a = (self.n_kv, self.page_size) if self.cache_layout == "BNSD" else (self.page_size, self.n_kv)

@@ -388,8 +388,32 @@ typedef struct {
   int64_t next_tokens;
   int32_t sparse_mode;         /* 0 (every cached token is visible) or 4 (BAND) */
   int32_t dtype;               /* SWA_DTYPE_BF16 (0, default) or SWA_DTYPE_FP16: q, k, v, out and the
-                                  pages.  fp32 is not built (SWA_ERR_UNSUPPORTED) */
+                                  pages (unless cache_dtype says otherwise).  fp32 is not built
+                                  (SWA_ERR_UNSUPPORTED) */
+  int64_t sink_tokens;         /* BAND: the first sink_tokens tokens of a sequence stay visible behind the
+                                  window, as in swa_params_t; default 0, no effect without BAND */
+  int32_t cache_dtype;         /* swa_cache_t: what the pages hold, SWA_CACHE_SAME (0, default) or
+                                  SWA_CACHE_E4M3 (1), see "8-bit cache" */
 } swa_paged_params_t;
+
+typedef enum { SWA_CACHE_SAME = 0, SWA_CACHE_E4M3 = 1 } swa_cache_t;
+
+/* 8-bit cache (cache_dtype SWA_CACHE_E4M3).  The pages hold e4m3 codes (a sign,
+ * 4 exponent bits of bias 7, 3 mantissa bits; one byte each, page strides in
+ * bytes, still multiples of 8), and two arrays int8 [num_pages, N_kv, page_size],
+ * dense whatever the layout of the pages and starting on 16 bytes, hold an
+ * exponent per token and key/value head: the row stands for code * 2^exponent,
+ * which dtype holds exactly.
+ * swa_paged_append_ext quantises: exponent = the least integer e with
+ * max |x| <= 448 * 2^e over the row (after the rotation, in fp32), held within
+ * [-100, 7] (bf16) or [-15, 7] (fp16); code = x * 2^-e rounded once to nearest
+ * even.  Infinities and values past 448 * 2^7 = 57344 saturate there, and so may
+ * only cost their own precision and that of what is 2^-15 of them; a row with a
+ * NaN gets exponent 127.
+ * Readers take an exponent above 7 for a row of NaN, one below the least for
+ * the least; what the NaN codes (0x7F, 0xFF) stand for under another exponent
+ * is not defined (NaN or 480 * 2^e).
+ * A slot that no query of a call sees is ignored, its exponent included. */
 
 SWA_API void swa_paged_params_default(swa_paged_params_t *p);
 
@@ -422,10 +446,45 @@ SWA_API swa_status_t swa_paged_append(const swa_paged_params_t *p, const void *k
                                       void *q_out, const swa_strides_t *q_out_strides, void *workspace,
                                       size_t workspace_bytes, swa_stream_t stream);
 
+/* swa_paged_append with an 8-bit cache too.
+ *   k_exponents, v_exponents
+ *                 device, int8 [num_pages, N_kv, page_size], 16-byte aligned;
+ *                 only the chunk's slots are written.  NULL iff the cache is
+ *                 not 8-bit (swa_paged_append refuses an 8-bit cache) */
+SWA_API swa_status_t swa_paged_append_ext(const swa_paged_params_t *p, const void *k, const swa_strides_t *k_strides,
+                                          const void *v, const swa_strides_t *v_strides, void *k_pages,
+                                          const swa_page_strides_t *k_page_strides, void *v_pages,
+                                          const swa_page_strides_t *v_page_strides, int8_t *k_exponents,
+                                          int8_t *v_exponents, const int32_t *block_table, int64_t table_stride,
+                                          const int32_t *kv_lens, const swa_rope_params_t *rope,
+                                          const int32_t *positions, const void *q, const swa_strides_t *q_strides,
+                                          void *q_out, const swa_strides_t *q_out_strides, void *workspace,
+                                          size_t workspace_bytes, swa_stream_t stream);
+
+/* Read a chunk's keys and values back from the cache, 16-bit or 8-bit: what
+ * swa_paged_append stored (N, scale, window and sinks are not used).  With
+ * chunks as long as the sequences it copies those out whole.
+ *   k_pages, v_pages, k_exponents, v_exponents, block_table, table_stride, kv_lens
+ *                 as for swa_paged_append_ext; read only
+ *   k, v          device, p->dtype, [T_q, N_kv, D]; must not overlap the pages.
+ *                 Tokens that do not exist in the cache, and those of a page
+ *                 number or length out of range, come back as zeros
+ *   workspace     as for swa_paged_append (swa_paged_append_workspace_size;
+ *                 swa_paged_append_status reports)
+ * Errors: as swa_paged_append. */
+SWA_API swa_status_t swa_paged_gather(const swa_paged_params_t *p, const void *k_pages,
+                                      const swa_page_strides_t *k_page_strides, const void *v_pages,
+                                      const swa_page_strides_t *v_page_strides, const int8_t *k_exponents,
+                                      const int8_t *v_exponents, const int32_t *block_table, int64_t table_stride,
+                                      const int32_t *kv_lens, void *k, const swa_strides_t *k_strides, void *v,
+                                      const swa_strides_t *v_strides, void *workspace, size_t workspace_bytes,
+                                      swa_stream_t stream);
+
 /* Attention of a chunk over the cache (which holds the chunk's own tokens
  * too): swa_forward's formula with query i of sequence b at position
  * p = kv_lens[b] - q_len_b + i, which sees key j iff p - pre_tokens <= j <=
- * p + next_tokens and 0 <= j < kv_lens[b] (mode 4), or every key (mode 0).  A
+ * p + next_tokens and 0 <= j < kv_lens[b] (mode 4; with sink_tokens also the
+ * keys j < sink_tokens up to p + next_tokens), or every key (mode 0).  A
  * row that sees no key gets out = 0, softmax_max = -inf, softmax_sum = 0.
  * Scores, statistics and sums are fp32; exp(scale q.k - maximum) is rounded to
  * p->dtype before the product with V, as in swa_forward, and out once more.
@@ -452,6 +511,42 @@ SWA_API swa_status_t swa_paged_forward(const swa_paged_params_t *p, const void *
                                        const int32_t *block_table, int64_t table_stride, const int32_t *kv_lens,
                                        void *out, float *softmax_max, float *softmax_sum, void *workspace,
                                        size_t workspace_bytes, swa_stream_t stream);
+
+/* The same with an 8-bit cache, and of a chunk that is a tree of drafted tokens
+ * (speculative decoding: several continuations in one call).
+ *
+ * Tree.  Row t of `tree` has bit c (bit c mod 32 of word c / 32) set iff chunk
+ * token t of its sequence sees token c of the same chunk: its ancestors and
+ * itself, or whatever the caller chooses; bits from the chunk's length on are
+ * ignored, and a row may be empty.  Of the keys before the chunk a token sees
+ * those that swa_paged_forward's formula gives for position kv_lens[b] - q_len_b +
+ * depth, depth[t] being its distance from the root (held within [0, q_len_b - 1]);
+ * with next_tokens >= 0, as a tree needs, that is its window and the sinks.  The
+ * tree alone decides on the chunk's own keys.  The slots hold the chunk in its
+ * order, whatever the depths: its tokens are appended as they come, rotated by
+ * `positions` of kv_lens[b] - q_len_b + depth.  What is read: pages of keys from
+ * the root's window on, the sinks' and the chunk's, every slot of the chunk
+ * counting as seen.  Afterwards the accepted tokens are appended again in their
+ * order, over the chunk.
+ *   extra         NULL, or host; the pointers in it are device memory:
+ *     k_exponents, v_exponents
+ *                 as for swa_paged_append_ext; NULL iff the cache is not 8-bit
+ *     tree        uint32 [T_q, words], rows tree_stride words apart (0: the words
+ *                 of the longest chunk, ceil(q_len / 32)); NULL: no tree
+ *     depth       int32 [T_q], or NULL: the token's place in its chunk */
+typedef struct {
+  const int8_t *k_exponents, *v_exponents;
+  const uint32_t *tree;
+  int64_t tree_stride;
+  const int32_t *depth;
+} swa_paged_extra_t;
+SWA_API swa_status_t swa_paged_forward_ext(const swa_paged_params_t *p, const void *q, const swa_strides_t *q_strides,
+                                           const void *k_pages, const swa_page_strides_t *k_page_strides,
+                                           const void *v_pages, const swa_page_strides_t *v_page_strides,
+                                           const swa_paged_extra_t *extra, const int32_t *block_table,
+                                           int64_t table_stride, const int32_t *kv_lens, void *out,
+                                           float *softmax_max, float *softmax_sum, void *workspace,
+                                           size_t workspace_bytes, swa_stream_t stream);
 
 /* Wait for `stream`, then report what the last paged call that used
  * `workspace` met on the device: SWA_OK, SWA_ERR_PAGE (a length or page number
