@@ -26,7 +26,7 @@ CHECKED_LIB_PATH = os.path.join(PKG, "libswa_checked.so")
 BIND_SOURCE = "swa_bind.cpp"
 SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_pair.cu", "swa_bwd_dkv.cu", "swa_bwd_dq.cu", "swa_aux.cu",
            "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged_rows_masks.cu",
-           "swa_paged_rows_e4m3.cu", "swa_paged_tile.cu", "swa_paged_tile_masks.cu", "swa_paged_tile_e4m3.cu",
+           "swa_paged_rows_e4m3.cu", "swa_paged_tile.cu", "swa_paged_tile_masks.cu", "swa_paged_unpack.cu",
            "swa_paged_join.cu", "swa_paged_gather.cu", "swa_paged.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -4,7 +4,6 @@
 #include <cmath>
 #include <cstring>
 #include <memory>
-#include <type_traits>
 
 #include "swa_paged.h"
 #include "swa_turn.h"
@@ -19,10 +18,16 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is b
 // does not hold a batch up.  201 sequences of up to 2000 keys and one of 131072:
 // 358 us, 354 with 8192 (twice the CTAs, most with nothing to do), 408 with 4096.
 constexpr int64_t kRowsMostKeys = 16384;
+// The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 202 us, 206 with
+// 4096, 220 with 1024, 250 with 16384; one of 131072: 54 us (76 splits either way).
+constexpr int64_t kRows8MostKeys = 2048;
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
 constexpr int64_t kTailSteps = 12;  // key tiles that splitting a last round must save (0.76 us each)
 constexpr double kLog2e = 1.4426950408889634;
+// Pages of 16-bit values that an 8-bit cache is unpacked into at a time, in all sequences of a pass together
+// (one sequence may take more).
+constexpr int64_t kScratchBytes = int64_t(1) << 30;
 constexpr int64_t kGatherWaves = 8;  // CTAs per SM that a gather spreads its tokens over, before a CTA takes several
 
 template <typename... A>
@@ -410,25 +415,30 @@ swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, cons
 }
 
 // Tensor map of the pages: boxes of `box_rows` slots x 64 columns, 128-byte
-// swizzle; columns past D and pages past the last read as zeros.
+// swizzle (8-bit: x 64 or 128 columns, a swizzle of as many bytes); columns past
+// D and pages past the last read as zeros.
 swa_status_t page_map(CUtensorMap* m, PageDims* dims, const void* ptr, const swa_page_strides_t& s,
                       const swa_paged_params_t* p, int64_t N_kv, int box_rows, const char* name) {
   auto fn = encode_fn();
   if (!fn) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const PageOrder o = page_order(s, p, N_kv);
+  const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
+  const cuuint32_t columns = q8 && p->D > 64 ? 128 : 64;
   cuuint64_t d[4] = {static_cast<cuuint64_t>(p->D)}, st[3];
-  cuuint32_t box[4] = {64, 1, 1, 1};
+  cuuint32_t box[4] = {columns, 1, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   for (int i = 0; i < 3; ++i) {
     d[i + 1] = static_cast<cuuint64_t>(o.n[i]);
-    st[i] = static_cast<cuuint64_t>(o.stride[i]) * 2;
+    st[i] = static_cast<cuuint64_t>(o.stride[i]) * (q8 ? 1 : 2);
   }
   box[o.at[0]] = static_cast<cuuint32_t>(box_rows);
   *dims = PageDims{o.at[0], o.at[1], o.at[2]};
-  const CUresult r = fn(m, p->dtype == SWA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        4, const_cast<void*>(ptr), d, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapDataType type =
+      q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+         : (p->dtype == SWA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+  const CUresult r = fn(m, type, 4, const_cast<void*>(ptr), d, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        q8 && columns == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SWA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", name, (int)r);
   return SWA_OK;
 }
@@ -439,9 +449,11 @@ swa_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
   return SWA_OK;
 }
 
-// Launch on the sequences (in `order`, or as they come) that `take` fills an entry for, at most CAP of them per table.
-template <int CAP, typename Take, typename Launch>
-cudaError_t each_table(const PagedPlan& plan, const std::vector<int32_t>& order, Take&& take, Launch&& launch) {
+// Launch on the sequences (in `order`, or as they come) that `take` fills an entry for, at most CAP of them per
+// table, and none that is `full` for the table so far.
+template <int CAP, typename Take, typename Launch, typename Full>
+cudaError_t each_table(const PagedPlan& plan, const std::vector<int32_t>& order, Take&& take, Launch&& launch,
+                       Full&& full) {
   static thread_local std::unique_ptr<PagedTable<CAP>> storage;
   if (!storage) storage.reset(new PagedTable<CAP>());
   PagedTable<CAP>& tab = *storage;
@@ -455,7 +467,12 @@ cudaError_t each_table(const PagedPlan& plan, const std::vector<int32_t>& order,
   for (size_t x = 0; x < plan.len.size(); ++x) {
     const int32_t b = order.empty() ? static_cast<int32_t>(x) : order[x];
     PagedDesc d{};
-    if (plan.len[b] == 0 || !take(b, d, tab)) continue;
+    if (plan.len[b] == 0) continue;
+    if (tab.count > 0 && full(b)) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return e;
+    }
+    if (!take(b, d, tab)) continue;
     tab.d[tab.count++] = d;
     if (tab.count == CAP) {
       const cudaError_t e = flush();
@@ -492,8 +509,9 @@ cudaError_t over_tokens(const swa_paged_params_t* p, const PagedPlan& plan, int6
     const int64_t begin = tab.d[0].q_start, end = last.q_start + last.q_len;
     return go(tab, begin, end, static_cast<int>(ceil_div(end - begin, tok)));
   };
-  return live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, one)
-                                                  : each_table<kPagedLargeTable>(plan, {}, take, one);
+  auto never = [](int) { return false; };
+  return live_sequences(plan) <= kPagedSmallTable ? each_table<kPagedSmallTable>(plan, {}, take, one, never)
+                                                  : each_table<kPagedLargeTable>(plan, {}, take, one, never);
 }
 
 // Workspace of an append or a gather call: the header and one page status per token.
@@ -503,20 +521,38 @@ size_t append_bytes(const swa_paged_params_t* p) { return kHeaderBytes + round25
 // The row tiles and splits of one kernel over the sequences it takes.
 struct Part {
   int64_t gs = 1, tok = 1, rows = 0;  // heads and tokens of a tile, rows of a partial
+  int64_t most = 0;                   // rows that some tile has
   int64_t items = 0, splits = 1, par = 1, cap = 1, least = 1, step = 1;
   int64_t whole = 0;  // items that are one unit each (tiles); the others are split
   bool cluster = false;
   size_t status_at = 0, ml_at = 0, o_at = 0;  // workspace offsets
   int64_t units() const { return whole + (items - whole) * splits; }
 };
+// The row tiles' keys of an 8-bit cache, unpacked: in passes over some of the
+// sequences each, one after the other, so that the pages of a pass fit the scratch.
+struct Scratch {
+  std::vector<int64_t> pages;  // per sequence, at most
+  int64_t held = 0;            // pages of the scratch
+  int64_t total = 0;           // of all passes
+  int64_t entries = 0;         // columns of its block table
+  size_t status_at = 0, table_at = 0, k_at = 0, v_at = 0;
+};
 struct ForwardPlan {
   PagedPlan seq;
+  Scratch scratch;
   // sequences with at most 16 query rows per key/value head (chunk length x
   // group), and the others
   Part rows, tile;
   size_t total = 0;
 };
 bool few_rows(int64_t q_len, int64_t group) { return q_len * group <= kRowsTile; }
+// The sequences with row tiles, long chunks first: they tend to hold the heaviest tiles.
+std::vector<int32_t> tile_order(const PagedPlan& seq) {
+  std::vector<int32_t> order(seq.len.size());
+  for (size_t b = 0; b < order.size(); ++b) order[b] = static_cast<int32_t>(b);
+  std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seq.len[x] > seq.len[y]; });
+  return order;
+}
 
 // Tensor map of q: boxes of the tile's tokens x heads x 64 columns, heads
 // innermost, as the rows of a tile go.  *usable = 0 where the row stride is not
@@ -547,6 +583,28 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   if (st != SWA_OK) return st;
   const int64_t G = p->N / f.seq.N_kv, DP = p->D <= 64 ? 64 : 128;
   f.total = kHeaderBytes;
+  Scratch& sc = f.scratch;
+  if (p->cache_dtype == SWA_CACHE_E4M3) {
+    sc.entries = ceil_div(f.seq.max_kv, kPagedTileStep);
+    sc.pages.assign(f.seq.len.size(), 0);
+    int64_t most = 0;
+    for (size_t b = 0; b < f.seq.len.size(); ++b) {
+      const int64_t n = f.seq.len[b];
+      if (n == 0 || few_rows(n, G)) continue;
+      sc.pages[b] = sc.entries;
+      if (p->sparse_mode == 4) {  // the window of a chunk (or a tree, which sees as far as its deepest token), and the sinks
+        const long double w = (long double)p->pre_tokens + (long double)std::max<int64_t>(p->next_tokens, 0) + (long double)n;
+        const int64_t sinks = ceil_div(std::min(p->sink_tokens, f.seq.max_kv), kPagedTileStep);
+        if (w < (long double)f.seq.max_kv)
+          sc.pages[b] = std::min(sc.entries, ceil_div(std::max<int64_t>(static_cast<int64_t>(w), 1), kPagedTileStep) + 1 + sinks);
+      }
+      sc.total += sc.pages[b];
+      most = std::max(most, sc.pages[b]);
+    }
+    const int64_t page_bytes = 2 * f.seq.N_kv * kPagedTileStep * p->D * 2;
+    sc.held = std::min(sc.total, std::max(most, kScratchBytes / page_bytes));
+    if (sc.total > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many keys for one call");
+  }
   auto lay_out = [&](Part& part, bool few, int64_t most_rows, int64_t step) {
     part.gs = divisor_up_to(G, most_rows);
     part.tok = most_rows / part.gs;
@@ -554,7 +612,10 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
     part.step = step;
     part.items = 0;
     for (int64_t n : f.seq.len)
-      if (few_rows(n, G) == few) part.items += ceil_div(n, part.tok) * (p->N / part.gs);
+      if (few_rows(n, G) == few) {
+        part.items += ceil_div(n, part.tok) * (p->N / part.gs);
+        part.most = std::max(part.most, std::min(n, part.tok) * part.gs);
+      }
     // keys a tile can see, in steps (one more: a run may begin inside a step)
     int64_t keys = f.seq.max_kv;
     if (p->sparse_mode == 4) {
@@ -572,8 +633,11 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       // the items are as many.  Measured (64 items of 8192 keys): 49 us in 128
       // CTAs, 48 in 256, 60 in 320, which start a second wave; 8 items of
       // 131072 keys: 83 us in 152, 92 in 304.
-      part.par = std::min(ceil_div(int64_t(kSms), items), steps);
-      part.cap = kRowsMostKeys / step + 2;
+      // An 8-bit cache: four CTAs an SM, each of which draws 11 GB/s, and so shorter
+      // runs (kRows8MostKeys).
+      const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
+      part.par = std::min(ceil_div(int64_t(kSms) * (q8 ? 4 : 1), items), steps);
+      part.cap = (q8 ? kRows8MostKeys : kRowsMostKeys) / step + 2;
       part.least = 1;
       // Up to 8 splits are one cluster, which joins them without a second
       // launch: a power of two of CTAs, all resident at once.  One token of
@@ -602,7 +666,8 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       for (int64_t n : f.seq.len) longest = std::max(longest, few_rows(n, G) ? 0 : n);
       const int64_t sure = std::min(keys, std::max<int64_t>(f.seq.max_kv - longest, 0)) / step;
       const int64_t last = part.items % kSms;
-      const bool one_launch = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedLargeTable;
+      const bool one_launch = sc.held == sc.total && ((f.seq.uniform > 0 && sc.total == 0) ||
+                                                      live_sequences(f.seq) <= kPagedLargeTable);
       if (part.items <= kSms / 2) {
         part.par = std::min(kSms / items, ceil_div(steps, part.least));
       } else if (one_launch && part.items > kSms && last > 0 && last <= kSms / 2) {
@@ -625,12 +690,17 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
   };
   lay_out(f.rows, true, kRowsTile, kRowsStep);
   lay_out(f.tile, false, kPagedTileRows, kPagedTileStep);
+  if (sc.total > 0) {
+    const size_t half = static_cast<size_t>(sc.held) * f.seq.N_kv * kPagedTileStep * p->D * 2;
+    sc.status_at = f.total;
+    sc.table_at = sc.status_at + round256(static_cast<size_t>(sc.total) * 4);
+    sc.k_at = sc.table_at + round256(static_cast<size_t>(p->B) * sc.entries * 4);
+    sc.v_at = sc.k_at + round256(half);
+    f.total = sc.v_at + round256(half);
+  }
   if (f.rows.items > 2147483647 || f.tile.items > 2147483647) return fail(SWA_ERR_PARAM_INVALID, "too many query rows for one call");
   return SWA_OK;
 }
-
-template <PagedKind K>
-using Kind = std::integral_constant<PagedKind, K>;
 
 template <int CAP>
 cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Part& part, PagedArgs a,
@@ -649,26 +719,63 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
   a.least = static_cast<int32_t>(part.least);
   a.cluster = part.cluster ? 1 : 0;
   a.rows_pad = static_cast<int32_t>(part.rows);
+  a.most_rows = static_cast<int32_t>(part.most);
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
   a.page_err = reinterpret_cast<int32_t*>(ws + part.status_at);
   a.part_ml = reinterpret_cast<float2*>(ws + part.ml_at);
   a.part_o = reinterpret_cast<float*>(ws + part.o_at);
+  // The sequences of `tab` unpacked into the scratch; `a` reads its pages from then on.
+  const PagedArgs packed = a;
+  int64_t unpacked = 0;  // pages of the passes before
+  auto unpack = [&](const PagedTable<CAP>& tab) {
+    const Scratch& sc = f.scratch;
+    UnpackArgs u{};
+    u.k = ws + sc.k_at;
+    u.v = ws + sc.v_at;
+    u.table = reinterpret_cast<int32_t*>(ws + sc.table_at);
+    u.table_stride = sc.entries;
+    while ((16 << u.lane_shift) < p->D) ++u.lane_shift;
+    u.lanes = 1 << u.lane_shift;
+    PagedTable<CAP> pages = tab;
+    int64_t n = 0;
+    for (int32_t x = 0; x < pages.count; ++x) {
+      pages.d[x].item_begin = static_cast<int32_t>(n);
+      n += pages.d[x].tiles = static_cast<int32_t>(sc.pages[pages.d[x].b]);
+    }
+    PagedArgs from = packed;
+    from.page_err = reinterpret_cast<int32_t*>(ws + sc.status_at);
+    from.clear_err = a.clear_err;
+    u.status_base = unpacked;
+    const cudaError_t e = launch_paged_unpack(from, pages, u, static_cast<int>(n), s);
+    unpacked += n;
+    a.clear_err = 0;
+    a.k_pages = u.k;
+    a.v_pages = u.v;
+    a.g.k_exp = a.g.v_exp = nullptr;
+    a.g.table = u.table;
+    a.g.table_stride = sc.entries;
+    a.g.page_size = kPagedTileStep;
+    a.g.num_pages = static_cast<int32_t>(sc.held);
+    a.g.n_table = p->B * sc.entries;
+    return e;
+  };
   auto go = [&](PagedTable<CAP>& tab) {
     cudaError_t e = cudaSuccess;
-    // calls without sinks, tree and 8-bit cache run the kernels that know nothing of them
-    const PagedKind kind = a.g.k_exp ? PagedKind::kE4m3 : (a.sinks > 0 || a.tree ? PagedKind::kMasks : PagedKind::kPlain);
-    auto launch = [&](auto k) {
-      return few ? launch_paged_rows<k.value>(a, tab, s) : launch_paged_tile<k.value>(a, tab, mk, mv, mq, s);
-    };
+    // calls without sinks and tree run the kernels that know nothing of them
+    const bool masks = a.sinks > 0 || a.tree;
+    if (!joins && !few && f.scratch.total > 0) e = unpack(tab);
+    if (e != cudaSuccess) return e;
     if (joins) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
-    else if (kind == PagedKind::kPlain) e = launch(Kind<PagedKind::kPlain>{});
-    else if (kind == PagedKind::kMasks) e = launch(Kind<PagedKind::kMasks>{});
-    else e = launch(Kind<PagedKind::kE4m3>{});
+    else if (!few) e = masks ? launch_paged_tile<PagedKind::kMasks>(a, tab, mk, mv, mq, s)
+                             : launch_paged_tile<PagedKind::kPlain>(a, tab, mk, mv, mq, s);
+    else if (a.g.k_exp) e = launch_paged_rows_e4m3(a, tab, mk, mv, s);
+    else e = masks ? launch_paged_rows<PagedKind::kMasks>(a, tab, s) : launch_paged_rows<PagedKind::kPlain>(a, tab, s);
     a.item_base += tab.n_items;
     a.clear_err = 0;
     return e;
   };
-  if (f.seq.uniform > 0) {
+  const bool scratch = !few && f.scratch.total > 0;
+  if (f.seq.uniform > 0 && !scratch) {
     PagedTable<CAP> tab{};
     tab.count = 1;
     tab.d[0].q_len = static_cast<int32_t>(f.seq.uniform);
@@ -677,8 +784,10 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     tab.n_items = static_cast<int32_t>(part.items);
     return go(tab);
   }
+  int64_t held = 0;  // pages of the scratch that the table's sequences take
   auto take = [&](int b, PagedDesc& d, PagedTable<CAP>& tab) {
     if (few_rows(f.seq.len[b], a.group) != few) return false;
+    if (scratch) held = (tab.count == 0 ? 0 : held) + f.scratch.pages[b];
     d.q_start = static_cast<int32_t>(f.seq.start[b]);
     d.q_len = static_cast<int32_t>(f.seq.len[b]);
     d.b = b;
@@ -687,14 +796,10 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     tab.n_items += d.tiles * a.groups;
     return true;
   };
-  // long chunks first: they tend to hold the heaviest tiles
   std::vector<int32_t> order;
-  if (!few) {
-    order.resize(f.seq.len.size());
-    for (size_t b = 0; b < order.size(); ++b) order[b] = static_cast<int32_t>(b);
-    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return f.seq.len[x] > f.seq.len[y]; });
-  }
-  return each_table<CAP>(f.seq, order, take, go);
+  if (!few) order = tile_order(f.seq);
+  auto full = [&](int b) { return scratch && !few_rows(f.seq.len[b], a.group) && held + f.scratch.pages[b] > f.scratch.held; };
+  return each_table<CAP>(f.seq, order, take, go, full);
 }
 
 // The first page status of n words at `at` that is not 0.
@@ -949,32 +1054,55 @@ swa_status_t swa_paged_forward_ext(const swa_paged_params_t* p, const void* q, c
     a.n_stats = less_slack(p->T_q * p->N);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    CUtensorMap mk{}, mv{}, mq{};
+    CUtensorMap mk{}, mv{}, mq{}, rk{}, rv{};
+    if (f.rows.items > 0 && a.g.k_exp && a.g.wide) {  // groups of 16 slots, for the few-row kernel
+      st = page_map(&rk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv, 16,
+                    "k_pages");
+      if (st == SWA_OK)
+        st = page_map(&rv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv, 16,
+                      "v_pages");
+      if (st != SWA_OK) return st;
+    }
+    PageDims rows_kd = a.kd, rows_vd = a.vd;
     if (f.tile.items > 0) {
-      const int64_t low = p->page_size & -p->page_size;
+      swa_paged_params_t of = *p;  // the pages that the tiles read
+      swa_page_strides_t ks{a.g.k_page, a.g.k_head, a.g.k_slot}, vs{a.g.v_page, a.g.v_head, a.g.v_slot};
+      const void *kp = k_pages, *vp = v_pages;
+      if (f.scratch.total > 0) {
+        kp = static_cast<uint8_t*>(workspace) + f.scratch.k_at;
+        vp = static_cast<uint8_t*>(workspace) + f.scratch.v_at;
+        of.cache_dtype = SWA_CACHE_SAME;
+        of.page_size = kPagedTileStep;
+        of.num_pages = f.scratch.held;
+        ks = vs = swa_page_strides_t{f.seq.N_kv * kPagedTileStep * p->D, kPagedTileStep * p->D, p->D};
+      }
+      const int64_t low = of.page_size & -of.page_size;
       a.box_rows = static_cast<int32_t>(std::min<int64_t>(low, kPagedTileStep));
-      if (!a.g.k_exp)
-        st = page_map(&mk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv,
-                      a.box_rows, "k_pages");
-      if (!a.g.k_exp && st == SWA_OK)
-        st = page_map(&mv, &a.vd, v_pages, swa_page_strides_t{a.g.v_page, a.g.v_head, a.g.v_slot}, p, f.seq.N_kv,
-                      a.box_rows, "v_pages");
+      st = page_map(&mk, &a.kd, kp, ks, &of, f.seq.N_kv, a.box_rows, "k_pages");
+      if (st == SWA_OK) st = page_map(&mv, &a.vd, vp, vs, &of, f.seq.N_kv, a.box_rows, "v_pages");
       if (st == SWA_OK) st = query_map(&mq, &a.q_tma, q, qs, p, f.tile);
       if (st != SWA_OK) return st;
     }
     if (SWA_CHECKS) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
-    const bool small = f.seq.uniform > 0 || live_sequences(f.seq) <= kPagedSmallTable;
+    const bool small = (f.seq.uniform > 0 && f.scratch.total == 0) || live_sequences(f.seq) <= kPagedSmallTable;
     auto run = [&](const Part& part, bool joins) {
       if (part.items == 0 || e != cudaSuccess || (joins && (part.splits <= 1 || part.cluster))) return;
-      e = small ? run_part<kPagedSmallTable>(p, f, part, a, mk, mv, mq, joins, s)
-                : run_part<kPagedLargeTable>(p, f, part, a, mk, mv, mq, joins, s);
+      const bool few = &part == &f.rows;
+      const CUtensorMap &k = few ? rk : mk, &v = few ? rv : mv;
+      if (few && a.g.k_exp) {
+        a.kd = rows_kd;
+        a.vd = rows_vd;
+      }
+      e = small ? run_part<kPagedSmallTable>(p, f, part, a, k, v, mq, joins, s)
+                : run_part<kPagedLargeTable>(p, f, part, a, k, v, mq, joins, s);
       a.clear_err = 0;
     };
     // A batch of both kinds whose tables fit one launch each: the few-row kernel
     // takes the SMs that the other leaves.  The joins come last: each waits for
     // the grid before it, and that one for the tiles.
-    const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable;
+    const bool both = f.tile.items > 0 && f.rows.items > 0 && live_sequences(f.seq) <= kPagedLargeTable &&
+                      f.scratch.held == f.scratch.total;
     a.signal = both ? 1 : 0;
     run(f.tile, false);
     a.overlap = both ? 1 : 0;
@@ -1058,6 +1186,7 @@ swa_status_t swa_paged_forward_status(const swa_paged_params_t* p, const void* w
     st = swa_workspace_status(workspace, stream);
     for (const Part* part : {&f.rows, &f.tile})
       if (st == SWA_OK) st = read_pages(part->units(), workspace, part->status_at);
+    if (st == SWA_OK) st = read_pages(f.scratch.total, workspace, f.scratch.status_at);
     return st;
   });
 }

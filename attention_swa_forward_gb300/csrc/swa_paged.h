@@ -138,6 +138,7 @@ struct PagedArgs {
   int32_t par, cap, least;  // paged_split
   int32_t cluster;    // few-row kernel: the splits are a cluster, which joins them itself
   int32_t rows_pad;   // rows of a partial tile
+  int32_t most_rows;  // rows that some tile has
   int32_t stall;      // test hook (kStallPaged)
   int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128
   PageDims kd, vd;
@@ -262,16 +263,31 @@ constexpr int kRowsStep = 64;     // keys per step of the few-row kernel (4 warp
 constexpr int kPagedTileRows = 128;  // rows of a tile of the tensor-memory kernel
 constexpr int kPagedTileStep = 128;  // keys per step of it
 
-// What a kernel can do beside the window over a 16-bit cache: sinks and trees
-// (extended masks), and those over an 8-bit cache.  Each is a translation unit
-// of its own, and calls that need neither run what they ran without them.
-enum class PagedKind { kPlain, kMasks, kE4m3 };
+// What a kernel can do beside the window: sinks and trees (extended masks).
+// Each is a translation unit of its own, and calls that need neither run what
+// they ran without them.
+enum class PagedKind { kPlain, kMasks };
 
 template <PagedKind KIND, int CAP>
 cudaError_t launch_paged_rows(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream);
+template <int CAP>
+cudaError_t launch_paged_rows_e4m3(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk,
+                                   const CUtensorMap& mv, cudaStream_t stream);
 template <PagedKind KIND, int CAP>
 cudaError_t launch_paged_tile(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk,
                               const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t stream);
+// The keys that row tiles see of an 8-bit cache as 16-bit pages of 128 slots.
+struct UnpackArgs {
+  void *k, *v;           // [page][N_kv][128][D]
+  int32_t* table;        // the block table of those pages
+  int64_t table_stride;
+  int64_t status_base;   // the pages' status words, behind the attention's
+  int32_t lanes, lane_shift;  // threads of a row: a power of two
+};
+// An entry's `item_begin` and `tiles` count pages here.
+template <int CAP>
+cudaError_t launch_paged_unpack(const PagedArgs& a, const PagedTable<CAP>& tab, const UnpackArgs& u, int pages,
+                                cudaStream_t stream);
 // Join the splits' partial results; `step_keys` as of the kernel that wrote them.
 template <int CAP>
 cudaError_t launch_paged_join(const PagedArgs& a, const PagedTable<CAP>& tab, int step_keys, cudaStream_t stream);

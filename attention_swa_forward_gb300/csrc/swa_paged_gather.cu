@@ -122,13 +122,9 @@ __global__ void __launch_bounds__(kGatherThreads)
       uint16_t* p = static_cast<uint16_t*>(a.dst[w.x]) + w.dst;
       if constexpr (Q8) {
         const uint32_t f = exp_factor<F16>(e[y]) * 0x10001u;
-        uint4 lo, hi;
-        codes4<F16>(in[y].x, lo.x, lo.y);
-        codes4<F16>(in[y].y, lo.z, lo.w);
-        codes4<F16>(in[y].z, hi.x, hi.y);
-        codes4<F16>(in[y].w, hi.z, hi.w);
-        lo = make_uint4(mul2<F16>(lo.x, f), mul2<F16>(lo.y, f), mul2<F16>(lo.z, f), mul2<F16>(lo.w, f));
-        hi = make_uint4(mul2<F16>(hi.x, f), mul2<F16>(hi.y, f), mul2<F16>(hi.z, f), mul2<F16>(hi.w, f));
+        const uint2 a0 = values4<F16>(in[y].x, f), a1 = values4<F16>(in[y].y, f);
+        const uint2 a2 = values4<F16>(in[y].z, f), a3 = values4<F16>(in[y].w, f);
+        const uint4 lo = make_uint4(a0.x, a0.y, a1.x, a1.y), hi = make_uint4(a2.x, a2.y, a3.x, a3.y);
         if (in_bounds(w.dst, 8, a.n_dst[w.x], a.err)) __stcs(reinterpret_cast<uint4*>(p), lo);
         if (c + 8 < g.D && in_bounds(w.dst + 8, 8, a.n_dst[w.x], a.err)) __stcs(reinterpret_cast<uint4*>(p + 8), hi);
       } else {

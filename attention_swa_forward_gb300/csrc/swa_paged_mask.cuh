@@ -6,6 +6,39 @@
 
 namespace swa {
 
+// Accesses to shared memory by 32-bit addresses: after the alignment of its base
+// the compiler no longer knows where a pointer points, and generic accesses wait
+// for more (a chunk over the 8-bit cache took 598 us with them, FILL without).
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int lds_s8(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Position of token i of the chunk.  A depth outside the chunk counts as the nearest inside.
 __device__ __forceinline__ int token_position(const PagedArgs& a, const PagedItem& w, int kv_len, int i) {
   int at = i;
@@ -34,13 +67,18 @@ __device__ __forceinline__ uint32_t tree_bits(const PagedArgs& a, const PagedIte
 // and its row's exponent e stand for code 2^e, which the 16-bit types hold
 // exactly over the exponents that a row may have.
 //
-// bf16: the code's exponent and mantissa bits, moved to the low exponent bits
-// and the high mantissa bits of a bf16, are the code's value times 2^-120 (the
-// formats' biases differ by 120; subnormals too, whose rule is the same); a
-// multiplication by 2^(120 + e) gives the value.  fp16: the conversion
-// instruction gives the code's value, and a multiplication by 2^e the rest.
+// The conversion instruction gives a pair of codes as fp16, exactly.  What reads a
+// row back multiplies by 2^e (fp16), or by 2^(e + 112) after moving the fp16 bits
+// to the places of a bf16, whose exponents' bias is 112 higher.  Attention over
+// an 8-bit cache multiplies in fp16 whatever the type of q: codes are exact there,
+// q is brought into its range row by row, and the exponents go into the scores
+// and the weights.
+//
+// (Codes as bf16 in the attention kernels: the integer instructions that move the
+// bits, 3 to 4 a pair at half the rate of others, set the time: 64 single tokens of
+// 100 to 16384 keys 448 us, a chunk of 1024 tokens behind 15360 633.)
 
-// 2^(120 + e) as bf16 bits, or 2^e as fp16 bits; NaN for an exponent above the most.
+// 2^(112 + e) as bf16 bits, or 2^e as fp16 bits; NaN for an exponent above the most.
 template <bool F16>
 __device__ __forceinline__ uint32_t exp_factor(int e) {
   if (e > kExpMost) return F16 ? 0x7E00u : 0x7FC0u;
@@ -48,8 +86,13 @@ __device__ __forceinline__ uint32_t exp_factor(int e) {
     e = max(e, kExpLeastF16);
     return e < -14 ? 0x0200u : static_cast<uint32_t>(e + 15) << 10;
   } else {
-    return static_cast<uint32_t>(max(e, kExpLeastBf16) + 247) << 7;
+    return static_cast<uint32_t>(max(e, kExpLeastBf16) + 239) << 7;
   }
+}
+// 2^e in fp32: 0 below its normal range, NaN above kExpMost.
+__device__ __forceinline__ float exp_f32(int e, int shift) {
+  const int x = max(e, kExpLeastBf16) + shift + 127;
+  return e > kExpMost ? __int_as_float(0x7FC00000) : __int_as_float(max(x, 0) << 23);
 }
 // Elementwise product of two pairs.
 template <bool F16>
@@ -59,32 +102,33 @@ __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
   else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-// bf16: the pair of codes in bytes 1 and 3 of x, times 2^-120.
-__device__ __forceinline__ uint32_t codes_high(uint32_t x) {
-  return ((x & 0x7F007F00u) >> 4) | (x & 0x80008000u);
-}
-// fp16: the pair of codes in the low two bytes of x.
+// The pair of codes in the low two bytes of x as fp16.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
   uint32_t r;
   asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(x));
   return r;
 }
-// Codes a (low half) and b (high half) of bytes `at` of x and y, as a pair; not yet times 2^e.
-template <bool F16>
+// Codes `at` of x (low half) and of y (high half).
 __device__ __forceinline__ uint32_t codes_of(uint32_t x, uint32_t y, int at) {
-  if constexpr (F16) return codes_f16(__byte_perm(x, y, static_cast<uint32_t>(at | (4 + at) << 4)));
-  else return codes_high(__byte_perm(x, y, static_cast<uint32_t>(at << 4 | (4 + at) << 12)));
+  return codes_f16(__byte_perm(x, y, static_cast<uint32_t>(at | (4 + at) << 4)));
 }
-// The four codes of x in order: pairs (0, 1) and (2, 3).
+// The values of the four codes of x, times the factor that exp_factor gives.
 template <bool F16>
-__device__ __forceinline__ void codes4(uint32_t x, uint32_t& p01, uint32_t& p23) {
-  if constexpr (F16) {
-    p01 = codes_f16(x);
-    p23 = codes_f16(x >> 16);
-  } else {
-    p01 = codes_high(__byte_perm(x, 0, 0x1000));
-    p23 = codes_high(__byte_perm(x, 0, 0x3020));
+__device__ __forceinline__ uint2 values4(uint32_t x, uint32_t factor) {
+  uint32_t lo = codes_f16(x), hi = codes_f16(x >> 16);
+  if constexpr (!F16) {  // 5 exponent bits and 3 of the mantissa, 3 places lower (a NaN stays one or becomes 480)
+    lo = ((lo & 0x7FFF7FFFu) >> 3 & 0x0FFF0FFFu) | (lo & 0x80008000u);
+    hi = ((hi & 0x7FFF7FFFu) >> 3 & 0x0FFF0FFFu) | (hi & 0x80008000u);
   }
+  return make_uint2(mul2<F16>(lo, factor), mul2<F16>(hi, factor));
 }
+// The power of two that brings a row of magnitude `top` (bits of |x|) to [2^14, 2^15),
+// as far as 2^+-100 go: its fp16 values then lose nothing of a bf16's 8 bits
+// down to 2^-29 of the largest.
+__device__ __forceinline__ int row_shift(uint32_t top) {
+  const int e = static_cast<int>(top >> 23) - 127;
+  return min(max(14 - e, -100), 100);
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
 
 }  // namespace swa

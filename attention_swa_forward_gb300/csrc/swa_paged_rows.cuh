@@ -36,48 +36,20 @@
 // Sinks: the 16-key groups that hold them come before those of the window, in
 // one list.  A tree: the groups of the chunk itself test a bit per row and key.
 //
-// 8-bit cache.  Half the bytes, so that what a warp does per group counts twice
-// as much.  The codes go from shared memory to registers in 16 bytes a thread,
-// and to 16-bit pairs there, 4 to 5 instructions a pair with the exponent's
-// product; the sums over the head dim and over the keys, and the result's
-// columns, are taken in the order in which a thread holds them: thread c of a
-// quad has head dims c D / 4 on of its keys for the scores, and D / 8 columns in
-// a row of its four keys for the second product, with no shuffle in between.
+// The 8-bit cache has a kernel of its own (swa_paged_rows_e4m3.cu).
 #pragma once
-#include "swa_paged.h"
-#include "swa_device.cuh"
-#include "swa_paged_mask.cuh"
-
-#include <type_traits>
+#include "swa_paged_rows_end.cuh"
 
 namespace swa {
 namespace {
 
-constexpr int kRowsWarps = kRowsStep / 16;
-constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.0f;  // rescale only when the maximum grows by more than 2^8
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -90,73 +62,26 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The CTAs of a cluster: barrier over all their threads (every thread arrives
-// and waits; orders shared-memory accesses across the cluster), this CTA's
-// rank, and reads of a peer's shared memory.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
-template <int DP, bool Q8>
+template <int DP>
 struct RowsSmem {
-  static constexpr int kRowsStages = Q8 ? 4 : 3;
-  static constexpr int kRowBytes = Q8 ? DP : DP * 2;
+  static constexpr int kRowsStages = 3;
+  static constexpr int kRowBytes = DP * 2;
   static constexpr int kGroupBytes = 16 * kRowBytes;  // 16 keys of K or V
   alignas(128) uint8_t ring[kRowsWarps][kRowsStages][2][kGroupBytes];
-  alignas(16) int8_t exps[kRowsWarps][Q8 ? kRowsStages : 1][2][16];
   float ml[kRowsWarps][kRowsTile][2];
-  // the warps' O, [warp][row][DP + 4], reuses the ring, and behind it the
-  // CTA's own joined rows and their maxima and sums, for the cluster
-  static constexpr int kOPitch = DP + 4;
+  // the warps' O and what the cluster reads reuse the ring
   static constexpr int kRingBytes = kRowsWarps * kRowsStages * 2 * kGroupBytes;
-  static constexpr int kJoinAt = kRowsWarps * kRowsTile * kOPitch;  // floats
-  static constexpr int kMlAt = kJoinAt + kRowsTile * DP;
-  static_assert(4 * (kMlAt + 2 * kRowsTile) <= kRingBytes, "join space");
+  static_assert(RowsEnd<DP>::kBytes <= kRingBytes, "join space");
 };
 
 // CL: the splits of an item are the CTAs of one cluster, which join their rows
 // through each other's shared memory; otherwise partial rows go to the
 // workspace and swa_paged_join_kernel joins them.
 template <PagedKind KIND, int DP, bool F16, bool CL, int CAP>
-__global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2)
+__global__ void __launch_bounds__(kRowsThreads, 2)
     swa_paged_rows_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab) {
-  constexpr bool X = KIND != PagedKind::kPlain, Q8 = KIND == PagedKind::kE4m3;
-  using Smem = RowsSmem<DP, Q8>;
+  constexpr bool X = KIND != PagedKind::kPlain;
+  using Smem = RowsSmem<DP>;
   constexpr int kRowsStages = Smem::kRowsStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw);
@@ -197,24 +122,14 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
     const int64_t e = static_cast<int64_t>(w.q_start + tok0 + i) * a.q_row + h * a.q_head;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + e;
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
-      if constexpr (Q8) {
-        // head dims c .. c + 3, in the order of the pairs that a word of K gives
-        const int c = (lane & 3) * (DP / 4) + kk * 4;
-        const uint2 d = valid && c < g.D && in_bounds(e + c, 4, a.n_q, a.err) ? *reinterpret_cast<const uint2*>(q + c)
-                                                                              : make_uint2(0u, 0u);
-        qf[kk][x] = F16 ? d.x : __byte_perm(d.x, d.y, 0x7632);      // dims 1, 3 (bf16); 0, 1 (fp16)
-        qf[kk][x + 2] = F16 ? d.y : __byte_perm(d.x, d.y, 0x5410);  // dims 0, 2; 2, 3
-      } else {
+    for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int c = kk * 16 + y * 8 + (lane & 3) * 2;
-          qf[kk][x + 2 * y] = valid && c < g.D && in_bounds(e + c, 2, a.n_q, a.err)
-                                  ? *reinterpret_cast<const uint32_t*>(q + c)
-                                  : 0u;
-        }
+      for (int y = 0; y < 2; ++y) {
+        const int c = kk * 16 + y * 8 + (lane & 3) * 2;
+        qf[kk][x + 2 * y] = valid && c < g.D && in_bounds(e + c, 2, a.n_q, a.err)
+                                ? *reinterpret_cast<const uint32_t*>(q + c)
+                                : 0u;
       }
-    }
   }
 
   int bad = 0;
@@ -262,9 +177,8 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
   }
 
   const int hk = w.vh * a.gs / a.group;
-  using Elem = std::conditional_t<Q8, uint8_t, uint16_t>;
-  const Elem* kb = static_cast<const Elem*>(a.k_pages) + hk * g.k_head;
-  const Elem* vb = static_cast<const Elem*>(a.v_pages) + hk * g.v_head;
+  const uint16_t* kb = static_cast<const uint16_t*>(a.k_pages) + hk * g.k_head;
+  const uint16_t* vb = static_cast<const uint16_t*>(a.v_pages) + hk * g.v_head;
   const uint32_t ring = smem_u32(s.ring[warp]);
   const int n_it = st1 - st0;  // the warp's groups: number (st0 + it) * 4 + warp
   const int gw = st0 * kRowsWarps + warp;
@@ -292,12 +206,11 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
     }
   };
   const int row_in = lane / kChunks, chunk = lane % kChunks;  // the lane's part of 32 / kChunks rows
-  const int live_chunks = Q8 ? kChunks : 2 * nk;              // chunks the products read
+  const int live_chunks = 2 * nk;                             // chunks the products read
   // The copies of K (V) of the warp's group `it`.  A stage is free once its
   // fragments are in registers, so close to a ring of each is in flight; every call commits one group, empty past the end.  A group
   // whose 16 keys are all seen needs no per-row test.
-  constexpr int kPer = 16 / sizeof(Elem);  // elements of a chunk
-  const int in_d = chunk * kPer < g.D;
+  const int in_d = chunk * 8 < g.D;
   const uint32_t lane_dst = ring + row_in * Smem::kRowBytes;
   auto issue = [&](int it, bool is_v) {
     if ((it & 31) == 0 && !is_v) fetch_pages(it);
@@ -305,42 +218,18 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
     if (it < n_it && chunk < live_chunks) {
       const int j0 = first_key(it);
       const uint32_t dst = lane_dst + ((it % kRowsStages) * 2 + (is_v ? 1 : 0)) * Smem::kGroupBytes;
-      const Elem* base = is_v ? vb : kb;
+      const uint16_t* base = is_v ? vb : kb;
       const int64_t step = is_v ? g.v_slot : g.k_slot;
-      const int64_t e0 = page * (is_v ? g.v_page : g.k_page) + (slot + row_in) * step + chunk * kPer;
+      const int64_t e0 = page * (is_v ? g.v_page : g.k_page) + (slot + row_in) * step + chunk * 8;
       const bool whole = page >= 0 && (j0 >= lo || (X && j0 + 15 < keys.sinks)) && j0 + 15 <= hi;
-      // the chunk's place in row r, against bank conflicts of the reads below
-      auto place = [&](int r) {
-        if constexpr (!Q8) return (chunk ^ (r & 7)) << 4;
-        else if constexpr (DP == 128) return (chunk ^ (is_v ? r & 6 : r & 1)) << 4;
-        else return ((((r & 1) << 2 | chunk) ^ (is_v ? r & 6 : 0)) << 4) - ((r & 1) << 6);
-      };
-      if (Q8 && lane == 0) {  // the group's exponents; those of a page not to be followed are 0
-        const int64_t e = page * g.exp_page + hk * g.page_size + slot;
-        const int8_t* exps = is_v ? g.v_exp : g.k_exp;
-        const bool ok = page >= 0 && in_bounds(e, 16, g.n_exp, a.err);
-        cp_async16(smem_u32(s.exps[warp][it % kRowsStages][is_v ? 1 : 0]), ok ? exps + e : exps, ok);
-      }
       const int64_t head = hk * (is_v ? g.v_head : g.k_head), extent = is_v ? g.n_v : g.n_k;
-      if (Q8 && !g.wide) {  // rows start on 8 bytes
-#pragma unroll
-        for (int x = 0; x < 16 * kChunks / 32; ++x) {
-          const int r = x * (32 / kChunks) + row_in;
-          const int64_t e = e0 + x * (32 / kChunks) * step;
-          const bool seen = page >= 0 && some_see(j0 + r);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const bool ok = seen && chunk * kPer + half * 8 < g.D && in_bounds(head + e + half * 8, 8, extent, a.err);
-            cp_async8(dst + x * (32 / kChunks) * Smem::kRowBytes + place(r) + half * 8, ok ? base + e + half * 8 : base, ok);
-          }
-        }
-      } else if (SWA_CHECKS == 0 && whole) {
-        const Elem* src = in_d ? base + e0 : base;
+      if (SWA_CHECKS == 0 && whole) {
+        const uint16_t* src = in_d ? base + e0 : base;
         const int64_t hop = in_d ? step * (32 / kChunks) : 0;
 #pragma unroll
         for (int x = 0; x < 16 * kChunks / 32; ++x) {
           const int r = x * (32 / kChunks) + row_in;
-          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + place(r), src, in_d);
+          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + ((chunk ^ (r & 7)) << 4), src, in_d);
           src += hop;
         }
       } else {
@@ -348,8 +237,8 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
         for (int x = 0; x < 16 * kChunks / 32; ++x) {
           const int r = x * (32 / kChunks) + row_in;
           const int64_t e = e0 + x * (32 / kChunks) * step;
-          const bool ok = in_d && page >= 0 && some_see(j0 + r) && in_bounds(head + e, kPer, extent, a.err);
-          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + place(r), ok ? base + e : base, ok);
+          const bool ok = in_d && page >= 0 && some_see(j0 + r) && in_bounds(head + e, 8, extent, a.err);
+          cp_async16(dst + x * (32 / kChunks) * Smem::kRowBytes + ((chunk ^ (r & 7)) << 4), ok ? base + e : base, ok);
         }
       }
     }
@@ -378,55 +267,7 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
     const int j0 = first_key(it);
     const uint32_t kd = ring + (it % kRowsStages) * 2 * Smem::kGroupBytes, vd = kd + Smem::kGroupBytes;
     float sc[2][4];  // scores of keys 0-7 and 8-15
-    // keys 0-7: lane / 4 is the row of K, and for V the lane's keys 2 (lane mod 4) + {0, 1, 8, 9}
-    const int8_t* exps = &s.exps[warp][Q8 ? it % kRowsStages : 0][0][0];
-    if constexpr (Q8) {
-      const int row = lane >> 2, quad = lane & 3;
-      uint32_t kw[2][DP / 16];  // DP / 4 codes of two keys
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int r = row + 8 * t;
-#pragma unroll
-        for (int x = 0; x < DP / 64; ++x) {
-          const int at = DP == 128 ? (((2 * quad + x) ^ (r & 1)) << 4) : quad << 4;
-          const uint4 v = lds128(kd + r * Smem::kRowBytes + at);
-          kw[t][4 * x] = v.x;
-          kw[t][4 * x + 1] = v.y;
-          kw[t][4 * x + 2] = v.z;
-          kw[t][4 * x + 3] = v.w;
-        }
-      }
-      const uint32_t f0 = exp_factor<F16>(exps[row]) * 0x10001u, f1 = exp_factor<F16>(exps[row + 8]) * 0x10001u;
-      __syncwarp();
-      issue(it + kRowsStages, false);  // K's stage is free
-      float s2[2][2][4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) s2[x][y][z] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t v = kw[t][kk], f = t == 0 ? f0 : f1;
-          uint32_t b0, b1;
-          if constexpr (F16) {
-            b0 = codes_f16(v);
-            b1 = codes_f16(v >> 16);
-          } else {
-            b0 = codes_high(v);
-            b1 = codes_high(v << 8);
-          }
-          mma16816<F16>(s2[kk & 1][t], qf[kk], mul2<F16>(b0, f), mul2<F16>(b1, f));
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int z = 0; z < 4; ++z) sc[y][z] = s2[0][y][z] + s2[1][y][z];
-    } else {
+    {
       uint32_t b[DP / 16][4];
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
@@ -454,42 +295,10 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
     }
     cp_async_wait<2 * kRowsStages - 1>();  // V(it): its fragments load behind the softmax
     __syncwarp();
-    uint32_t vf[DP / 16][Q8 ? 2 : 4];  // 8-bit: DP / 8 codes of four keys
-    uint32_t vm0 = 0, vm1 = 0;         // and the keys' factors
-    if constexpr (Q8) {
-      const int row = lane >> 2, quad = lane & 3;
+    uint32_t vf[DP / 16][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int r = 2 * quad + (t & 1) + 8 * (t >> 1);
-        uint32_t* v = &vf[0][0] + t * (DP / 32);
-        if constexpr (DP == 128) {
-          const uint4 x = lds128(vd + r * Smem::kRowBytes + ((row ^ (r & 6)) << 4));
-          v[0] = x.x;
-          v[1] = x.y;
-          v[2] = x.z;
-          v[3] = x.w;
-        } else {
-          const uint2 x = lds64(vd + (r >> 1) * 128 + ((((r & 1) << 2 | row >> 1) ^ (r & 6)) << 4) + (row & 1) * 8);
-          v[0] = x.x;
-          v[1] = x.y;
-        }
-      }
-      uint32_t f[4];
-      const bool edge = j0 < lo || j0 + 15 > hi;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int r = 2 * quad + (t & 1) + 8 * (t >> 1);
-        f[t] = exp_factor<F16>(exps[16 + r]);
-        // a slot that no row sees holds any exponent, a NaN's too
-        if (edge && !some_see(j0 + r)) f[t] = 0;
-      }
-      vm0 = f[0] | f[1] << 16;
-      vm1 = f[2] | f[3] << 16;
-    } else {
-#pragma unroll
-      for (int nb = 0; nb < DP / 16; ++nb)
-        if (nb < nk) ldsm_x4_trans(vf[nb], vd + v_row + (((nb * 2 + (mat >> 1)) ^ lr) << 4));
-    }
+    for (int nb = 0; nb < DP / 16; ++nb)
+      if (nb < nk) ldsm_x4_trans(vf[nb], vd + v_row + (((nb * 2 + (mat >> 1)) ^ lr) << 4));
     __syncwarp();
     issue(it + kRowsStages, true);  // V's stage is free
     // mask (groups at the ends of the visible run only), running maximum
@@ -547,22 +356,12 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
       p[x] = pack2<F16>(p0, p1);      // keys 0-7
       p[2 + x] = pack2<F16>(p2, p3);  // keys 8-15
     }
-    if constexpr (Q8) {
-      const uint32_t* v = &vf[0][0];
 #pragma unroll
-      for (int nb = 0; nb < DP / 8; ++nb) {  // columns (lane / 4) DP / 8 + nb of the result
-        const int x = nb >> 2;
-        mma16816<F16>(o[nb], p, mul2<F16>(codes_of<F16>(v[x], v[DP / 32 + x], nb & 3), vm0),
-                      mul2<F16>(codes_of<F16>(v[2 * (DP / 32) + x], v[3 * (DP / 32) + x], nb & 3), vm1));
+    for (int nb = 0; nb < DP / 16; ++nb)
+      if (nb < nk) {
+        mma16816<F16>(o[2 * nb], p, vf[nb][0], vf[nb][1]);
+        mma16816<F16>(o[2 * nb + 1], p, vf[nb][2], vf[nb][3]);
       }
-    } else {
-#pragma unroll
-      for (int nb = 0; nb < DP / 16; ++nb)
-        if (nb < nk) {
-          mma16816<F16>(o[2 * nb], p, vf[nb][0], vf[nb][1]);
-          mma16816<F16>(o[2 * nb + 1], p, vf[nb][2], vf[nb][3]);
-        }
-    }
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -584,124 +383,23 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == PagedKind::kE4m3 ? 3 : 2
       s.ml[warp][r][1] = l[x] * f;
     }
     const float f = m_true[x] == -INFINITY ? 0.f : ex2_approx(m[x] - m_true[x]);
-    float* row = so + (warp * kRowsTile + r) * Smem::kOPitch;
-    if constexpr (Q8) {
+    float* row = so + (warp * kRowsTile + r) * RowsEnd<DP>::kOPitch;
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int t = 0; t < DP / 8; t += 4)
-          *reinterpret_cast<float4*>(row + (2 * (lane & 3) + y) * (DP / 8) + t) =
-              make_float4(o[t][2 * x + y] * f, o[t + 1][2 * x + y] * f, o[t + 2][2 * x + y] * f, o[t + 3][2 * x + y] * f);
-    } else {
-#pragma unroll
-      for (int t = 0; t < DP / 8; ++t)
-        *reinterpret_cast<float2*>(row + t * 8 + (lane & 3) * 2) = make_float2(o[t][2 * x] * f, o[t][2 * x + 1] * f);
-    }
+    for (int t = 0; t < DP / 8; ++t)
+      *reinterpret_cast<float2*>(row + t * 8 + (lane & 3) * 2) = make_float2(o[t][2 * x] * f, o[t][2 * x + 1] * f);
   }
-  const int any_len = __syncthreads_or(bad == kPageErrLength), any_entry = __syncthreads_or(bad == kPageErrEntry);
-  if (threadIdx.x == 0)
-    a.page_err[item * a.splits + split] = any_len ? kPageErrLength : (any_entry ? kPageErrEntry : 0);
-
-  // four columns of row r, from their maximum, sum and unnormalised values
-  auto finish = [&](int r, int col, float M, float L, const float (&acc)[4]) {
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    const int i = row_token(r, a.gs_magic), h = w.vh * a.gs + (r - i * a.gs);
-    const int64_t row = static_cast<int64_t>(w.q_start + tok0 + i) * g.N + h;
-    if (col < g.D && in_bounds(row * g.D + col, 4, a.n_out, a.err))
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D + col) =
-          make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
-    if (col == 0 && in_bounds(row, 1, a.n_stats, a.err)) {
-      if (a.smax) a.smax[row] = M == -INFINITY ? -INFINITY : M * kLn2;
-      if (a.ssum) a.ssum[row] = L;
-    }
-  };
-  // join the four warps: thread = 4 columns of a row
-  constexpr int kCols4 = DP / 4;
-  for (int x = threadIdx.x; x < n_rows * kCols4; x += kRowsThreads) {
-    const int r = x / kCols4, col = (x % kCols4) * 4;
-    float M = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < kRowsWarps; ++v) M = fmaxf(M, s.ml[v][r][0]);
-    const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < kRowsWarps; ++v) {
-      const float f = ex2_approx(s.ml[v][r][0] - ms);
-      L += s.ml[v][r][1] * f;
-      const float4 ov = *reinterpret_cast<const float4*>(so + (v * kRowsTile + r) * Smem::kOPitch + col);
-      acc[0] += ov.x * f;
-      acc[1] += ov.y * f;
-      acc[2] += ov.z * f;
-      acc[3] += ov.w * f;
-    }
-    if (CL) {
-      *reinterpret_cast<float4*>(so + Smem::kJoinAt + r * DP + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (col == 0) *reinterpret_cast<float2*>(so + Smem::kMlAt + 2 * r) = make_float2(M, L);
-    } else if (!direct) {
-      const int64_t pr = (item * a.splits + split) * a.rows_pad + r;
-      *reinterpret_cast<float4*>(a.part_o + pr * DP + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (col == 0) a.part_ml[pr] = make_float2(M, L);
-    } else {
-      finish(r, col, M, L, acc);
-    }
-  }
-  if constexpr (CL) {
-    // row r of the item is finished by the CTA of rank r mod splits
-    cluster_sync();
-    const uint32_t rank = cluster_rank(), mine = smem_u32(so + Smem::kJoinAt), mine_ml = smem_u32(so + Smem::kMlAt);
-    for (int x = threadIdx.x;; x += kRowsThreads) {
-      const int r = static_cast<int>(rank) + x / kCols4 * a.splits, col = (x % kCols4) * 4;
-      if (r >= n_rows) break;
-      float M = -INFINITY;
-#pragma unroll 8
-      for (int v = 0; v < a.splits; ++v) M = fmaxf(M, ld_peer2(peer_smem(mine_ml + 8 * r, v)).x);
-      const float ms = M == -INFINITY ? 0.f : M;
-      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int v = 0; v < a.splits; ++v) {
-        const float2 ml = ld_peer2(peer_smem(mine_ml + 8 * r, v));
-        const float4 ov = ld_peer4(peer_smem(mine + 4 * (r * DP + col), v));
-        const float f = ex2_approx(ml.x - ms);
-        L += ml.y * f;
-        acc[0] += ov.x * f;
-        acc[1] += ov.y * f;
-        acc[2] += ov.z * f;
-        acc[3] += ov.w * f;
-      }
-      finish(r, col, M, L, acc);
-    }
-    cluster_sync();  // a CTA's shared memory stays until its peers have read it
-  }
+  rows_end<DP, F16, CL>(a, w, split, item, tok0, n_rows, direct, bad, so, s.ml);
   if (a.overlap && blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();  // (no early return: split 0 always runs)
 }
 
 template <PagedKind KIND, int DP, bool F16, bool CL, int CAP>
 cudaError_t launch_rows_t(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream) {
-  const size_t smem = sizeof(RowsSmem<DP, KIND == PagedKind::kE4m3>);
+  const size_t smem = sizeof(RowsSmem<DP>);
   auto kernel = swa_paged_rows_kernel<KIND, DP, F16, CL, CAP>;
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = set_smem_limit(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const dim3 grid(tab.n_items, a.splits), block(kRowsThreads);
-  if constexpr (!CL) {
-    return launch_pdl(kernel, grid, block, smem, stream, a, tab);
-  } else {
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = static_cast<unsigned>(a.splits);
-    attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a, tab);
-  }
+  return launch_rows_grid<CL>(kernel, dim3(tab.n_items, a.splits), smem, stream, a, tab);
 }
 
 }  // namespace

@@ -41,15 +41,7 @@
 // Sinks: the key tiles that hold them come before those of the window, in one
 // list.  A tree: the tiles that hold the chunk's own keys take 32 bits per row
 // and 32 columns.  The fast path without per-column tests is as it was.
-//
-// 8-bit cache: four more warps (8-11) bring in the codes and their rows'
-// exponents by cp.async, 32 keys of K and V a warp and tile, up to two tiles
-// ahead, and write them as 16-bit values into the swizzled tiles that the
-// products read, one barrier arrival a warp.  The values are exact, so all that
-// follows is as for the 16-bit cache.  A pair of values takes 5 instructions
-// (bf16) or 2.5 (fp16), 2700 per tile of 128 x 128 keys and values, spread over
-// the four schedulers beside the softmax.  12 warps leave a thread 168
-// registers: the softmax spills 100 bytes.
+// An 8-bit cache is written out as 16-bit pages first (swa_paged_unpack.cu).
 // TMEM columns as in swa_fwd.cu: S0 [0,128), S1 [128,256), O [256,256+D),
 // P0 [384,448), P1 [448,512).
 #pragma once
@@ -60,26 +52,21 @@
 namespace swa {
 namespace {
 
+constexpr int kStages = 3;
 constexpr int kThreads = 256;  // (more than 8 warps would cap a thread at 168 registers: the softmax spills)
-constexpr int kUnpackWarps = 4, kUnpackKeys = kPagedTileStep / kUnpackWarps;  // 8-bit cache
-constexpr int kRawStages = 2;
 
-template <int D, bool Q8>
+template <int D>
 struct TileSmem {
-  static constexpr int kStages = Q8 ? 2 : 3;
   static constexpr int kTileBytes = kPagedTileRows * D * 2;
   alignas(1024) uint8_t q[kTileBytes];
   alignas(1024) uint8_t k[kStages][kTileBytes];
   alignas(1024) uint8_t v[kStages][kTileBytes];
-  alignas(16) uint8_t raw[Q8 ? kUnpackWarps : 0][kRawStages][2][kUnpackKeys * D];
-  alignas(16) int8_t exps[Q8 ? kUnpackWarps : 0][kRawStages][2][kUnpackKeys];
   uint64_t q_full, q_empty, o_free, k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2], drain_s, drain_pv;
   uint64_t never;  // completed by nothing: the target of the stall test hook
   uint32_t tmem_base;
 };
-static_assert(sizeof(TileSmem<128, false>) + 1024 <= 232448 && sizeof(TileSmem<128, true>) + 1024 <= 232448,
-              "shared memory budget");
+static_assert(sizeof(TileSmem<128>) + 1024 <= 232448, "shared memory budget");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256, kColP = 384;
@@ -227,8 +214,7 @@ struct UnitWalk {
   }
 };
 
-// Position in a ring of `stages`: stage, and the parity of its current use.
-template <int kStages>
+// Position in a ring of kStages: stage, and the parity of its current use.
 struct Ring {
   int st = 0;
   uint32_t use = 0;  // times the ring has wrapped
@@ -240,129 +226,15 @@ struct Ring {
   }
 };
 
-// 8-bit cache: one of the warps that bring in codes and write them as 16-bit
-// values, `part` of kUnpackWarps.  A lane converts the chunks that it copied.
-template <int D, bool F16>
-struct Unpack {
-  using Smem = TileSmem<D, true>;
-  static constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;  // 16 codes; rows that a warp takes at a time
-  int part, lane, hk;
-  int my_page, my_slot, bad;  // of group lane & 7 of the tile lane >> 3 of the four in hand
-
-  __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-  }
-  __device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
-  }
-  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  template <int N>
-  __device__ __forceinline__ void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-    __syncwarp();
-  }
-  static __device__ __forceinline__ bool seen(const Unit& x, int j) {
-    return (j >= x.keys.lo || j < x.keys.sinks) && j <= x.keys.hi;
-  }
-  __device__ __forceinline__ void fetch_pages(const PagedArgs& a, const Unit& x, int it) {
-    const int t = it + (lane >> 3);
-    my_page = -1;
-    my_slot = 0;
-    if (t >= x.n_kv) return;
-    const int j = x.key0(t) + (lane & 7) * 16;
-    if (j >= x.keys.sinks && (j > x.keys.hi || j + 15 < x.keys.lo)) return;  // no key of it is seen
-    const int entry = j / a.g.page_size;
-    my_slot = j - entry * a.g.page_size;
-    const int64_t e = x.w.b * a.g.table_stride + entry;
-    const int page = in_bounds(e, 1, a.g.n_table, a.err) ? a.g.table[e] : -1;
-    if (page >= 0 && page < a.g.num_pages) my_page = page;
-    else bad = kPageErrEntry;
-  }
-  // The copies of K (V) of tile `it`, a group each, empty past the last.
-  __device__ __forceinline__ void issue(const PagedArgs& a, Smem& s, const Unit& x, int it, int raw, bool is_v) {
-    if (it < x.n_kv) {
-      if (!is_v && (it & 3) == 0) fetch_pages(a, x, it);
-      const PagedGeom& g = a.g;
-      const int j0 = x.key0(it) + part * kUnpackKeys;
-      const int64_t head = hk * (is_v ? g.v_head : g.k_head), step = is_v ? g.v_slot : g.k_slot;
-      const int64_t extent = is_v ? g.n_v : g.n_k;
-      const uint8_t* base = static_cast<const uint8_t*>(is_v ? a.v_pages : a.k_pages);
-      const int8_t* exps = is_v ? g.v_exp : g.k_exp;
-      const int chunk = lane % kChunks, row_in = lane / kChunks;
-      const uint32_t dst = smem_u32(s.raw[part][raw][is_v]);
-#pragma unroll
-      for (int y = 0; y < kUnpackKeys / 16; ++y) {
-        const int from = (it & 3) * 8 + part * (kUnpackKeys / 16) + y;
-        const int page = __shfl_sync(0xFFFFFFFFu, my_page, from), slot = __shfl_sync(0xFFFFFFFFu, my_slot, from);
-        if (lane == 0) {
-          const int64_t e = page * g.exp_page + hk * g.page_size + slot;
-          const bool ok = page >= 0 && in_bounds(e, 16, g.n_exp, a.err);
-          copy16(smem_u32(s.exps[part][raw][is_v] + y * 16), ok ? exps + e : exps, ok);
-        }
-        const int64_t e0 = head + page * (is_v ? g.v_page : g.k_page) + slot * step + chunk * 16;
-#pragma unroll
-        for (int r0 = 0; r0 < 16; r0 += kRowsPer) {
-          const int r = r0 + row_in;
-          const int64_t e = e0 + r * step;
-          const bool ok = page >= 0 && seen(x, j0 + y * 16 + r);
-          const uint32_t d = dst + (y * 16 + r) * D + chunk * 16;
-          if (g.wide) {
-            const bool in = ok && chunk * 16 < g.D && in_bounds(e, 16, extent, a.err);
-            copy16(d, in ? base + e : base, in);
-          } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const bool in = ok && chunk * 16 + half * 8 < g.D && in_bounds(e + half * 8, 8, extent, a.err);
-              copy8(d + half * 8, in ? base + e + half * 8 : base, in);
-            }
-          }
-        }
-      }
-    }
-    commit();
-  }
-  // This warp's 32 rows of a tile, from raw stage `raw` into the swizzled tile.
-  __device__ __forceinline__ void convert(Smem& s, const Unit& x, int it, int raw, bool is_v, uint8_t* tile) {
-    const int chunk = lane % kChunks, row_in = lane / kChunks;
-    const uint8_t* src = s.raw[part][raw][is_v];
-    const int8_t* exps = s.exps[part][raw][is_v];
-    const int j0 = x.key0(it) + part * kUnpackKeys;
-    // eight lanes store one row: those of the second atom column take their odd chunk first
-    const int odd = D == 128 ? chunk >> 2 : 0;
-#pragma unroll
-    for (int r0 = 0; r0 < kUnpackKeys; r0 += kRowsPer) {
-      const int r = r0 + row_in;
-      uint4 v = *reinterpret_cast<const uint4*>(src + r * D + chunk * 16);
-      // (a slot that no row sees holds any exponent, a NaN's too)
-      const uint32_t f = seen(x, j0 + r) ? exp_factor<F16>(exps[r]) * 0x10001u : 0u;
-      if (odd) v = make_uint4(v.z, v.w, v.x, v.y);
-      uint4 lo, hi;
-      codes4<F16>(v.x, lo.x, lo.y);
-      codes4<F16>(v.y, lo.z, lo.w);
-      codes4<F16>(v.z, hi.x, hi.y);
-      codes4<F16>(v.w, hi.z, hi.w);
-      lo = make_uint4(mul2<F16>(lo.x, f), mul2<F16>(lo.y, f), mul2<F16>(lo.z, f), mul2<F16>(lo.w, f));
-      hi = make_uint4(mul2<F16>(hi.x, f), mul2<F16>(hi.y, f), mul2<F16>(hi.z, f), mul2<F16>(hi.w, f));
-      st_chunk_sw128(tile, part * kUnpackKeys + r, 2 * chunk + odd, lo);
-      st_chunk_sw128(tile, part * kUnpackKeys + r, 2 * chunk + 1 - odd, hi);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-  }
-};
-
 template <PagedKind KIND, int D, bool F16, int CAP>
-__global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackWarps * 32 : kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     swa_paged_tile_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                           const __grid_constant__ CUtensorMap mq) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr bool X = KIND != PagedKind::kPlain, Q8 = KIND == PagedKind::kE4m3;
-  using Smem = TileSmem<D, Q8>;
-  constexpr int kStages = Smem::kStages;
-  using Ring = Ring<kStages>;
-  Smem& s = *reinterpret_cast<Smem*>(align1024(smem_raw));
-  constexpr int kTileBytes = Smem::kTileBytes;
+  constexpr bool X = KIND != PagedKind::kPlain;
+  TileSmem<D>& s = *reinterpret_cast<TileSmem<D>*>(align1024(smem_raw));
+  constexpr int kTileBytes = TileSmem<D>::kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   // the few-row kernel of the same call may fill the SMs that this one leaves
@@ -380,8 +252,8 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.o_free, kPagedTileRows);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.k_full[i], Q8 ? kUnpackWarps : 1);
-      mbar_init(&s.v_full[i], Q8 ? kUnpackWarps : 1);
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.v_full[i], 1);
       mbar_init(&s.k_empty[i], 1);
       mbar_init(&s.v_empty[i], 1);
     }
@@ -395,10 +267,8 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
     mbar_init(&s.drain_pv, 1);
     mbar_init(&s.never, 1);
     fence_mbar_init();
-    if (!Q8) {
-      tma_prefetch_desc(&mk);
-      tma_prefetch_desc(&mv);
-    }
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
     if (a.q_tma) tma_prefetch_desc(&mq);
   }
   if (warp == 5) {
@@ -410,43 +280,7 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
   tc_fence_after_sync();
   const uint32_t tmem = s.tmem_base;
 
-  if (Q8 && warp >= 8) {
-    // ------------------------------------ 8-bit pages -> 16-bit tiles --
-    if constexpr (Q8) {
-      Unpack<D, F16> u;
-      u.part = warp - 8;
-      u.lane = lane;
-      Ring ring;
-      bool ok = true;
-      while (ok && walk.next(a, tab, n_units, x)) {
-        u.bad = x.bad_len ? kPageErrLength : 0;
-        u.hk = x.w.vh * a.gs / a.group;
-#pragma unroll
-        for (int it = 0; it < kRawStages; ++it) {
-          u.issue(a, s, x, it, it, false);
-          u.issue(a, s, x, it, it, true);
-        }
-        for (int it = 0; ok && it < x.n_kv; ++it) {
-#pragma unroll
-          for (int is_v = 0; is_v < 2; ++is_v) {
-            u.template wait<2 * kRawStages - 1>();  // the oldest group in flight
-            if (ring.use > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(is_v ? &s.v_empty[ring.st] : &s.k_empty[ring.st],
-                                                                   (ring.use - 1) & 1, a.err, kErrFwdLoad))) {
-              ok = false;
-              break;
-            }
-            u.convert(s, x, it, it % kRawStages, is_v, is_v ? s.v[ring.st] : s.k[ring.st]);
-            if (lane == 0) mbar_arrive(is_v ? &s.v_full[ring.st] : &s.k_full[ring.st]);
-            u.issue(a, s, x, it + kRawStages, it % kRawStages, is_v);
-          }
-          ring.advance();
-        }
-        u.template wait<0>();  // the raw stages are the next unit's
-        const int bad = __reduce_max_sync(0xFFFFFFFFu, u.bad);
-        if (u.part == 0 && lane == 0) a.page_err[x.slot_id] = bad;
-      }
-    }
-  } else if (warp == 4 || warp == 7) {
+  if (warp == 4 || warp == 7) {
     // ------------------------------------------- producers: pages -> tiles --
     const bool is_k = warp == 4;
     uint64_t* full = is_k ? s.k_full : s.v_full;
@@ -459,16 +293,14 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
     int issued = 0;
     uint32_t uc = 0;  // units so far (Q)
     bool ok = true;
-    while (ok && !(Q8 && is_k) && walk.next(a, tab, n_units, x)) {
+    while (ok && walk.next(a, tab, n_units, x)) {
       int bad = x.bad_len ? kPageErrLength : 0;
       const int hk = x.w.vh * a.gs / a.group;
       PageWalk pages;
       int raw0, at0, raw1, at1;  // block table entries of this tile and the next
-      if constexpr (!Q8) {
-        pages.start(a, x.w.b, x.tiles, x.first, box, x.keys);
-        pages.template next<X>(mine && x.n_kv > 0, raw0, at0);
-        pages.template next<X>(mine && x.n_kv > 1, raw1, at1);
-      }
+      pages.start(a, x.w.b, x.tiles, x.first, box, x.keys);
+      pages.template next<X>(mine && x.n_kv > 0, raw0, at0);
+      pages.template next<X>(mine && x.n_kv > 1, raw1, at1);
       if (!is_k && x.n_kv > 0) {
         // Q, once the last scores of the unit before have read its place (the
         // unit's first V tile is needed well after).  By one box per atom
@@ -504,7 +336,6 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
         }
         ++uc;
       }
-      if constexpr (Q8) continue;
       for (int it = 0; it < x.n_kv; ++it) {
         if (ring.use > 0 &&
             !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[ring.st], (ring.use - 1) & 1, a.err, kErrFwdLoad))) {
@@ -591,8 +422,7 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
       for (int it = 0; it < x.n_kv; ++it) {
         const uint32_t pb = t & 1;
         const int j0 = x.key0(it);
-        if (!Q8 && ((j0 < seen.lo && !(X && j0 + kPagedTileStep - 1 < seen.sinks)) ||
-                    j0 + kPagedTileStep - 1 > seen.hi)) {
+        if ((j0 < seen.lo && !(X && j0 + kPagedTileStep - 1 < seen.sinks)) || j0 + kPagedTileStep - 1 > seen.hi) {
           // rows of V that no query of the chunk sees
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s.v_full[ring.st], ring.use & 1, a.err, kErrFwdMma))) {
             ok = false;
@@ -875,14 +705,13 @@ __global__ void __launch_bounds__(KIND == PagedKind::kE4m3 ? kThreads + kUnpackW
 template <PagedKind KIND, int D, bool F16, int CAP>
 cudaError_t launch_tile_t(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk, const CUtensorMap& mv,
                           const CUtensorMap& mq, cudaStream_t stream) {
-  constexpr bool Q8 = KIND == PagedKind::kE4m3;
-  const size_t smem = sizeof(TileSmem<D, Q8>) + 1024;
+  const size_t smem = sizeof(TileSmem<D>) + 1024;
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = set_smem_limit(swa_paged_tile_kernel<KIND, D, F16, CAP>, smem, smem_set);
   if (e != cudaSuccess) return e;
   const int units = a.whole + (tab.n_items - a.whole) * a.splits;
-  return launch_pdl(swa_paged_tile_kernel<KIND, D, F16, CAP>, dim3(units < kSms ? units : kSms),
-                    dim3(Q8 ? kThreads + kUnpackWarps * 32 : kThreads), smem, stream, a, tab, mk, mv, mq);
+  return launch_pdl(swa_paged_tile_kernel<KIND, D, F16, CAP>, dim3(units < kSms ? units : kSms), dim3(kThreads), smem,
+                    stream, a, tab, mk, mv, mq);
 }
 
 }  // namespace

@@ -530,7 +530,13 @@ SWA_API swa_status_t swa_paged_forward(const swa_paged_params_t *p, const void *
  * order, over the chunk.
  *   extra         NULL, or host; the pointers in it are device memory:
  *     k_exponents, v_exponents
- *                 as for swa_paged_append_ext; NULL iff the cache is not 8-bit
+ *                 as for swa_paged_append_ext; NULL iff the cache is not 8-bit.
+ *                 What sequences of more than 16 query rows per key/value head see
+ *                 of an 8-bit cache is first written out as 16-bit pages in the
+ *                 workspace: 4 N_kv D bytes per key that such a sequence may see
+ *                 (max_kv_len, or its window, chunk and sinks; to 128 keys), for
+ *                 as many sequences at a time as fit 1 GB, and 4 B bytes per 128
+ *                 keys of max_kv_len
  *     tree        uint32 [T_q, words], rows tree_stride words apart (0: the words
  *                 of the longest chunk, ceil(q_len / 32)); NULL: no tree
  *     depth       int32 [T_q], or NULL: the token's place in its chunk */

@@ -1,9 +1,13 @@
 """64-bit reference of paged attention with sinks, trees of drafted tokens and an
 8-bit cache, and the problems their tests draw.
 
-Tolerances are those of tests/paged_ref.py: the values of an 8-bit cache are
-exact in the 16-bit types (a code has 4 significant bits, its exponent keeps it
-in range), so attention over them rounds as over any other values."""
+Tolerances are those of tests/paged_ref.py.  Attention over an 8-bit cache rounds
+the values besides to multiples of 2^-25 2^E, E the largest exponent of a tile,
+2^-33 of the tile's largest value at most: that of the keys, times the row's sum
+of |q|, adds to the scores, that of the values to the result; a row of q loses
+2^-39 of its largest.  Its weights are rounded to fp16 as p 2^(e - E + 7), to
+2^-25 absolutely where they are small: 2^-32 2^E and so 2^-31 of the largest
+value in the result, for each key."""
 import torch
 
 from tests.paged_ref import DT, U
@@ -70,9 +74,10 @@ def seen_of(geom, n, m, see=None, depth=None):
     return seen
 
 
-def draw_cache(geom, kv_lens, seed, trees=None):
+def draw_cache(geom, kv_lens, seed, trees=None, spread=0):
     """Random sequences in shuffled pages.  Slots that a call may not need hold
-    NaN (and a NaN's exponent), and their table entries are -1."""
+    NaN (and a NaN's exponent), and their table entries are -1.  Rows differ by up
+    to 2^spread in size, with rows of zeros among them."""
     g = torch.Generator().manual_seed(seed)
     P, q8 = geom.page_size, geom.cache_dtype == "e4m3"
     dt = torch.float8_e4m3fn if q8 else DT[geom.dtype]
@@ -92,6 +97,9 @@ def draw_cache(geom, kv_lens, seed, trees=None):
         values = []
         for x in range(2):
             v = torch.randn(n, geom.n_kv, geom.D, generator=g) * (loud if x == 0 else 1.0)
+            if spread:
+                v *= torch.pow(2.0, -torch.randint(0, spread + 1, (n, geom.n_kv, 1), generator=g).float())
+                v *= (torch.rand(n, geom.n_kv, 1, generator=g) > 0.1)
             if q8:
                 codes, e = encode(v.to(DT[geom.dtype]) / (4.0 if x == 0 else 1.0), geom.dtype)
                 values.append((codes, e))
@@ -141,9 +149,14 @@ def attention_ref(geom, q, ks, vs, kv_lens, trees=None):
             P = w / torch.where(l > 0, l, 1.0)[:, None]
             out[r, h], smax[r, h], ssum[r, h] = P @ v, torch.where(live, mx, -float("inf")), l
             e = D * 2.0 ** -23 * size + 2.0 ** -22 * (size + 1)
+            if geom.cache_dtype:
+                e = e + abs(geom.scale) * (x.abs().sum(1) * 2.0 ** -33 * k.abs().amax() +
+                                           x.abs().amax(1) * 2.0 ** -39 * k.abs().sum(1).amax())
             eo[r, h] = (P @ v.abs()) * (u + 2 * e + n * 2.0 ** -24)[:, None]
             if geom.dtype == "fp16":
                 eo[r, h] += n * 2.0 ** -25 * v.abs().amax()
+            if geom.cache_dtype:
+                eo[r, h] += (n * 2.0 ** -31 + 2.0 ** -33) * v.abs().amax()
             eo[r, h] += u * (out[r, h].abs() + eo[r, h]) + (2.0 ** -25 if geom.dtype == "fp16" else 0.0)
             em[r, h] = e
             es[r, h] = l * (2 * e + n * 2.0 ** -24)

@@ -20,13 +20,13 @@ def geometry(q_lens, kv_lens, page=16, extra_pages=3, **kw):
                          page_size=page, max_pages=max(1, max(-(-n // page) for n in kv_lens)) + 1, **kw)
 
 
-def make(geom, kv_lens, seed, tree=False, words_more=0):
+def make(geom, kv_lens, seed, tree=False, words_more=0, spread=0, loud=1.0):
     """Everything a call needs, on the CPU."""
     trees = None
     if tree:
         trees = [tree_of(draw_tree(m, seed + 7 * b)) for b, m in enumerate(geom.q_lens())]
-    ks, vs, pages, exps, table, lens = draw_cache(geom, kv_lens, seed, trees)
-    q = torch.randn(geom.T_q, geom.N, geom.D, generator=torch.Generator().manual_seed(seed + 1)).to(DT[geom.dtype])
+    ks, vs, pages, exps, table, lens = draw_cache(geom, kv_lens, seed, trees, spread)
+    q = (torch.randn(geom.T_q, geom.N, geom.D, generator=torch.Generator().manual_seed(seed + 1)) * loud).to(DT[geom.dtype])
     kw = {}
     if geom.cache_dtype:
         kw.update(k_exponents=exps[0], v_exponents=exps[1])
@@ -126,6 +126,10 @@ CASES = {
     "e4m3_scale_negative": ([1, 140], [77, 140], 16, False, dict(N=4, N_kv=2, D=64, scale=-0.1, **W)),
     "e4m3_rows_without_keys": ([20, 3], [40, 3], 16, False, dict(N=2, N_kv=1, D=64, sparse_mode=4, pre_tokens=30,
                                                                next_tokens=-5)),
+    "e4m3_short_units": ([16 * 9] * 8, [144, 150, 200, 256, 300, 400, 144, 145], 16, False, dict(N=16, N_kv=16, D=64, pre_tokens=3,
+                                                                                             **W)),
+    "e4m3_short_units_d72": ([144] * 8, [144, 150, 200, 256, 300, 400, 144, 145], 16, False,
+                             dict(N=16, N_kv=16, D=72, pre_tokens=3, **W)),
     "e4m3_mqa_48": ([3], [200], 16, False, dict(N=48, N_kv=1, D=64, **W)),
 }
 
@@ -134,6 +138,41 @@ CASES = {
 def test_attention_matches_the_definition(name):
     q_lens, kv_lens, page, tree, kw = CASES[name]
     check(geometry(q_lens, kv_lens, page, **kw), kv_lens, 11, tree)
+
+
+@pytest.mark.parametrize("dtype,spread,loud", [("bf16", 25, 1.0), ("bf16", 60, 1.0), ("fp16", 12, 1.0), ("bf16", 6, 1e-20),
+                                               ("bf16", 6, 30.0)])
+@pytest.mark.parametrize("q_lens,kv_lens,D", [([1, 2], [700, 90], 128), ([140, 40], [700, 90], 128), ([1], [3000], 64),
+                                              ([90], [300], 72), ([3], [300], 40)])
+def test_rows_of_very_different_size_in_the_8_bit_cache(dtype, spread, loud, q_lens, kv_lens, D):
+    """Exponents far apart within a tile and from tile to tile, rows of zeros, queries of any size."""
+    geom = geometry(q_lens, kv_lens, 16, N=4, N_kv=2, D=D, dtype=dtype, cache_dtype="e4m3",
+                    scale=D ** -0.5 * (1e20 if loud < 1e-9 else 1.0), **W)
+    check(geom, kv_lens, 17, spread=spread, loud=loud)
+
+
+@pytest.mark.parametrize("q_len", [1, 150])
+def test_a_key_without_values_may_have_all_the_weight(q_len):
+    """A first key that every query prefers, with a row of zeros for its values, among keys with large ones."""
+    n = 500
+    geom = geometry([q_len], [n], 16, N=2, N_kv=1, D=64, cache_dtype="e4m3", **W)
+    p = make(geom, [n], 8)
+    k, v = p["ks"][0].clone(), p["vs"][0].clone()
+    k[0] = 0.6
+    p["q"] = (p["q"].float().abs() + 1.0).to(p["q"].dtype)
+    v[0] = 0.0
+    v[-3:] *= 64.0
+    for x, t in enumerate((k, v)):
+        codes, e = encode(t, "bf16")
+        for j in range(n):
+            page, slot = int(p["table"][0, j // 16]), j % 16
+            p["pages"][x].view(torch.uint8)[page, :, slot] = codes[j].view(torch.uint8)
+            p["kw"][("k_exponents", "v_exponents")[x]][page, :, slot] = e[j]
+        p["ks" if x == 0 else "vs"] = [decode(codes, e)]
+    ref, err = attention_ref(geom, p["q"], p["ks"], p["vs"], [n])
+    assert (ref[2] < 6.0).all()  # (a good part of the weight is on it)
+    for what, x, r, e in zip(("out", "softmax_max", "softmax_sum"), run(geom, p), ref, err):
+        assert_within(x, r, e, what)
 
 
 def test_more_sequences_than_a_table_holds():
@@ -433,3 +472,210 @@ def test_serving_a_conversation(cache):
     # two evaluations, each within the roundings of P and of the result (2^-8 each) of |values| that reach 4.5
     assert (out - dense.float()).abs().max() <= 2 * 2 * 2.0 ** -8 * v.float().abs().max()
     assert (out - dense.float()).norm() <= 6e-3 * dense.float().norm()
+
+
+# ----------------------------------------------------------------- safety --
+def test_unpacked_pages_in_passes():
+    """Bounds on the lengths whose 16-bit pages do not fit the workspace at once: some sequences after the others."""
+    q_lens, kv_lens = [40, 30, 1, 50, 33], [300, 90, 40, 200, 33]
+    geom = geometry(q_lens, kv_lens, 16, N=8, N_kv=8, D=128, cache_dtype="e4m3", sparse_mode=4, next_tokens=0)
+    geom.max_pages = 131072 // 16
+    assert swa.swa_paged_forward_workspace_size(swa.PagedParams(geom)) < (1 << 30) + (64 << 20)
+    check(geom, kv_lens, 9)
+    check(geometry(q_lens, kv_lens, 16, N=8, N_kv=8, D=128, cache_dtype="e4m3", max_kv_len=300, **W), kv_lens, 9)
+
+
+def guarded(call):
+    """Status that `call` raises, or None."""
+    try:
+        call()
+    except swa.SwaError as e:
+        return e.status
+    return None
+
+
+@pytest.mark.parametrize("name", ["sinks_mixed", "tree_mixed", "e4m3_mixed", "e4m3_tree_sinks", "e4m3_d72", "e4m3_sinks",
+                                  "tree_past_a_tile", "e4m3_split", "e4m3_chunk_split"])
+def test_bounds_checked_build_gives_the_same_bits(name):
+    q_lens, kv_lens, page, tree, kw = CASES[name]
+    if name.startswith("e4m3"):
+        kw = dict(kw, cache_dtype="e4m3")
+    geom = geometry(q_lens, kv_lens, page, **kw)
+    p = make(geom, kv_lens, 11, tree)
+    ref = run(geom, p)
+    with swa.using(swa.checked_lib()):
+        got = run(geom, p)  # (raises where an access was skipped)
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cache", ["", "e4m3"])
+@pytest.mark.parametrize("q_len", [1, 4, 60])
+def test_bad_pages_and_lengths_are_reported_and_not_followed(cache, q_len):
+    kv_lens = [200, 100]
+    kw = dict(N=4, N_kv=2, D=64, pre_tokens=60, sink_tokens=20, cache_dtype=cache, **W)
+    geom = geometry([q_len, q_len], kv_lens, 16, **kw)
+    p = make(geom, kv_lens, 3)
+    good = run(geom, p)
+    for entry, bad in ((0, -1), (0, geom.num_pages), (11, 2 ** 31 - 1), (12, -2 ** 31)):
+        table = p["table"].clone()
+        table[0, entry] = bad
+        ws = swa.paged_forward_workspace(geom, DEV)
+        ws.fill_(0xA5)
+        dev = {n: t.to(DEV) for n, t in p["kw"].items()}
+        out = swa.paged_forward(geom, p["q"].to(DEV), *[t.to(DEV) for t in p["pages"]], table.to(DEV), p["lens"].to(DEV),
+                                workspace=ws, **dev)
+        assert guarded(lambda: swa.check_paged_forward(geom, ws)) == swa.SWA_ERR_PAGE
+        for a, b in zip(out, good):
+            assert torch.equal(a[q_len:], b[q_len:])
+        # a page that is not followed reads as zeros
+        ks, vs = [t.clone() for t in p["ks"]], [t.clone() for t in p["vs"]]
+        ks[0][16 * entry:16 * entry + 16], vs[0][16 * entry:16 * entry + 16] = 0, 0
+        ref, err = attention_ref(geom, p["q"], ks, vs, kv_lens)
+        for x, r, e in zip(out, ref, err):
+            assert_within(x, r, e, (entry, bad))
+    for bad in (-1, geom.max_pages * 16 + 1):
+        lens = p["lens"].clone()
+        lens[0] = bad
+        ws = swa.paged_forward_workspace(geom, DEV)
+        dev = {n: t.to(DEV) for n, t in p["kw"].items()}
+        out = swa.paged_forward(geom, p["q"].to(DEV), *[t.to(DEV) for t in p["pages"]], p["table"].to(DEV), lens.to(DEV),
+                                workspace=ws, **dev)
+        assert guarded(lambda: swa.check_paged_forward(geom, ws)) == swa.SWA_ERR_PAGE
+        assert (out[0][:q_len] == 0).all() and torch.isinf(out[1][:q_len]).all() and (out[2][:q_len] == 0).all()
+        for a, b in zip(out, good):
+            assert torch.equal(a[q_len:], b[q_len:])
+
+
+def test_bad_pages_in_append_and_gather():
+    geom = geometry([20, 3], [90, 40], 16, N=2, D=64, cache_dtype="e4m3")
+    rows = [torch.randn(23, 2, 64, generator=torch.Generator().manual_seed(x)).bfloat16().to(DEV) for x in range(2)]
+    table, lens = chunk_pages(geom, [90, 40], 1)
+    for bad_table, bad_lens in (((0, 5, geom.num_pages), None), ((1, 2, -1), None), (None, (0, -3)), (None, (1, 10 ** 9))):
+        t, n = table.clone(), lens.clone()
+        if bad_table:
+            t[bad_table[0], bad_table[1]] = bad_table[2]
+        if bad_lens:
+            n[bad_lens[0]] = bad_lens[1]
+        pages, exps = empty_cache(geom)
+        kw = dict(k_exponents=exps[0], v_exponents=exps[1])
+        ws = swa.paged_append_workspace(geom, DEV)
+        swa.paged_append(geom, *rows, *pages, t, n, workspace=ws, **kw)
+        assert guarded(lambda: swa.check_paged_append(geom, ws)) == swa.SWA_ERR_PAGE
+        k, v = swa.paged_gather(geom, *pages, t, n, workspace=ws, **kw)
+        assert guarded(lambda: swa.check_paged_append(geom, ws)) == swa.SWA_ERR_PAGE
+        # what was stored comes back; the rest is zeros
+        for x, got in zip(rows, (k, v)):
+            want = decode(*encode(x.cpu(), "bf16"))
+            got = got.cpu().double()
+            hit = (got == want).all(-1).all(-1)
+            assert (got[~hit] == 0).all() and hit.any() and not hit.all()
+
+
+@pytest.mark.parametrize("cache,tree,q_len", [("", True, 61), ("", False, 1), ("e4m3", False, 1), ("e4m3", True, 61),
+                                              ("e4m3", False, 4)])
+def test_replayed_graph_follows_new_lengths_trees_and_pages(cache, tree, q_len):
+    """A captured step replays with new lengths, tables, trees, depths and exponents in place, on another stream; two
+    captured steps with workspaces of their own run after one another; the bits are the eager ones."""
+    kv = [[300, 90], [500, 61], [70, 444]]
+    base = dict(N=8, N_kv=2, D=64, pre_tokens=100, sink_tokens=5, cache_dtype=cache, **W)
+    most = geometry([q_len] * 2, [500, 500], 16, max_kv_len=500, **base)
+    problems = []
+    for x, lens in enumerate(kv):
+        geom = geometry([q_len] * 2, [max(n, q_len) for n in lens], 16, **base)
+        geom.num_pages, geom.max_pages, geom.max_kv_len = most.num_pages, most.max_pages, most.max_kv_len
+        problems.append(make(geom, [max(n, q_len) for n in lens], 20 + x, tree))
+    fixed = {n: t.to(DEV) for n, t in problems[0]["kw"].items()}
+    fixed.update(q=problems[0]["q"].to(DEV), k=problems[0]["pages"][0].to(DEV), v=problems[0]["pages"][1].to(DEV),
+                 table=problems[0]["table"].to(DEV), lens=problems[0]["lens"].to(DEV))
+    plan = swa.PagedParams(most)
+    extra = {n: fixed[n] for n in problems[0]["kw"]}
+
+    def call(ws):
+        return swa.paged_forward(plan, fixed["q"], fixed["k"], fixed["v"], fixed["table"], fixed["lens"], workspace=ws, **extra)
+
+    spaces = [swa.paged_forward_workspace(plan, DEV) for _ in range(3)]
+    call(spaces[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for ws in spaces[1:]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res = call(ws)
+        graphs.append((graph, res, ws))
+    side = torch.cuda.Stream()
+    for p in problems:
+        as_bytes = lambda t: t.view(torch.uint8) if cache else t
+        for n, t in (("q", p["q"]), ("table", p["table"]), ("lens", p["lens"]), *p["kw"].items()):
+            fixed[n].copy_(t.to(DEV))
+        for n, t in zip("kv", p["pages"]):
+            as_bytes(fixed[n]).copy_(as_bytes(t).to(DEV))
+        ref = call(spaces[0])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for graph, _, _ in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, res, ws in graphs:
+            swa.check_paged_forward(plan, ws)
+            for a, b in zip(ref, res):
+                assert torch.equal(a, b)
+
+
+def test_another_stream():
+    geom = geometry([61, 1], [500, 300], 16, N=8, N_kv=2, D=64, cache_dtype="e4m3", **W)
+    p = make(geom, [500, 300], 4)
+    ref = run(geom, p)
+    dev = dict(q=p["q"].to(DEV), table=p["table"].to(DEV), lens=p["lens"].to(DEV), **{n: t.to(DEV) for n, t in p["kw"].items()})
+    pages = [t.to(DEV) for t in p["pages"]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = swa.paged_forward(geom, dev["q"], *pages, dev["table"], dev["lens"], k_exponents=dev["k_exponents"],
+                            v_exponents=dev["v_exponents"], stream=side)
+    k, v = swa.paged_gather(geom, *pages, dev["table"], dev["lens"], k_exponents=dev["k_exponents"],
+                            v_exponents=dev["v_exponents"], stream=side)
+    side.synchronize()
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+    assert torch.equal(k[-1].cpu().double(), p["ks"][1][-1])
+
+
+def test_python_refusals():
+    geom = geometry([3, 40], [50, 90], 16, N=4, N_kv=2, D=64, cache_dtype="e4m3")
+    p = make(geom, [50, 90], 4, True)
+    a = dict(q=p["q"], k_pages=p["pages"][0], v_pages=p["pages"][1], block_table=p["table"], kv_lens=p["lens"], **p["kw"])
+    a = {n: t.to(DEV) for n, t in a.items()}
+    swa.paged_forward(geom, **a)
+    wrong = {
+        "k_pages": [a["k_pages"].view(torch.uint8), a["k_pages"].view(torch.int8), a["k_pages"][:-1]],
+        "v_pages": [a["v_pages"].float().bfloat16()],
+        "k_exponents": [a["k_exponents"].view(torch.uint8), a["k_exponents"][:-1], a["k_exponents"].transpose(1, 2),
+                        a["k_exponents"].cpu(), 3],
+        "v_exponents": [a["v_exponents"].int(), a["v_exponents"][..., :-1]],
+        "tree": [a["tree"].long(), a["tree"][:-1], a["tree"][:, :1], a["tree"].flatten(), a["tree"].t().contiguous().t(),
+                 a["tree"].cpu(), "tree"],
+        "depth": [a["depth"].long(), a["depth"][:-1], a["depth"][:, None], a["depth"].cpu(), a["depth"].repeat(2)[::2]],
+    }
+    for name, values in wrong.items():
+        for value in values:
+            with pytest.raises(ValueError, match="k_exponents|v_exponents|tree|depth|k_pages|v_pages"):
+                swa.paged_forward(geom, **{**a, name: value})
+    for name in ("k_exponents", "v_exponents"):
+        with pytest.raises(swa.SwaError) as e:
+            swa.paged_forward(geom, **{**a, name: None})
+        assert e.value.status == swa.SWA_ERR_PARAM_NULLPTR
+    with pytest.raises(swa.SwaError):
+        swa.paged_forward(geom, **{**a, "tree": None})  # a depth without a tree
+    kv = [torch.zeros(43, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    cache = {n: a[n] for n in ("k_pages", "v_pages", "block_table", "kv_lens")}
+    exps = {n: a[n] for n in ("k_exponents", "v_exponents")}
+    for value in (kv[0][:-1], kv[0].half(), kv[0].cpu(), kv[0][..., :-1]):
+        with pytest.raises(ValueError):
+            swa.paged_gather(geom, **cache, k=value, v=kv[1], **exps)
+        with pytest.raises(ValueError):
+            swa.paged_append(geom, value, kv[1], **cache, **exps)
+    with pytest.raises(swa.SwaError):
+        swa.paged_gather(geom, **cache)
+    with pytest.raises(swa.SwaError):
+        swa.paged_append(geom, *kv, **cache)
+    torch.cuda.synchronize()
