@@ -24,7 +24,8 @@ CHECKED_BUILD_DIR = os.path.join(PKG, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libswa_checked.so")
 # the CPython extension that calls the rotary and paged-cache entry points on torch tensors
 BIND_SOURCE = "swa_bind.cpp"
-SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_pair.cu", "swa_bwd_dkv.cu", "swa_bwd_dq.cu", "swa_aux.cu",
+SOURCES = ["swa_api.cpp", "swa_fwd.cu", "swa_fwd_sinks.cu", "swa_fwd_pair.cu", "swa_fwd_pair_sinks.cu", "swa_bwd_dkv.cu",
+           "swa_bwd_dkv_sinks.cu", "swa_bwd_dq.cu", "swa_bwd_dq_sinks.cu", "swa_bwd_join.cu", "swa_aux.cu",
            "swa_noalloc.cu", "swa_host.cpp", "swa_rope.cu", "swa_paged_rows.cu", "swa_paged_rows_masks.cu",
            "swa_paged_rows_e4m3.cu", "swa_paged_tile.cu", "swa_paged_tile_masks.cu", "swa_paged_unpack.cu",
            "swa_paged_join.cu", "swa_paged_gather.cu", "swa_paged.cpp"]

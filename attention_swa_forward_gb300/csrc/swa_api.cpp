@@ -575,7 +575,9 @@ swa_status_t swa_forward(const swa_params_t* p, const void* q, const void* k, co
   auto one = [&](const auto& t) {
     FwdArgs at = a;
     at.clear_err = (launches++ == 0 && !SWA_CHECKS) ? 1 : 0;
-    return pair ? launch_forward_pair(at, t, mq, mk, mv, s) : launch_forward(at, t, mq, mk, mv, s);
+    if (at.g.sinks > 0)
+      return pair ? launch_forward_pair<true>(at, t, mq, mk, mv, s) : launch_forward<true>(at, t, mq, mk, mv, s);
+    return pair ? launch_forward_pair<false>(at, t, mq, mk, mv, s) : launch_forward<false>(at, t, mq, mk, mv, s);
   };
   e = run_tables(descs, one, one);
   if (t_ev[1]) cudaEventRecord(t_ev[1], s);
@@ -667,7 +669,8 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
   const std::vector<SeqDesc> kv_descs = build_descs(plan, false);
   if (t_ev[2]) cudaEventRecord(t_ev[2], s);
   auto key_major = [&](const auto& t) {
-    const cudaError_t le = launch_backward_dkv(a, t, mq, mk, mv, mdy, s);
+    const cudaError_t le = a.g.sinks > 0 ? launch_backward_dkv<true>(a, t, mq, mk, mv, mdy, s)
+                                         : launch_backward_dkv<false>(a, t, mq, mk, mv, mdy, s);
     a.part_base += piece_items(t.d, t.count);
     return le;
   };
@@ -677,9 +680,11 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
   // query-major pass: dQ (one work item per query tile)
   const std::vector<SeqDesc> q_descs = build_descs(plan, true);
   if (t_ev[4]) cudaEventRecord(t_ev[4], s);
-  e = run_tables(
-      q_descs, [&](const SeqTable<kSmallTable>& t) { return launch_backward_dq(a, t, mq, mk, mv, mdy, s); },
-      [&](const SeqTable<kLargeTable>& t) { return launch_backward_dq(a, t, mq, mk, mv, mdy, s); });
+  auto query_major = [&](const auto& t) {
+    return a.g.sinks > 0 ? launch_backward_dq<true>(a, t, mq, mk, mv, mdy, s)
+                         : launch_backward_dq<false>(a, t, mq, mk, mv, mdy, s);
+  };
+  e = run_tables(q_descs, query_major, query_major);
   if (t_ev[5]) cudaEventRecord(t_ev[5], s);
   if (e != cudaSuccess) return cuda_fail(e, "backward dQ launch");
   // (behind the query-major pass, which ends after the key-major one)

@@ -1,0 +1,13 @@
+// swa_bwd_dq_sinks.cu — swa_bwd_dq.cuh with sinks.
+#include "swa_bwd_dq.cuh"
+
+namespace swa {
+
+template cudaError_t launch_backward_dq<true, kSmallTable>(
+    const BwdArgs&, const SeqTable<kSmallTable>&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+    cudaStream_t);
+template cudaError_t launch_backward_dq<true, kLargeTable>(
+    const BwdArgs&, const SeqTable<kLargeTable>&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+    cudaStream_t);
+
+}  // namespace swa

@@ -81,10 +81,11 @@ __device__ __forceinline__ void key_window(const Geometry& g, const SeqInfo& s, 
 __device__ __forceinline__ int d_steps(const Geometry& g) { return (g.D + 15) >> 4; }
 
 // Is every (i, j) of the query tile [q0, q0+128) x key tile [j0, j0+128) visible?
+template <bool SINKS>
 __device__ __forceinline__ bool tile_fully_visible(const Geometry& g, const SeqInfo& s, int q0, int j0) {
   if (q0 + 127 >= s.q_len || j0 + 127 >= s.kv_len) return false;
   if (g.sparse_mode != 4) return true;
-  return (j0 >= q0 + 127 - g.pre || j0 + 127 < g.sinks) && j0 + 127 <= q0 + g.next;
+  return (j0 >= q0 + 127 - g.pre || (SINKS && j0 + 127 < g.sinks)) && j0 + 127 <= q0 + g.next;
 }
 
 // TMA load of 128 rows x D columns starting at local row `row0` of (b, n) into

@@ -188,19 +188,21 @@ int64_t debug_extent_slack();
 
 // Kernel launchers (defined in the .cu files).  Each returns the launch's
 // cudaError_t.
-template <int CAP>
+// SINKS (here and below): the problem has sinks; each in a translation unit of its own, and problems without run
+// what they ran before there were any.
+template <bool SINKS, int CAP>
 cudaError_t launch_forward(const FwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq, const CUtensorMap& mk,
                            const CUtensorMap& mv, cudaStream_t stream);
 // D <= 64: one CTA per pair of query tiles; the table's entries count pairs
 // (tiles = ceil(query tiles / 2)).
-template <int CAP>
+template <bool SINKS, int CAP>
 cudaError_t launch_forward_pair(const FwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq,
                                 const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream);
-template <int CAP>
+template <bool SINKS, int CAP>
 cudaError_t launch_backward_dkv(const BwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq,
                                 const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdy,
                                 cudaStream_t stream);
-template <int CAP>
+template <bool SINKS, int CAP>
 cudaError_t launch_backward_dq(const BwdArgs& a, const SeqTable<CAP>& tab, const CUtensorMap& mq,
                                const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdy,
                                cudaStream_t stream);

@@ -179,7 +179,7 @@ swa_status_t rope_plan(const swa_rope_params_t* p, RopeArgs& a, int64_t* n_kv) {
 // Split of the tokens over CTAs, and of a CTA over its threads: units of
 // 2 * VEC elements, row_lanes rows at a time.
 void set_split(RopeArgs& a, int dtype, int64_t rows) {
-  const bool q8 = a.pg.k_exp != nullptr;
+  const bool q8 = a.ex.k != nullptr;
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
   a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.H - 1) / a.H);
   a.units = static_cast<int32_t>(ceil_div(a.D, 2 * rope_vec(dtype, a.R)));
@@ -364,7 +364,7 @@ swa_status_t page_strides(const swa_page_strides_t* given, const swa_paged_param
 swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, const void* k_pages,
                         const swa_page_strides_t* k_s, const void* v_pages, const swa_page_strides_t* v_s,
                         const int8_t* k_exp, const int8_t* v_exp, const int32_t* table, int64_t table_stride,
-                        const int32_t* kv_lens, PagedGeom& g) {
+                        const int32_t* kv_lens, PagedGeom& g, PagedExps& ex) {
   swa_status_t st;
   const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
   if (q8) {
@@ -403,11 +403,11 @@ swa_status_t paged_geom(const swa_paged_params_t* p, const PagedPlan& plan, cons
   g.n_k = less_slack(g.n_k);
   g.n_v = less_slack(g.n_v);
   if (q8) {
-    g.k_exp = const_cast<int8_t*>(k_exp);
-    g.v_exp = const_cast<int8_t*>(v_exp);
-    g.exp_page = plan.N_kv * p->page_size;
-    g.n_exp = less_slack(p->num_pages * g.exp_page);
-    g.wide = (p->D | g.k_page | g.k_head | g.k_slot | g.v_page | g.v_head | g.v_slot) % 16 == 0 ? 1 : 0;
+    ex.k = const_cast<int8_t*>(k_exp);
+    ex.v = const_cast<int8_t*>(v_exp);
+    ex.page = plan.N_kv * p->page_size;
+    ex.n = less_slack(p->num_pages * ex.page);
+    ex.wide = (p->D | g.k_page | g.k_head | g.k_slot | g.v_page | g.v_head | g.v_slot) % 16 == 0 ? 1 : 0;
   }
   g.n_table = (p->B - 1) * table_stride + p->max_pages;
   g.n_lens = p->B;
@@ -751,7 +751,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     a.clear_err = 0;
     a.k_pages = u.k;
     a.v_pages = u.v;
-    a.g.k_exp = a.g.v_exp = nullptr;
+    a.ex = PagedExps{};
     a.g.table = u.table;
     a.g.table_stride = sc.entries;
     a.g.page_size = kPagedTileStep;
@@ -768,7 +768,7 @@ cudaError_t run_part(const swa_paged_params_t* p, const ForwardPlan& f, const Pa
     if (joins) e = launch_paged_join(a, tab, static_cast<int>(part.step), s);
     else if (!few) e = masks ? launch_paged_tile<PagedKind::kMasks>(a, tab, mk, mv, mq, s)
                              : launch_paged_tile<PagedKind::kPlain>(a, tab, mk, mv, mq, s);
-    else if (a.g.k_exp) e = launch_paged_rows_e4m3(a, tab, mk, mv, s);
+    else if (a.ex.k) e = launch_paged_rows_e4m3(a, tab, mk, mv, s);
     else e = masks ? launch_paged_rows<PagedKind::kMasks>(a, tab, s) : launch_paged_rows<PagedKind::kPlain>(a, tab, s);
     a.item_base += tab.n_items;
     a.clear_err = 0;
@@ -907,7 +907,7 @@ swa_status_t swa_paged_append_ext(const swa_paged_params_t* p, const void* k, co
     if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
     if (q && ((st = check_pointer(q, "q")) != SWA_OK || (st = check_pointer(q_out, "q_out")) != SWA_OK)) return st;
     st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, k_exponents, v_exponents, block_table,
-                    table_stride, kv_lens, a.pg);
+                    table_stride, kv_lens, a.pg, a.ex);
     if (st != SWA_OK) return st;
     const size_t need = append_bytes(p);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != SWA_OK) return st;
@@ -1005,7 +1005,7 @@ swa_status_t swa_paged_forward_ext(const swa_paged_params_t* p, const void* q, c
       return fail(SWA_ERR_PARAM_INVALID, "softmax_max and softmax_sum must be 4-byte aligned");
     PagedArgs a{};
     st = paged_geom(p, f.seq, k_pages, k_page_strides, v_pages, v_page_strides, x.k_exponents, x.v_exponents,
-                    block_table, table_stride, kv_lens, a.g);
+                    block_table, table_stride, kv_lens, a.g, a.ex);
     if (st != SWA_OK) return st;
     if (x.tree) {
       const int64_t words = ceil_div(*std::max_element(f.seq.len.begin(), f.seq.len.end()), 32);
@@ -1055,7 +1055,7 @@ swa_status_t swa_paged_forward_ext(const swa_paged_params_t* p, const void* q, c
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     CUtensorMap mk{}, mv{}, mq{}, rk{}, rv{};
-    if (f.rows.items > 0 && a.g.k_exp && a.g.wide) {  // groups of 16 slots, for the few-row kernel
+    if (f.rows.items > 0 && a.ex.k && a.ex.wide) {  // groups of 16 slots, for the few-row kernel
       st = page_map(&rk, &a.kd, k_pages, swa_page_strides_t{a.g.k_page, a.g.k_head, a.g.k_slot}, p, f.seq.N_kv, 16,
                     "k_pages");
       if (st == SWA_OK)
@@ -1090,7 +1090,7 @@ swa_status_t swa_paged_forward_ext(const swa_paged_params_t* p, const void* q, c
       if (part.items == 0 || e != cudaSuccess || (joins && (part.splits <= 1 || part.cluster))) return;
       const bool few = &part == &f.rows;
       const CUtensorMap &k = few ? rk : mk, &v = few ? rv : mv;
-      if (few && a.g.k_exp) {
+      if (few && a.ex.k) {
         a.kd = rows_kd;
         a.vd = rows_vd;
       }
@@ -1126,7 +1126,7 @@ swa_status_t swa_paged_gather(const swa_paged_params_t* p, const void* k_pages, 
     if ((st = check_pointer(k, "k")) != SWA_OK || (st = check_pointer(v, "v")) != SWA_OK) return st;
     GatherArgs a{};
     st = paged_geom(p, plan, k_pages, k_page_strides, v_pages, v_page_strides, k_exponents, v_exponents, block_table,
-                    table_stride, kv_lens, a.pg);
+                    table_stride, kv_lens, a.pg, a.ex);
     if (st != SWA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, append_bytes(p))) != SWA_OK) return st;
     a.src[0] = k_pages;
@@ -1145,7 +1145,7 @@ swa_status_t swa_paged_gather(const swa_paged_params_t* p, const void* k_pages, 
       a.dst_h[x] = s.head;
       a.n_dst[x] = less_slack(n);
     }
-    const int64_t pieces = ceil_div(p->D, a.pg.k_exp ? 16 : 8);  // threads of a row
+    const int64_t pieces = ceil_div(p->D, a.ex.k ? 16 : 8);  // threads of a row
     while ((int64_t(1) << a.lane_shift) < pieces) ++a.lane_shift;
     a.lanes = 1 << a.lane_shift;
     // few tokens: over the SMs; many: as many per CTA as a thread needs for its rows in flight

@@ -37,12 +37,16 @@ struct PagedGeom {
   int64_t v_page, v_head, v_slot;
   const int32_t* table;
   const int32_t* kv_lens;
-  // 8-bit cache: the exponents of its rows, [pages][N_kv][page_size]; exp_page: of a page
-  int8_t *k_exp, *v_exp;
-  int64_t exp_page;
-  int32_t wide;  // 8-bit cache: rows start on 16 bytes and are multiples of 16 long (else of 8)
   // extents of the caller's tensors in elements, for the bounds-checked build
-  int64_t n_k, n_v, n_table, n_lens, n_exp;
+  int64_t n_k, n_v, n_table, n_lens;
+};
+
+// 8-bit cache: the exponents of its rows, [pages][N_kv][page_size].
+struct PagedExps {
+  int8_t *k, *v;  // NULL: a 16-bit cache
+  int64_t page;   // exponents of a page
+  int64_t n;      // extent, for the bounds-checked build
+  int32_t wide;   // rows of codes start on 16 bytes and are multiples of 16 long (else of 8)
 };
 
 // The exponents of an 8-bit row: least (bf16, fp16) and most.  A larger one
@@ -81,12 +85,14 @@ struct RopeArgs {
   int32_t tok_begin;  // append: first token of this launch
   uint64_t freq[64];  // angle per position as a fraction of a turn, 2^64 = one turn
   uint8_t axis[64];
+  PagedExps ex;       // append
 };
 
 // The tokens of a chunk read back from the pages.
 constexpr int kGatherThreads = 256, kGatherMostTok = 16;
 struct GatherArgs {
   PagedGeom pg;
+  PagedExps ex;
   const void* src[2];           // k, v pages
   void* dst[2];
   int64_t dst_r[2], dst_h[2];   // strides: row, head
@@ -126,19 +132,12 @@ struct PagedArgs {
   int32_t f16;
   int32_t sparse_mode;
   int32_t pre, next;  // clamped so that position sums stay inside int32
-  int32_t sinks;      // BAND: keys below this one stay visible behind the window
-  // a chunk that is a tree of drafted tokens: bit c of row t: token t sees token c of its chunk
-  const uint32_t* tree;
-  int64_t tree_row;      // words between rows
-  const int32_t* depth;  // of each token; NULL: its place in the chunk
-  int64_t n_tree, n_depth;  // extents, for the bounds-checked build
   float scale_log2;
   int32_t whole;      // tile kernel: the first items of the launch, one unit each; the others are split
   int32_t splits;     // CTAs (units) per split item along the keys, at most
   int32_t par, cap, least;  // paged_split
   int32_t cluster;    // few-row kernel: the splits are a cluster, which joins them itself
   int32_t rows_pad;   // rows of a partial tile
-  int32_t most_rows;  // rows that some tile has
   int32_t stall;      // test hook (kStallPaged)
   int32_t box_rows;   // slots per TMA box: the largest power of two dividing the page size, up to 128
   PageDims kd, vd;
@@ -159,6 +158,15 @@ struct PagedArgs {
   int32_t overlap;    // few-row kernel: that next grid
   int32_t* page_err;  // per unit of the call: [whole], then [items - whole][splits]
   int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build
+  // (what only some calls have comes last: the others' kernels load fewer lines of their arguments)
+  int32_t sinks;      // BAND: keys below this one stay visible behind the window
+  int32_t most_rows;  // rows that some tile has
+  // a chunk that is a tree of drafted tokens: bit c of row t: token t sees token c of its chunk
+  const uint32_t* tree;
+  int64_t tree_row;      // words between rows
+  const int32_t* depth;  // of each token; NULL: its place in the chunk
+  int64_t n_tree, n_depth;  // extents, for the bounds-checked build
+  PagedExps ex;
 };
 
 // Row r of a tile belongs to its token r / gs (r < 128; gs_magic = ceil(2^16 / gs), exact there).

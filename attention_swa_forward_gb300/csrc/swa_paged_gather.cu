@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kGatherThreads)
       if (page >= 0 && page < g.num_pages) {
         k = page * g.k_page + slot * g.k_slot;
         v = page * g.v_page + slot * g.v_slot;
-        ex = page * g.exp_page + slot;
+        ex = page * a.ex.page + slot;
       } else {
         bad = kPageErrEntry;
       }
@@ -102,14 +102,14 @@ __global__ void __launch_bounds__(kGatherThreads)
       const int64_t extent = w.x ? g.n_v : g.n_k;
       if constexpr (Q8) {
         const uint8_t* p = static_cast<const uint8_t*>(a.src[w.x]) + w.src;
-        if (g.wide) {
+        if (a.ex.wide) {
           if (in_bounds(w.src, 16, extent, a.err)) in[y] = __ldcs(reinterpret_cast<const uint4*>(p));
         } else {  // rows start on 8 bytes, and the last 16 codes may be 8
           if (in_bounds(w.src, 8, extent, a.err)) *reinterpret_cast<uint2*>(&in[y].x) = __ldcs(reinterpret_cast<const uint2*>(p));
           if (c + 8 < g.D && in_bounds(w.src + 8, 8, extent, a.err))
             *reinterpret_cast<uint2*>(&in[y].z) = __ldcs(reinterpret_cast<const uint2*>(p + 8));
         }
-        if (in_bounds(w.ex, 1, g.n_exp, a.err)) e[y] = (w.x ? g.v_exp : g.k_exp)[w.ex];
+        if (in_bounds(w.ex, 1, a.ex.n, a.err)) e[y] = (w.x ? a.ex.v : a.ex.k)[w.ex];
       } else if (in_bounds(w.src, 8, extent, a.err)) {
         in[y] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[w.x]) + w.src));
       }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kGatherThreads)
 template <int CAP>
 cudaError_t launch_gather(const GatherArgs& a, const PagedTable<CAP>& tab, bool f16, int n_ctas, cudaStream_t stream) {
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(n_ctas), dim3(kGatherThreads), 0, stream, a, tab); };
-  if (a.pg.k_exp) return f16 ? go(swa_paged_gather_kernel<true, true, CAP>) : go(swa_paged_gather_kernel<false, true, CAP>);
+  if (a.ex.k) return f16 ? go(swa_paged_gather_kernel<true, true, CAP>) : go(swa_paged_gather_kernel<false, true, CAP>);
   return go(swa_paged_gather_kernel<false, false, CAP>);  // (copies bits)
 }
 template cudaError_t launch_gather<kPagedSmallTable>(const GatherArgs&, const PagedTable<kPagedSmallTable>&, bool, int,

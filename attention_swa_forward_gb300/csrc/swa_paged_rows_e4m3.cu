@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kRowsThreads, NB == 1 ? 4 : 2)
     const int page = __shfl_sync(0xFFFFFFFFu, my_page, it & 31), slot = __shfl_sync(0xFFFFFFFFu, my_slot, it & 31);
     if (it >= n_it) return;
     const int st = it % kStages;
-    const int64_t e = static_cast<int64_t>(page) * g.exp_page + hk * g.page_size + slot;
+    const int64_t e = static_cast<int64_t>(page) * a.ex.page + hk * g.page_size + slot;
     if constexpr (WIDE) {
       if (lane == 0) {
         uint64_t* bar = &s.full[warp][st];
@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(kRowsThreads, NB == 1 ? 4 : 2)
         auto at = [&](const PageDims& d, int dim) { return d.slot_at == dim ? slot : (d.head_at == dim ? hk : page); };
         tma_load_4d(s.ring[warp][st][0], &mk, bar, 0, at(a.kd, 1), at(a.kd, 2), at(a.kd, 3));
         tma_load_4d(s.ring[warp][st][1], &mv, bar, 0, at(a.vd, 1), at(a.vd, 2), at(a.vd, 3));
-        const bool in = page < g.num_pages && in_bounds(e, 16, g.n_exp, a.err);
-        bulk_load16(s.exps[warp][st][0], in ? g.k_exp + e : kNoExponents, bar);
-        bulk_load16(s.exps[warp][st][1], in ? g.v_exp + e : kNoExponents, bar);
+        const bool in = page < g.num_pages && in_bounds(e, 16, a.ex.n, a.err);
+        bulk_load16(s.exps[warp][st][0], in ? a.ex.k + e : kNoExponents, bar);
+        bulk_load16(s.exps[warp][st][1], in ? a.ex.v + e : kNoExponents, bar);
       }
     } else {
       // two lanes a row, 8 bytes at a time
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kRowsThreads, NB == 1 ? 4 : 2)
         }
       }
       if (lane < 4) {  // exponents: 8 of K, 8 of K, 8 of V, 8 of V
-        const int8_t* exps = lane < 2 ? g.k_exp : g.v_exp;
-        const bool in = page < g.num_pages && in_bounds(e + half * 8, 8, g.n_exp, a.err);
+        const int8_t* exps = lane < 2 ? a.ex.k : a.ex.v;
+        const bool in = page < g.num_pages && in_bounds(e + half * 8, 8, a.ex.n, a.err);
         cp_async8(smem_u32(s.exps[warp][st][lane >> 1] + half * 8), in ? exps + e + half * 8 : exps, in);
       }
       cp_async_arrive(&s.full[warp][st]);
@@ -485,7 +485,7 @@ cudaError_t launch_paged_rows_e4m3(const PagedArgs& a, const PagedTable<CAP>& ta
                      : launch_rows8_t<dp.value, nb.value, wide.value, false>(a, tab, mk, mv, stream);
   };
   auto pick = [&](auto dp, auto nb) {
-    return a.g.wide ? go(dp, nb, std::true_type{}) : go(dp, nb, std::false_type{});
+    return a.ex.wide ? go(dp, nb, std::true_type{}) : go(dp, nb, std::false_type{});
   };
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads)
       if (page >= 0 && page < g.num_pages) {
         k = page * g.k_page + slot * g.k_slot;
         v = page * g.v_page + slot * g.v_slot;
-        e = page * g.exp_page + slot;
+        e = page * a.ex.page + slot;
       } else {
         s_bad = kPageErrEntry;
       }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads)
                            hk * (x ? g.v_head : g.k_head) + c;
         const int64_t extent = x ? g.n_v : g.n_k;
         const uint8_t* p = static_cast<const uint8_t*>(x ? a.v_pages : a.k_pages) + at;
-        if (g.wide) {
+        if (a.ex.wide) {
           if (in_bounds(at, 16, extent, a.err)) in[y][x] = __ldcs(reinterpret_cast<const uint4*>(p));
         } else {  // rows start on 8 bytes, and the last 16 codes may be 8
           if (in_bounds(at, 8, extent, a.err)) *reinterpret_cast<uint2*>(&in[y][x].x) = __ldcs(reinterpret_cast<const uint2*>(p));
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads)
             *reinterpret_cast<uint2*>(&in[y][x].z) = __ldcs(reinterpret_cast<const uint2*>(p + 8));
         }
         const int64_t ex = s_e[r >> 4] + (r & 15) + static_cast<int64_t>(hk) * g.page_size;
-        if (in_bounds(ex, 1, g.n_exp, a.err)) e[y][x] = (x ? g.v_exp : g.k_exp)[ex];
+        if (in_bounds(ex, 1, a.ex.n, a.err)) e[y][x] = (x ? a.ex.v : a.ex.k)[ex];
       }
     }
 #pragma unroll

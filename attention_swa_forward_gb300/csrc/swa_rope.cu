@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED && !Q8 ? kAppendResident :
         if (page >= 0 && page < a.pg.num_pages) {
           kd = page * a.pg.k_page + slot * a.pg.k_slot;
           vd = page * a.pg.v_page + slot * a.pg.v_slot;
-          if (Q8) ex = page * a.pg.exp_page + slot;
+          if (Q8) ex = page * a.ex.page + slot;
         } else {
           bad = kPageErrEntry;
         }
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED && !Q8 ? kAppendResident :
         if (w.ia < a.D && rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ia, fa, scale);
         if (w.ib < a.D && rope_in_bounds(w.dst + w.ib, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ib, fb, scale);
         const int64_t x = s.ex[w.tk] + static_cast<int64_t>(w.h) * a.pg.page_size;
-        if (u == 0 && rope_in_bounds(x, 1, a.pg.n_exp, a.err))
-          (w.sg == 1 ? a.pg.k_exp : a.pg.v_exp)[x] = static_cast<int8_t>(e);
+        if (u == 0 && rope_in_bounds(x, 1, a.ex.n, a.err))
+          (w.sg == 1 ? a.ex.k : a.ex.v)[x] = static_cast<int8_t>(e);
         continue;
       }
       // the chunk's pairs: VEC of them, from pair u * VEC on in both forms
@@ -375,7 +375,7 @@ cudaError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, cudaStre
 template <int CAP>
 cudaError_t launch_append(const RopeArgs& a, const PagedTable<CAP>& tab, int dtype, bool interleaved, int n_ctas,
                           cudaStream_t stream) {
-  return a.pg.k_exp ? launch_any<true, true, CAP>(a, tab, dtype, interleaved, n_ctas, stream)
+  return a.ex.k ? launch_any<true, true, CAP>(a, tab, dtype, interleaved, n_ctas, stream)
                     : launch_any<true, false, CAP>(a, tab, dtype, interleaved, n_ctas, stream);
 }
 template cudaError_t launch_append<kPagedSmallTable>(const RopeArgs&, const PagedTable<kPagedSmallTable>&, int, bool,

@@ -32,7 +32,8 @@ struct Item {
 // Work item k of a launch's table.  `nh` is the number of heads per batch
 // the table enumerates: query heads for the query-major kernels, key/value
 // heads for the key-major one.
-template <int CAP>
+// (SINKS false, here and below: as without sinks, which Geometry::sinks = 0 says too.)
+template <bool SINKS = true, int CAP>
 SWA_HD Item resolve_item(const SeqTable<CAP>& tab, const Geometry& g, int k, int nh) {
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
@@ -42,16 +43,16 @@ SWA_HD Item resolve_item(const SeqTable<CAP>& tab, const Geometry& g, int k, int
   const SeqDesc& d = tab.d[lo];
   int local = k - d.item_begin;
   Item it;
-  it.pieces = d.pieces;
+  it.pieces = SINKS ? d.pieces : 0;
   it.piece = 0;
-  if (d.pieces > 1) {
+  if (SINKS && d.pieces > 1) {
     const int whole = local / d.pieces;
     it.piece = local - whole * d.pieces;
     local = whole;
   }
   const int h = local / d.tiles;  // head by head: the CTAs in flight share a head's tiles in L2
   const int rank = local - h * d.tiles;
-  it.tile = d.tile0 + (d.descending ? d.tiles - 1 - rank : rank);
+  it.tile = (SINKS ? d.tile0 : 0) + (d.descending ? d.tiles - 1 - rank : rank);
   if (d.b < 0) {
     it.b = h / nh;
     it.n = h - it.b * nh;
@@ -79,6 +80,7 @@ SWA_HD int sink_tiles(const Geometry& g, const SeqInfo& s, int q_last) {
 // Key tiles [*t0, *t0 + *n) that query tile `tile` of sequence s touches; the
 // sink tiles are among them where they reach the window's run, else before it
 // (sink_tiles_before).
+template <bool SINKS = true>
 SWA_HD void key_tiles_of_query_tile(const Geometry& g, const SeqInfo& s, int tile, int* t0, int* n) {
   const int q0 = tile * kTileM;
   const int q_last = q0 + kTileM - 1 < s.q_len - 1 ? q0 + kTileM - 1 : s.q_len - 1;
@@ -93,7 +95,7 @@ SWA_HD void key_tiles_of_query_tile(const Geometry& g, const SeqInfo& s, int til
     *t0 = lo / kTileN;
     *n = hi / kTileN - *t0 + 1;
   }
-  if (g.sinks > 0) {
+  if (SINKS && g.sinks > 0) {
     const int sinks = sink_tiles(g, s, q_last);
     if (sinks >= *t0) {
       *n = *t0 + *n > sinks ? *t0 + *n : sinks;
@@ -103,8 +105,9 @@ SWA_HD void key_tiles_of_query_tile(const Geometry& g, const SeqInfo& s, int til
 }
 
 // Sink tiles [0, .) that query tile `tile` touches before its run, which begins at t0.
+template <bool SINKS = true>
 SWA_HD int sink_tiles_before(const Geometry& g, const SeqInfo& s, int tile, int t0) {
-  if (g.sinks <= 0) return 0;
+  if (!SINKS || g.sinks <= 0) return 0;
   const int q0 = tile * kTileM;
   const int sinks = sink_tiles(g, s, q0 + kTileM - 1 < s.q_len - 1 ? q0 + kTileM - 1 : s.q_len - 1);
   return sinks < t0 ? sinks : 0;
@@ -114,10 +117,11 @@ SWA_HD int sink_tiles_before(const Geometry& g, const SeqInfo& s, int tile, int 
 // visit between them (the forward at D <= 64 takes the two in one CTA; the
 // second may not exist).  A tile with no visible key adds nothing; the union
 // of two runs is taken from the first start to the last end.
+template <bool SINKS = true>
 SWA_HD void key_tiles_of_query_pair(const Geometry& g, const SeqInfo& s, int p, int* u0, int* n) {
   int ta = 0, na = 0, tb = 0, nb = 0;
-  if (2 * p * kTileM < s.q_len) key_tiles_of_query_tile(g, s, 2 * p, &ta, &na);
-  if ((2 * p + 1) * kTileM < s.q_len) key_tiles_of_query_tile(g, s, 2 * p + 1, &tb, &nb);
+  if (2 * p * kTileM < s.q_len) key_tiles_of_query_tile<SINKS>(g, s, 2 * p, &ta, &na);
+  if ((2 * p + 1) * kTileM < s.q_len) key_tiles_of_query_tile<SINKS>(g, s, 2 * p + 1, &tb, &nb);
   *u0 = 0;
   *n = 0;
   if (na > 0 && nb > 0) {
@@ -134,13 +138,14 @@ SWA_HD void key_tiles_of_query_pair(const Geometry& g, const SeqInfo& s, int p, 
 
 // Query tiles [*t0, *t0 + *n) that see key tile `tile` of sequence s:
 // i - pre <= j <= i + next  <=>  j - next <= i <= j + pre; a sink is seen by every i >= j - next.
+template <bool SINKS = true>
 SWA_HD void query_tiles_of_key_tile(const Geometry& g, const SeqInfo& s, int tile, int* t0, int* n) {
   const int j0 = tile * kTileN;
   const int j_last = j0 + kTileN - 1 < s.kv_len - 1 ? j0 + kTileN - 1 : s.kv_len - 1;
   int lo = 0, hi = s.q_len - 1;
   if (g.sparse_mode == 4) {
     lo = j0 - g.next > lo ? j0 - g.next : lo;
-    if (j0 >= g.sinks) hi = j_last + g.pre < hi ? j_last + g.pre : hi;
+    if (!SINKS || j0 >= g.sinks) hi = j_last + g.pre < hi ? j_last + g.pre : hi;
   }
   *t0 = 0;
   *n = 0;
