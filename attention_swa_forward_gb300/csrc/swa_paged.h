@@ -2,6 +2,8 @@
 // and paged-cache operators (include/swa.h, "Rotary positions, a paged
 // key/value cache, and attention over it").
 #pragma once
+#include <type_traits>
+
 #include "swa_internal.h"
 
 #if defined(__CUDACC__)
@@ -124,7 +126,7 @@ struct PageDims {
 
 // Row tile: `tok` tokens x `gs` query heads that share one key/value head,
 // row r = token r / gs, head r mod gs of head group vh (heads vh*gs ...).
-struct PagedArgs {
+struct PagedBase {
   PagedGeom g;
   int32_t gs, tok, groups;  // groups = N / gs head groups
   uint32_t gs_magic;        // ceil(2^16 / gs)
@@ -158,7 +160,9 @@ struct PagedArgs {
   int32_t overlap;    // few-row kernel: that next grid
   int32_t* page_err;  // per unit of the call: [whole], then [items - whole][splits]
   int64_t n_q, n_out, n_stats;  // extents, for the bounds-checked build
-  // (what only some calls have comes last: the others' kernels load fewer lines of their arguments)
+};
+// What only some calls have: the kernels of the others are launched without it.
+struct PagedArgs : PagedBase {
   int32_t sinks;      // BAND: keys below this one stay visible behind the window
   int32_t most_rows;  // rows that some tile has
   // a chunk that is a tree of drafted tokens: bit c of row t: token t sees token c of its chunk
@@ -212,15 +216,27 @@ struct PagedKeys {
 // depth, at least that of depth 0, and it may see the whole chunk.  X: there may
 // be sinks or a tree.
 template <bool X>
-SWA_PAGED_HD PagedKeys paged_keys(const PagedArgs& a, int kv_len, int q_len, int tok0, int n_tok) {
+using ArgsOf = std::conditional_t<X, PagedArgs, PagedBase>;
+template <bool X>
+SWA_PAGED_HD const uint32_t* tree_of(const ArgsOf<X>& a) {
+  if constexpr (X) return a.tree;
+  else return nullptr;
+}
+template <bool X>
+SWA_PAGED_HD int sinks_of(const ArgsOf<X>& a) {
+  if constexpr (X) return a.sinks;
+  else return 0;
+}
+template <bool X>
+SWA_PAGED_HD PagedKeys paged_keys(const ArgsOf<X>& a, int kv_len, int q_len, int tok0, int n_tok) {
   PagedKeys k{0, kv_len - 1, 0};
   if (a.sparse_mode == 4) {
-    const bool tree = X && a.tree != nullptr;
+    const bool tree = tree_of<X>(a) != nullptr;
     const int p0 = kv_len - q_len + (tree ? 0 : tok0), p1 = p0 + n_tok - 1;
     k.lo = p0 - a.pre > 0 ? p0 - a.pre : 0;
     if (!tree) k.hi = p1 + a.next < k.hi ? p1 + a.next : k.hi;
-    if (X && a.sinks > 0) {
-      const int n = a.sinks < k.hi + 1 ? a.sinks : k.hi + 1;
+    if (const int sinks = sinks_of<X>(a); sinks > 0) {
+      const int n = sinks < k.hi + 1 ? sinks : k.hi + 1;
       if (k.lo > k.hi) {
         k.lo = 0;
         k.hi = n - 1;

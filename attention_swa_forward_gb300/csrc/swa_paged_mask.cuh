@@ -40,11 +40,14 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 }
 
 // Position of token i of the chunk.  A depth outside the chunk counts as the nearest inside.
-__device__ __forceinline__ int token_position(const PagedArgs& a, const PagedItem& w, int kv_len, int i) {
+template <bool X = true>
+__device__ __forceinline__ int token_position(const ArgsOf<X>& a, const PagedItem& w, int kv_len, int i) {
   int at = i;
-  if (a.tree && a.depth) {
-    const int64_t t = w.q_start + i;
-    at = in_bounds(t, 1, a.n_depth, a.err) ? min(max(a.depth[t], 0), w.q_len - 1) : 0;
+  if constexpr (X) {
+    if (a.tree && a.depth) {
+      const int64_t t = w.q_start + i;
+      at = in_bounds(t, 1, a.n_depth, a.err) ? min(max(a.depth[t], 0), w.q_len - 1) : 0;
+    }
   }
   return kv_len - w.q_len + at;
 }

@@ -79,7 +79,8 @@ struct RowsSmem {
 // workspace and swa_paged_join_kernel joins them.
 template <PagedKind KIND, int DP, bool F16, bool CL, int CAP>
 __global__ void __launch_bounds__(kRowsThreads, 2)
-    swa_paged_rows_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab) {
+    swa_paged_rows_kernel(const __grid_constant__ ArgsOf<KIND != PagedKind::kPlain> a,
+                          const __grid_constant__ PagedTable<CAP> tab) {
   constexpr bool X = KIND != PagedKind::kPlain;
   using Smem = RowsSmem<DP>;
   constexpr int kRowsStages = Smem::kRowsStages;
@@ -157,11 +158,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     row_lo[x] = 0;
     row_hi[x] = kv_len - 1;
     if (a.sparse_mode == 4) {
-      const int p = X ? token_position(a, w, kv_len, tok0 + row_tok[x]) : kv_len - w.q_len + tok0 + row_tok[x];
+      const int p = token_position<X>(a, w, kv_len, tok0 + row_tok[x]);
       row_lo[x] = max(0, p - a.pre);
       row_hi[x] = min(kv_len - 1, p + a.next);
     }
-    if (X && a.tree) row_hi[x] = kv_len - w.q_len - 1;  // the chunk's own keys go by the tree's bits
+    if (tree_of<X>(a)) row_hi[x] = kv_len - w.q_len - 1;  // the chunk's own keys go by the tree's bits
   }
 
   // keys every row of the tile sees: from the last token's first to the first token's last
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     all_lo = max(0, p0 + n_tok - 1 - a.pre);
     all_hi = min(kv_len - 1, p0 + a.next);
   }
-  if (X && a.tree) {  // the deepest token may be q_len - 1 deep
+  if (tree_of<X>(a)) {  // the deepest token may be q_len - 1 deep
     if (a.sparse_mode == 4) all_lo = max(0, kv_len - 1 - a.pre);
     all_hi = kv_len - w.q_len - 1;
   }
@@ -303,13 +304,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     issue(it + kRowsStages, true);  // V's stage is free
     // mask (groups at the ends of the visible run only), running maximum
     float mx[2] = {-INFINITY, -INFINITY};
-    if (!fold || (j0 < all_lo && !(X && j0 + 15 < a.sinks)) || j0 + 15 > all_hi) {
+    if (!fold || (j0 < all_lo && !(X && j0 + 15 < sinks_of<X>(a))) || j0 + 15 > all_hi) {
       uint32_t drafted[2] = {0u, 0u};  // bit t: key j0 + t is a token of the chunk that the row sees
-      if (X && a.tree) {
+      if constexpr (X) {
         const int c0 = j0 - (kv_len - w.q_len);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (c0 > -16) drafted[x] = tree_bits(a, w, tok0 + row_tok[x], c0);
+          if (a.tree && c0 > -16) drafted[x] = tree_bits(a, w, tok0 + row_tok[x], c0);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         for (int y = 0; y < 4; ++y) {
           const int x = y >> 1;
           const int j = j0 + t * 8 + (lane & 3) * 2 + (y & 1);
-          bool vis = (j >= row_lo[x] || (X && j < a.sinks)) && j <= row_hi[x];
+          bool vis = (j >= row_lo[x] || (X && j < sinks_of<X>(a))) && j <= row_hi[x];
           if (X) vis = vis || ((drafted[x] >> (j - j0)) & 1u) != 0;
           sc[t][y] = vis ? (fold ? sc[t][y] : sc[t][y] * c) : -INFINITY;
         }
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
 }
 
 template <PagedKind KIND, int DP, bool F16, bool CL, int CAP>
-cudaError_t launch_rows_t(const PagedArgs& a, const PagedTable<CAP>& tab, cudaStream_t stream) {
+cudaError_t launch_rows_t(const ArgsOf<KIND != PagedKind::kPlain>& a, const PagedTable<CAP>& tab, cudaStream_t stream) {
   const size_t smem = sizeof(RowsSmem<DP>);
   auto kernel = swa_paged_rows_kernel<KIND, DP, F16, CL, CAP>;
   static std::atomic<uint64_t> smem_set{0};

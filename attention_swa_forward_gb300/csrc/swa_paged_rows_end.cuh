@@ -71,7 +71,7 @@ struct RowsEnd {
 // Page status, and the item's rows from the warps' O (in `so`), maxima and sums
 // (ml): to the results, to the workspace, or through the cluster.
 template <int DP, bool F16, bool CL>
-__device__ __forceinline__ void rows_end(const PagedArgs& a, const PagedItem& w, int split, int64_t item, int tok0,
+__device__ __forceinline__ void rows_end(const PagedBase& a, const PagedItem& w, int split, int64_t item, int tok0,
                                          int n_rows, bool direct, int bad, float* so, float (*ml)[kRowsTile][2]) {
   using Layout = RowsEnd<DP>;
   const PagedGeom& g = a.g;

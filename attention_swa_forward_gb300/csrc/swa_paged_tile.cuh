@@ -91,7 +91,7 @@ struct PageWalk {
     slot = j - entry * page_size;
   }
   // From tile number `first` of the unit list on.
-  __device__ __forceinline__ void start(const PagedArgs& a, int b, const PagedUnits& tiles, int first, int box,
+  __device__ __forceinline__ void start(const PagedBase& a, int b, const PagedUnits& tiles, int first, int box,
                                         const PagedKeys& keys) {
     lo = keys.lo;
     hi = keys.hi;
@@ -168,20 +168,20 @@ struct UnitWalk {
   PagedItem w_next;
 
   // The first `whole` units are whole items, the others splits of the rest.
-  static __device__ __forceinline__ int item_of(const PagedArgs& a, int u) {
+  static __device__ __forceinline__ int item_of(const PagedBase& a, int u) {
     return u < a.whole ? u : (a.splits > 1 ? a.whole + (u - a.whole) / a.splits : u);
   }
-  __device__ __forceinline__ void fetch(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units) {
+  __device__ __forceinline__ void fetch(const PagedBase& a, const PagedTable<CAP>& tab, int n_units) {
     u_next = unit_index(k, n_units);
     if (u_next < 0) return;
     w_next = resolve_paged(tab, a.groups, item_of(a, u_next));
     kv_next = in_bounds(w_next.b, 1, a.g.n_lens, a.err) ? a.g.kv_lens[w_next.b] : 0;
   }
-  __device__ __forceinline__ void start(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units) {
+  __device__ __forceinline__ void start(const PagedBase& a, const PagedTable<CAP>& tab, int n_units) {
     k = 0;
     fetch(a, tab, n_units);
   }
-  __device__ __forceinline__ bool next(const PagedArgs& a, const PagedTable<CAP>& tab, int n_units, Unit& x) {
+  __device__ __forceinline__ bool next(const ArgsOf<X>& a, const PagedTable<CAP>& tab, int n_units, Unit& x) {
     if (u_next < 0) return false;
     const bool whole = u_next < a.whole;
     x.w = w_next;
@@ -228,7 +228,7 @@ struct Ring {
 
 template <PagedKind KIND, int D, bool F16, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-    swa_paged_tile_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab,
+    swa_paged_tile_kernel(const __grid_constant__ ArgsOf<KIND != PagedKind::kPlain> a, const __grid_constant__ PagedTable<CAP> tab,
                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                           const __grid_constant__ CUtensorMap mq) {
   extern __shared__ uint8_t smem_raw[];
@@ -496,14 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int all_lo = 0, all_hi = x.kv_len - 1;
       if (a.sparse_mode == 4) {
         const int p0 = x.kv_len - x.w.q_len + x.tok0;
-        const int p = X ? token_position(a, x.w, x.kv_len, x.tok0 + min(i, x.n_tok - 1)) : p0 + i;
+        const int p = X ? token_position<X>(a, x.w, x.kv_len, x.tok0 + min(i, x.n_tok - 1)) : p0 + i;
         wlo = max(0, p - a.pre);
         whi = min(x.kv_len - 1, p + a.next);
         all_lo = max(0, p0 + x.n_tok - 1 - a.pre);
         all_hi = min(x.kv_len - 1, p0 + a.next);
       }
       const int prefix = x.kv_len - x.w.q_len;  // a tree: keys before the chunk, whose own go by bits
-      if (X && a.tree) {
+      if (tree_of<X>(a)) {
         whi = all_hi = prefix - 1;
         if (a.sparse_mode == 4) all_lo = max(0, x.kv_len - 1 - a.pre);  // the deepest token may be q_len - 1 deep
       }
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto score = [&](int y) -> float { return __uint_as_float(xr[y]); };
 
         const int j0 = x.key0(it);
-        const bool fast = fold && (j0 >= all_lo || (X && j0 + kPagedTileStep - 1 < a.sinks)) &&
+        const bool fast = fold && (j0 >= all_lo || (X && j0 + kPagedTileStep - 1 < sinks_of<X>(a))) &&
                           j0 + kPagedTileStep - 1 <= all_hi;
         float mx;
         {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t from = a0 <= 0 ? ~0u : (a0 > 31 ? 0u : ~0u << a0);
               const uint32_t to = b0 >= 31 ? ~0u : (b0 < 0 ? 0u : (2u << b0) - 1u);
               seen[q] = from & to;
-              if (X) {
+              if constexpr (X) {
                 // and the sinks, up to the row's last key
                 const int n = min(a.sinks, whi + 1) - j0 - 32 * q;
                 seen[q] |= n <= 0 ? 0u : (n > 31 ? ~0u : (1u << n) - 1u);
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <PagedKind KIND, int D, bool F16, int CAP>
-cudaError_t launch_tile_t(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk, const CUtensorMap& mv,
+cudaError_t launch_tile_t(const ArgsOf<KIND != PagedKind::kPlain>& a, const PagedTable<CAP>& tab, const CUtensorMap& mk, const CUtensorMap& mv,
                           const CUtensorMap& mq, cudaStream_t stream) {
   const size_t smem = sizeof(TileSmem<D>) + 1024;
   static std::atomic<uint64_t> smem_set{0};

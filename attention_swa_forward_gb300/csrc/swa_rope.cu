@@ -137,6 +137,50 @@ __device__ __forceinline__ int row_exponent(uint32_t top, int least) {
   const int e = static_cast<int>(top >> 23) - 126 - 9 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return min(max(e, least), kExpMost);
 }
+// The same of a chunk that is not rotated, two elements at a time.
+template <typename T, int VEC>
+__device__ __forceinline__ uint32_t top_pairs(const T (&x)[VEC]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+  uint32_t top = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < VEC / 2; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+  return top;
+}
+// Bits in fp32 of the larger of a pair of magnitudes.
+template <typename T>
+__device__ __forceinline__ uint32_t top_of_pair(uint32_t w) {
+  const uint32_t t = max(w & 0xFFFFu, w >> 16);
+  if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half(t))) & 0x7FFFFFFFu;
+  else return t << 16;
+}
+// VEC codes of x times 2^-e, from their own type.  (fp16: the product is exact
+// but where it is below 2^-14, and there a code is 0 on either side.)
+template <typename T, int VEC>
+__device__ __forceinline__ void store_codes_of(uint8_t* dst, const T (&x)[VEC], int e) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+  uint32_t out[VEC / 4];
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    uint16_t lo, hi;
+    if constexpr (std::is_same<T, __half>::value) {
+      const uint32_t f = static_cast<uint32_t>(e == kExpNan ? 15 : 15 - e) * 0x04000400u;
+      uint32_t a, b;
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(w[2 * i]), "r"(f));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2 * i + 1]), "r"(f));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
+    } else {
+      const float f = e == kExpNan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(lo) : "f"(__uint_as_float(w[2 * i] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[2 * i] << 16) * f));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(hi) : "f"(__uint_as_float(w[2 * i + 1] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[2 * i + 1] << 16) * f));
+    }
+    out[i] = lo | static_cast<uint32_t>(hi) << 16;
+  }
+  if constexpr (VEC == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = out[0];
+}
 // VEC codes of x times 2^-e, nearest even, saturated at 448.
 template <int VEC>
 __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[VEC], float scale) {
@@ -301,6 +345,13 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED && !Q8 ? kAppendResident :
       Place w;
       if (!locate(r0 + k * a.row_lanes, w)) continue;
       const T* p = static_cast<const T*>(a.src[w.sg]);
+      if constexpr (Q8) {  // one check for the row: idle lanes of it read its start
+        if (rope_in_bounds(w.src, a.D, a.n_src[w.sg], a.err)) {
+          ra[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + (w.ia < a.D ? w.ia : 0)));
+          rb[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + (w.ib < a.D ? w.ib : 0)));
+        }
+        continue;
+      }
       if ((!Q8 || w.ia < a.D) && rope_in_bounds(w.src + w.ia, VEC, a.n_src[w.sg], a.err))
         ra[k] = __ldcs(reinterpret_cast<const R*>(p + w.src + w.ia));
       if (w.ib < a.D && rope_in_bounds(w.src + w.ib, VEC, a.n_src[w.sg], a.err))
@@ -315,19 +366,30 @@ __global__ void __launch_bounds__(kRopeThreads, PAGED && !Q8 ? kAppendResident :
       *reinterpret_cast<R*>(xb) = rb[k];
       if (Q8 && w.sg != 0) {
         // (the threads of a row, neighbours in a warp, are all here or none)
+        const bool turns = w.sg == 1 && a.R > 0;
         float fa[VEC], fb[VEC];
-        turn_float<T, VEC, IL>(xa, xb, fa, fb, &s.cs[w.tk][u * VEC], &s.sn[w.tk][u * VEC],
-                               w.sg == 1 && u * 2 * VEC < a.R);
         uint32_t top = 0;
-        if (w.ia < a.D) top = top_bits<VEC>(fa, top);
-        if (w.ib < a.D) top = top_bits<VEC>(fb, top);
+        if (turns) {
+          turn_float<T, VEC, IL>(xa, xb, fa, fb, &s.cs[w.tk][u * VEC], &s.sn[w.tk][u * VEC], u * 2 * VEC < a.R);
+          if (w.ia < a.D) top = top_bits<VEC>(fa, top);
+          if (w.ib < a.D) top = top_bits<VEC>(fb, top);
+        } else {
+          // (an idle lane holds the row's start, which changes no maximum)
+          top = top_of_pair<T>(__vmaxu2(top_pairs<T, VEC>(xa), top_pairs<T, VEC>(xb)));
+        }
         const uint32_t row_mask = ((1u << a.units) - 1u) << ((tid & 31) & ~(a.units - 1));
         for (int d = a.units >> 1; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(row_mask, top, d));
         const int e = row_exponent(top, std::is_same<T, __half>::value ? kExpLeastF16 : kExpLeastBf16);
         const float scale = e == kExpNan ? 1.f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         uint8_t* p = static_cast<uint8_t*>(a.dst[w.sg]) + w.dst;
-        if (w.ia < a.D && rope_in_bounds(w.dst + w.ia, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ia, fa, scale);
-        if (w.ib < a.D && rope_in_bounds(w.dst + w.ib, VEC, a.n_dst[w.sg], a.err)) store_codes<VEC>(p + w.ib, fb, scale);
+        const bool put = rope_in_bounds(w.dst, a.D, a.n_dst[w.sg], a.err), put_a = put && w.ia < a.D, put_b = put && w.ib < a.D;
+        if (turns) {
+          if (put_a) store_codes<VEC>(p + w.ia, fa, scale);
+          if (put_b) store_codes<VEC>(p + w.ib, fb, scale);
+        } else {
+          if (put_a) store_codes_of<T, VEC>(p + w.ia, xa, e);
+          if (put_b) store_codes_of<T, VEC>(p + w.ib, xb, e);
+        }
         const int64_t x = s.ex[w.tk] + static_cast<int64_t>(w.h) * a.pg.page_size;
         if (u == 0 && rope_in_bounds(x, 1, a.ex.n, a.err))
           (w.sg == 1 ? a.ex.k : a.ex.v)[x] = static_cast<int8_t>(e);
