@@ -555,7 +555,7 @@ swa_status_t swa_forward(const swa_params_t* p, const void* q, const void* k, co
     if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
   }
   // D <= 64: TMEM holds two query tiles' S, O and P, and one CTA takes a pair
-  // of consecutive query tiles (swa_fwd_pair.cu), when the pairs still fill
+  // of consecutive query tiles (swa_fwd_pair.cuh), when the pairs still fill
   // every SM at least once; smaller problems keep one CTA per query tile
   bool pair = false;
   if (plan.g.D <= 64) {

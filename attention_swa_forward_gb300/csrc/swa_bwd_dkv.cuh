@@ -11,7 +11,7 @@
 // and dK by scale/keep.
 // lse2 = softmax_max*log2e + log2(softmax_sum) and D = rowsum(dY*O) come from
 // the preprocess kernel.  dQ is computed by the query-major pass
-// (swa_bwd_dq.cu), so nothing here accumulates through global memory.
+// (swa_bwd_dq.cuh), so nothing here accumulates through global memory.
 //
 // One CTA = one 128-row key tile of one (batch, head); it walks the query
 // tiles of the band with dK / dV accumulating in TMEM.  Warps:

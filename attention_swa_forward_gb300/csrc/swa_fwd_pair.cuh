@@ -1,7 +1,7 @@
 // swa_fwd_pair.cuh — sliding-window attention forward for D <= 64, two query
 // tiles per CTA.
 //
-// The same computation as swa_fwd.cu (FlashAttentionVarLenScore doc,
+// The same computation as swa_fwd.cuh (FlashAttentionVarLenScore doc,
 // "计算公式"; the online softmax of the PyPTO-Gym article's forward), with
 // one CTA covering two consecutive 128-row query tiles A = 2p and B = 2p + 1
 // of one (batch, head).  At D <= 64 TMEM holds a score tile, an O

@@ -21,6 +21,7 @@ constexpr int64_t kRowsMostKeys = 16384;
 // The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 202 us, 206 with
 // 4096, 220 with 1024, 250 with 16384; one of 131072: 54 us (76 splits either way).
 constexpr int64_t kRows8MostKeys = 2048;
+constexpr int64_t kMostSplits = 65535;  // a grid's second dimension
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
 constexpr int64_t kTailSteps = 12;  // key tiles that splitting a last round must save (0.76 us each)
@@ -637,7 +638,7 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       // runs (kRows8MostKeys).
       const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
       part.par = std::min(ceil_div(int64_t(kSms) * (q8 ? 4 : 1), items), steps);
-      part.cap = (q8 ? kRows8MostKeys : kRowsMostKeys) / step + 2;
+      part.cap = std::max((q8 ? kRows8MostKeys : kRowsMostKeys) / step + 2, ceil_div(steps, kMostSplits));
       part.least = 1;
       // Up to 8 splits are one cluster, which joins them without a second
       // launch: a power of two of CTAs, all resident at once.  One token of

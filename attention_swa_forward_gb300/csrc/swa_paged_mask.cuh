@@ -8,7 +8,7 @@ namespace swa {
 
 // Accesses to shared memory by 32-bit addresses: after the alignment of its base
 // the compiler no longer knows where a pointer points, and generic accesses wait
-// for more (a chunk over the 8-bit cache took 598 us with them, FILL without).
+// for more.
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -19,24 +19,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ int lds_s8(uint32_t addr) {
   int v;
   asm volatile("ld.shared.s8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Position of token i of the chunk.  A depth outside the chunk counts as the nearest inside.
@@ -72,14 +58,9 @@ __device__ __forceinline__ uint32_t tree_bits(const PagedArgs& a, const PagedIte
 //
 // The conversion instruction gives a pair of codes as fp16, exactly.  What reads a
 // row back multiplies by 2^e (fp16), or by 2^(e + 112) after moving the fp16 bits
-// to the places of a bf16, whose exponents' bias is 112 higher.  Attention over
-// an 8-bit cache multiplies in fp16 whatever the type of q: codes are exact there,
-// q is brought into its range row by row, and the exponents go into the scores
-// and the weights.
-//
-// (Codes as bf16 in the attention kernels: the integer instructions that move the
-// bits, 3 to 4 a pair at half the rate of others, set the time: 64 single tokens of
-// 100 to 16384 keys 448 us, a chunk of 1024 tokens behind 15360 633.)
+// to the places of a bf16, whose exponents' bias is 112 higher.  That takes 3 to 4
+// integer instructions a pair, at half the rate of others, and so the kernel of
+// few query rows multiplies in fp16 whatever the type of q (swa_paged_rows_e4m3.cu).
 
 // 2^(112 + e) as bf16 bits, or 2^e as fp16 bits; NaN for an exponent above the most.
 template <bool F16>

@@ -3,10 +3,11 @@
 //
 // The same work as swa_paged_rows.cuh on half the bytes, so what a warp does per
 // 16 keys sets the time unless it is kept short:
-//  * Each warp has a ring of three groups of 16 keys (six of heads up to 64).  One lane brings a group in:
-//    K and V by a TMA box each (swizzled), the exponents by two copies of 16
-//    bytes, all on one barrier.  Rows that start on 8 bytes only (head dims that
-//    are no multiples of 16) are copied by all lanes, 8 bytes at a time.
+//  * Each warp has a ring of three groups of 16 keys (six of heads up to 64).  One
+//    lane brings a group in: K and V by a TMA box each (swizzled), the exponents by
+//    two copies of 16 bytes, all on one barrier.  Rows that start on 8 bytes only
+//    (head dims that are no multiples of 16) are copied by all lanes, 8 bytes at a
+//    time.
 //  * The products are transposed, S^T = K Q^T and O^T = V^T P^T, with keys and
 //    columns as the 16 rows of an instruction and 8 query rows as its columns: up
 //    to 8 rows (a token of 8 heads) take half the instructions, exponentials and
@@ -23,9 +24,12 @@
 //    its weight, rounded to fp16 as p 2^(e - E + 7), E the largest exponent so far
 //    (the results move with it): 11 bits where that is at least 2^-14 (p <= 2^8),
 //    2^-25 below.  A lane makes the factor of one of the 32 exponents.
-// (As bf16, by moving bits with integer instructions and multiplying each pair by
-// its row's power of two, and with copies by all lanes: 765 instructions a group
-// instead of FILL; 64 tokens of 100 to 16384 keys 448 us instead of FILL.)
+// Bound by HBM where the keys are many: 64 tokens of 100 to 16384 keys, 32 / 8
+// heads of 128, 199 us (1.13 GB; a copy would take 166), of 8192 keys each 179.
+// (Measured on the first of those on the way here: codes as bf16, by moving bits
+// with integer instructions and multiplying each pair by its row's power of two,
+// 765 instructions a group, 448 us; as fp16 394; by TMA instead of copies by all
+// lanes 317; transposed, and in shorter runs of keys, 199.)
 #include "swa_paged_rows_end.cuh"
 
 namespace swa {

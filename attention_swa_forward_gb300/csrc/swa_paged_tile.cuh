@@ -5,10 +5,10 @@
 // Per row (include/swa.h): O = sum_j softmax_j(scale q.k_j) v_j over visible
 // keys, softmax_max, softmax_sum; online softmax in fp32 (log2 units).  P is
 // rounded to the element type, which the second product's operands have (as in
-// swa_fwd.cu; swa_paged_rows.cu says what that does to the result).
+// swa_fwd.cuh; swa_paged_rows.cuh says what that does to the result).
 //
 // Bound by the tensor pipe and its hand-offs to the softmax, like the dense
-// forward, whose roles it keeps (swa_fwd.cu): one thread per row in warps 0-3,
+// forward, whose roles it keeps (swa_fwd.cuh): one thread per row in warps 0-3,
 // S = Q K^T into one of two TMEM tiles by the thread of warp 5, O += P V by the
 // thread of warp 6 with P taken from TMEM.  What is different:
 //  * Packing the G heads of a key/value head into the rows (128 / G tokens per
@@ -42,7 +42,7 @@
 // list.  A tree: the tiles that hold the chunk's own keys take 32 bits per row
 // and 32 columns.  The fast path without per-column tests is as it was.
 // An 8-bit cache is written out as 16-bit pages first (swa_paged_unpack.cu).
-// TMEM columns as in swa_fwd.cu: S0 [0,128), S1 [128,256), O [256,256+D),
+// TMEM columns as in swa_fwd.cuh: S0 [0,128), S1 [128,256), O [256,256+D),
 // P0 [384,448), P1 [448,512).
 #pragma once
 #include "swa_paged.h"
@@ -71,7 +71,7 @@ static_assert(sizeof(TileSmem<128>) + 1024 <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256, kColP = 384;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // as in swa_fwd.cu
+constexpr float kRescaleThreshold = 8.0f;  // as in swa_fwd.cuh
 
 // Where one lane of a gathering warp finds its part of successive key tiles:
 // box `box` (box_rows slots) of the tile, in atom column `atom`.

@@ -5,13 +5,14 @@
 // Each 128-key tile of the chunk's list (the sinks' tiles, then the window's) is
 // a page of 128 slots, [N_kv][128][D]; values are exact, rows that no query of
 // the chunk sees and those of a page that is not to be followed are zeros.  A CTA
-// takes a page and a head.  It reads a byte per value and writes two, which the
-// attention reads once per row tile from L2 or HBM: FILL.
+// takes a page and a head.  Bound by HBM and L2: it reads a byte per value and
+// writes two, which the attention then reads once per row tile.  A chunk of 1024
+// tokens behind 15360 keys, 32 / 8 heads of 128: 226 us in all, 205 over a 16-bit
+// cache.
 //
-// (Converting in the attention kernel, by four more warps, was measured: a chunk
-// of 1024 tokens behind 15360, 32 / 8 heads of 128, took 536 us at best, 209 over
-// a 16-bit cache.  A tile's 128 x 256 values take 3000 instructions, which share
-// the schedulers and the instruction cache with the softmax, and every row tile
+// (Converting in the attention kernel, by four more warps, took that chunk 536 us
+// at best.  A tile's 128 x 256 values take 3000 instructions, which share the
+// schedulers and the instruction cache with the softmax, and every row tile
 // converts them again.)
 #include "swa_paged.h"
 #include "swa_device.cuh"

@@ -41,8 +41,8 @@ METRIC = "SWA fwd+bwd TFLOPS (unmasked FLOPs, bf16) and % of GB300 bf16 dense pe
 UNIT = "TFLOP/s"
 FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0}
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "roofline_traffic.json")
-KERNEL_SOURCES = ["attention_swa_forward_gb300/csrc/swa_fwd.cu", "attention_swa_forward_gb300/csrc/swa_bwd_dkv.cu",
-                  "attention_swa_forward_gb300/csrc/swa_bwd_dq.cu",
+KERNEL_SOURCES = ["attention_swa_forward_gb300/csrc/swa_fwd.cuh", "attention_swa_forward_gb300/csrc/swa_bwd_dkv.cuh",
+                  "attention_swa_forward_gb300/csrc/swa_bwd_dq.cuh",
                   "attention_swa_forward_gb300/csrc/swa_device.cuh", "attention_swa_forward_gb300/csrc/sm103.cuh"]
 
 

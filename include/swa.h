@@ -382,7 +382,7 @@ typedef struct {
                                   default): max_pages * page_size.  How the keys are split over the GPU
                                   follows from it, whatever the lengths are: without a window, up to 16
                                   query rows of a sequence and key/value head take a CTA, and up to 8 KB
-                                  of workspace, per 16384 keys of this bound */
+                                  of workspace, per 16384 keys of this bound (2048 with an 8-bit cache) */
   double scale;                /* score scale, default 1.0 */
   int64_t pre_tokens;          /* BAND, around each token's position; defaults 2147483647 */
   int64_t next_tokens;
@@ -413,7 +413,12 @@ typedef enum { SWA_CACHE_SAME = 0, SWA_CACHE_E4M3 = 1 } swa_cache_t;
  * Readers take an exponent above 7 for a row of NaN, one below the least for
  * the least; what the NaN codes (0x7F, 0xFF) stand for under another exponent
  * is not defined (NaN or 480 * 2^e).
- * A slot that no query of a call sees is ignored, its exponent included. */
+ * A slot that no query of a call sees is ignored, its exponent included.
+ * Attention of up to 16 query rows per sequence and key/value head rounds the
+ * weight of a value to fp16, relative to the largest exponent E among the
+ * sequence's visible values: to 11 bits down to an exponent of E - 21, and to
+ * 2^(E - 32) below; q (bf16) loses what is below 2^-39 of its row's largest.  With
+ * more rows the keys and values are exact and the weights as without the cache. */
 
 SWA_API void swa_paged_params_default(swa_paged_params_t *p);
 

@@ -1,13 +1,13 @@
 """64-bit reference of paged attention with sinks, trees of drafted tokens and an
 8-bit cache, and the problems their tests draw.
 
-Tolerances are those of tests/paged_ref.py.  Attention over an 8-bit cache rounds
-the values besides to multiples of 2^-25 2^E, E the largest exponent of a tile,
-2^-33 of the tile's largest value at most: that of the keys, times the row's sum
-of |q|, adds to the scores, that of the values to the result; a row of q loses
-2^-39 of its largest.  Its weights are rounded to fp16 as p 2^(e - E + 7), to
-2^-25 absolutely where they are small: 2^-32 2^E and so 2^-31 of the largest
-value in the result, for each key."""
+Tolerances are those of tests/paged_ref.py.  Over an 8-bit cache a row of q may lose
+2^-39 of its largest, and weights are rounded to fp16 as p 2^(e - E + 7) (E the
+largest exponent so far, p at most 1 here), to 2^-25 absolutely where they are
+small: 2^-32 2^E in the weight of a code up to 448, and 2^E is at most 2^-7 of the
+largest value with the codes from 224 on that an exponent above the least has, so
+2^-31 of the largest value in the result for each key (the least exponent: codes of
+less, and weights of p 2^7)."""
 import torch
 
 from tests.paged_ref import DT, U
@@ -150,13 +150,12 @@ def attention_ref(geom, q, ks, vs, kv_lens, trees=None):
             out[r, h], smax[r, h], ssum[r, h] = P @ v, torch.where(live, mx, -float("inf")), l
             e = D * 2.0 ** -23 * size + 2.0 ** -22 * (size + 1)
             if geom.cache_dtype:
-                e = e + abs(geom.scale) * (x.abs().sum(1) * 2.0 ** -33 * k.abs().amax() +
-                                           x.abs().amax(1) * 2.0 ** -39 * k.abs().sum(1).amax())
+                e = e + abs(geom.scale) * x.abs().amax(1) * 2.0 ** -39 * k.abs().sum(1).amax()
             eo[r, h] = (P @ v.abs()) * (u + 2 * e + n * 2.0 ** -24)[:, None]
             if geom.dtype == "fp16":
                 eo[r, h] += n * 2.0 ** -25 * v.abs().amax()
             if geom.cache_dtype:
-                eo[r, h] += (n * 2.0 ** -31 + 2.0 ** -33) * v.abs().amax()
+                eo[r, h] += n * 2.0 ** -31 * v.abs().amax()
             eo[r, h] += u * (out[r, h].abs() + eo[r, h]) + (2.0 ** -25 if geom.dtype == "fp16" else 0.0)
             em[r, h] = e
             es[r, h] = l * (2 * e + n * 2.0 ** -24)

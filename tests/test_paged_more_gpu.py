@@ -485,6 +485,13 @@ def test_unpacked_pages_in_passes():
     check(geometry(q_lens, kv_lens, 16, N=8, N_kv=8, D=128, cache_dtype="e4m3", max_kv_len=300, **W), kv_lens, 9)
 
 
+def test_the_largest_bound_on_the_lengths():
+    """2^28 keys: runs of keys so long that a grid holds them."""
+    geom = geometry([2], [500], 65536, N=1, D=16, cache_dtype="e4m3")
+    geom.max_pages = (1 << 28) // 65536
+    check(geom, [500], 12)
+
+
 def guarded(call):
     """Status that `call` raises, or None."""
     try:

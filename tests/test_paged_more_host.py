@@ -132,3 +132,10 @@ def test_workspace_covers_sinks():
     assert size(**window, sink_tokens=100000) >= size(**window)
     assert size(sink_tokens=100000) == size()
     assert size(**window, sink_tokens=1 << 60) >= size(**window)
+
+
+def test_workspace_of_the_longest_bound():
+    """Splits of the keys stay what a grid's second dimension holds: 16 rows of 64 sums, a maximum and a sum each."""
+    g = PagedGeometry(B=1, N=1, N_kv=1, D=64, cu_seqlens_q=[1], num_pages=1, page_size=65536, max_pages=4096,
+                      cache_dtype="e4m3")
+    assert swa.swa_paged_forward_workspace_size(swa.PagedParams(g)) <= 65535 * (16 * (64 * 4 + 8) + 4) + 4096
