@@ -184,7 +184,11 @@ void set_split(RopeArgs& a, int dtype, int64_t rows) {
   a.H = a.heads[0] + a.heads[1] + a.heads[2];
   a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.H - 1) / a.H);
   a.units = static_cast<int32_t>(ceil_div(a.D, 2 * rope_vec(dtype, a.R)));
-  while (q8 && (a.units & (a.units - 1))) ++a.units;  // a row's threads then share a warp
+  if (q8) {  // a row's threads then share a warp
+    while (a.units & (a.units - 1)) ++a.units;
+    while ((1 << a.unit_shift) < a.units) ++a.unit_shift;
+    a.h_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + a.heads[1] - 1) / a.heads[1]);
+  }
   a.row_lanes = kRopeThreads / a.units;
   const int x = a.heads[0] ? 0 : 1;
   a.tok_inner = a.src_r[x] < a.src_h[x] ? 1 : 0;

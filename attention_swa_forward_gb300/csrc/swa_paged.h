@@ -69,9 +69,10 @@ struct RopeArgs {
   int64_t n_src[3], n_dst[3];            // extents, for the bounds-checked build
   int32_t heads[3];
   int32_t H;          // heads[0] + heads[1] + heads[2]
-  uint32_t h_magic;   // ceil(2^32 / H)
+  uint32_t h_magic;   // ceil(2^32 / H); 8-bit cache: ceil(2^32 / heads[1])
   int32_t D, R;
   int32_t units;      // 2 * VEC-element units of a head row
+  int32_t unit_shift; // 8-bit cache: log2(units)
   int32_t row_lanes;  // rows a CTA takes at a time: threads / units
   int32_t tok, tok_shift;  // tokens per CTA (tok_inner: a power of two, 1 << tok_shift)
   int32_t tok_inner;  // 1: walk the tokens of a head first
