@@ -266,7 +266,11 @@ std::vector<SeqDesc> build_descs(const Plan& plan, bool forward) {
       wmax = std::max(wmax, forward ? fwd_tile_cost(g, s, t) : bwd_tile_cost(g, s, t));
     const int64_t per = std::max({kPieceSteps, g.group * wmax, share});
     const int64_t n_pieces = std::min((g.group * wsink + per - 1) / per, kMostPieces);
-    if (n_pieces > 1) {
+    // (a later tile with sinks has no more steps; about 300 tiles in all have more than `share`)
+    int64_t cut = 0;
+    while (cut < with_sinks && g.group * bwd_tile_cost(g, s, cut) > per) ++cut;
+    for (int64_t t = cut; t < with_sinks; ++t) wmax = std::max(wmax, bwd_tile_cost(g, s, t));
+    if (cut > 0) {
       SeqDesc d{};
       d.q_start = static_cast<int32_t>(s.q_start);
       d.q_len = static_cast<int32_t>(s.q_len);
@@ -274,15 +278,13 @@ std::vector<SeqDesc> build_descs(const Plan& plan, bool forward) {
       d.kv_len = static_cast<int32_t>(s.kv_len);
       d.mask_base = s.mask_base;
       d.b = b;
-      d.tiles = static_cast<int32_t>(with_sinks);
+      d.tiles = static_cast<int32_t>(cut);
       d.heads = heads;
       d.pieces = static_cast<uint16_t>(n_pieces);
       pieces.push_back(Entry{d, (wsink + n_pieces - 1) / n_pieces});
-      tile0 = with_sinks;
-      tiles -= with_sinks;
+      tile0 = cut;
+      tiles -= cut;
       if (tiles == 0) return;
-    } else {
-      wmax = std::max(wmax, wsink);
     }
     const int64_t c0 = forward ? fwd_tile_cost(g, s, tile0) : bwd_tile_cost(g, s, tile0);
     const int64_t c1 = forward ? fwd_tile_cost(g, s, tile0 + tiles - 1) : bwd_tile_cost(g, s, tile0 + tiles - 1);

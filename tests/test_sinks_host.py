@@ -87,3 +87,15 @@ def test_the_oracle_refuses_sinks():
 
     with pytest.raises(ValueError, match="sinks"):
         orc._Call(orc.Problem("BNSD", 1, 1, 8, S_q=4, S_kv=4, sink_tokens=1))
+
+
+def test_a_long_run_of_sinks_behind_few_queries():
+    """Sinks in every key tile: only the tiles that have many steps are cut."""
+    n = 1 << 20
+    g = Geometry("TND", 1, 1, 8, cu_seqlens_q=[60000], cu_seqlens_kv=[n], sparse_mode=4, pre_tokens=100, next_tokens=0,
+                 sink_tokens=n)
+    rows = swa.swa_debug_schedule(swa.Params(g), 1)
+    tiles, count = np.unique(rows[:, 3], return_counts=True)
+    assert np.array_equal(tiles, np.arange(n // T)) and (np.diff(count) <= 0).all() and count[0] == 2 and count[-1] == 1
+    size = lambda sinks: swa.swa_backward_workspace_size(swa.Params(Geometry(**{**g.as_dict(), "sink_tokens": sinks})))
+    assert size(n) - size(0) <= 2 * 304 * 65536
