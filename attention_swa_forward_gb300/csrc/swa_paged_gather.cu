@@ -3,10 +3,12 @@
 // in the other direction.
 //
 // A row of an 8-bit cache is code 2^e, exact in the 16-bit types
-// (swa_paged_mask.cuh).  Bound by HBM: every code is read once and every value
-// written once.  A CTA takes up to 16 tokens, all heads of K and V; its first
-// threads look up their pages, then each thread moves 16 bytes of a row at a time,
-// four rows in flight.
+// (swa_paged_mask.cuh).  A CTA takes up to 16 tokens, all heads of K and V; its
+// first threads look up their pages, then each thread moves 16 bytes of a row at a
+// time, four rows in flight.  Bound by HBM: every code is read once and every value
+// written once.  131072 tokens of 8 + 8 heads of 128, 807 MB: 125 us, 0.95 of the
+// copy rate; 19205 tokens of 96, 74 MB: 18.2, 0.60 (with up to 32 tokens per CTA 127
+// and 24).
 #include "swa_paged.h"
 #include "swa_device.cuh"
 #include "swa_paged_mask.cuh"
