@@ -3,11 +3,11 @@
 //
 // The same work as swa_paged_rows.cuh on half the bytes, so what a warp does per
 // 16 keys sets the time unless it is kept short:
-//  * Each warp has a ring of three groups of 16 keys (six of heads up to 64).  One
+//  * Each warp has a ring of three groups of 16 keys (four of heads up to 64).  One
 //    lane brings a group in: K and V by a TMA box each (swizzled), the exponents by
 //    two copies of 16 bytes, all on one barrier.  Rows that start on 8 bytes only
 //    (head dims that are no multiples of 16) are copied by all lanes, 8 bytes at a
-//    time.
+//    time, into six of heads up to 64.
 //  * The products are transposed, S^T = K Q^T and O^T = V^T P^T, with keys and
 //    columns as the 16 rows of an instruction and 8 query rows as its columns: up
 //    to 8 rows (a token of 8 heads) take half the instructions, exponentials and
@@ -35,9 +35,20 @@
 namespace swa {
 namespace {
 
-template <int DP>
+// CTAs an SM, as registers and shared memory allow.  64 tokens of 100 to 16384
+// keys, 8 key/value heads, 16 rows: heads of 128 284 us with 3, 308 with 2, 439
+// (spills) with 4; of 64 185 with 4, 252 with 2; 8 rows, heads of 64: 142 with 6
+// (and four stages), 151 with 4.  Clusters are few CTAs, and spills would cost
+// them time; copies by all lanes want more stages instead (heads of 40: 162 us, 186
+// with 6 CTAs).
+template <int DP, int NB, bool WIDE, bool CL>
+constexpr int rows8_ctas() {
+  if (!WIDE || CL) return NB == 1 ? 4 : 2;
+  return DP == 64 ? (NB == 1 ? 6 : 4) : (NB == 1 ? 4 : 3);
+}
+template <int DP, bool WIDE>
 struct Rows8Smem {
-  static constexpr int kStages = DP == 128 ? 3 : 6;  // (four CTAs an SM)
+  static constexpr int kStages = DP == 128 ? 3 : (WIDE ? 4 : 6);
   static constexpr int kGroupBytes = 16 * DP;
   alignas(1024) uint8_t ring[kRowsWarps][kStages][2][kGroupBytes];
   alignas(16) int8_t exps[kRowsWarps][kStages][2][16];
@@ -76,10 +87,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // WIDE: rows of the cache start on 16 bytes, and TMA brings them in.  NB: blocks
 // of 8 query rows.
 template <int DP, int NB, bool WIDE, bool CL, int CAP>
-__global__ void __launch_bounds__(kRowsThreads, NB == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>()))
     swa_paged_rows_e4m3_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedTable<CAP> tab,
                                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using Smem = Rows8Smem<DP>;
+  using Smem = Rows8Smem<DP, WIDE>;
   constexpr int kStages = Smem::kStages;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(align1024(smem_raw));
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kRowsThreads, NB == 1 ? 4 : 2)
 template <int DP, int NB, bool WIDE, bool CL, int CAP>
 cudaError_t launch_rows8_t(const PagedArgs& a, const PagedTable<CAP>& tab, const CUtensorMap& mk, const CUtensorMap& mv,
                            cudaStream_t stream) {
-  const size_t smem = sizeof(Rows8Smem<DP>) + 1024;
+  const size_t smem = sizeof(Rows8Smem<DP, WIDE>) + 1024;
   auto kernel = swa_paged_rows_e4m3_kernel<DP, NB, WIDE, CL, CAP>;
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = set_smem_limit(kernel, smem, smem_set);
