@@ -130,6 +130,10 @@ CASES = {
                                                                                              **W)),
     "e4m3_short_units_d72": ([144] * 8, [144, 150, 200, 256, 300, 400, 144, 145], 16, False,
                              dict(N=16, N_kv=16, D=72, pre_tokens=3, **W)),
+    "e4m3_below_chunk": ([20, 3, 1, 1], [10, 0, 0, 1], 16, False, dict(N=4, N_kv=2, D=64, pre_tokens=5, next_tokens=25,
+                                                                     sink_tokens=3, sparse_mode=4)),
+    "e4m3_sixteen_rows": ([2, 1, 2], [900, 33, 16], 16, False, dict(N=8, N_kv=1, D=64, pre_tokens=300, sink_tokens=20, **W)),
+    "e4m3_sixteen_rows_d120": ([4, 3], [250, 77], 48, False, dict(N=8, N_kv=2, D=120, dtype="fp16", **W)),
     "e4m3_mqa_48": ([3], [200], 16, False, dict(N=48, N_kv=1, D=64, **W)),
 }
 
@@ -344,6 +348,55 @@ def test_gather_of_whole_sequences_with_strides(dtype, cache):
     k, v = swa.paged_gather(geom, *[t.to(DEV) for t in p["pages"]], p["table"].to(DEV), p["lens"].to(DEV), k=both[:, 0:3],
                             v=both[:, 3:6], **kw)
     assert torch.equal(k.cpu().double(), torch.cat(p["ks"])) and torch.equal(v.cpu().double(), torch.cat(p["vs"]))
+
+
+@pytest.mark.parametrize("rotary", [0, 48, 64])
+@pytest.mark.parametrize("fused", [False, True])
+def test_append_of_heads_first_rows(rotary, fused):
+    """K, V and Q whose tokens are nearer than their heads: the same codes as of packed rows."""
+    q_lens, kv_lens, N, N_kv, D = [5, 37, 1], [9, 60, 1], 6, 3, 64
+    geom = geometry(q_lens, kv_lens, 16, N=N, N_kv=N_kv, D=D, cache_dtype="e4m3")
+    rope = RopeGeometry("TND", 1, geom.T_q, N, D, N_kv=N_kv, rotary_dim=rotary) if rotary else None
+    if fused and not rotary:
+        return
+    g = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn(n, geom.T_q, D, generator=g).bfloat16().to(DEV) for n in (N, N_kv, N_kv))
+    table, lens = chunk_pages(geom, kv_lens, 2)
+    results = []
+    for first in (lambda t: t.transpose(0, 1), lambda t: t.transpose(0, 1).contiguous()):
+        pages, exps = empty_cache(geom)
+        kw = dict(k_exponents=exps[0], v_exponents=exps[1], rope=rope)
+        if fused:
+            kw["q"] = first(q)
+        out = swa.paged_append(geom, first(k), first(v), *pages, table, lens, **kw)
+        results.append([t.view(torch.uint8) for t in pages] + exps + ([out] if fused else []))
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits():
+    """Codes behind 2^32: append, gather and both kernels give what they give near the start."""
+    q_lens, kv_lens, N_kv, D, P = [1, 70], [300, 200], 8, 128, 256
+    geom = geometry(q_lens, kv_lens, P, N=16, N_kv=N_kv, D=D, cache_dtype="e4m3", **W)
+    whole = geometry(kv_lens, kv_lens, P, N=16, N_kv=N_kv, D=D, cache_dtype="e4m3")
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(whole.T_q, N_kv, D, generator=g).bfloat16().to(DEV) for _ in range(2))
+    q = torch.randn(geom.T_q, 16, D, generator=g).bfloat16().to(DEV)
+    lens = torch.tensor(kv_lens, dtype=torch.int32, device=DEV)
+    results = []
+    for num_pages, first in ((8, 0), (17000, 16990)):  # 4.46 GB of codes each
+        geom.num_pages = whole.num_pages = num_pages
+        table = torch.full((2, geom.max_pages), -1, dtype=torch.int32)
+        table[0, :2], table[1, 0] = torch.tensor([first + 3, first]), first + 2
+        table = table.to(DEV)
+        pages = [torch.empty(geom.page_shape(), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+        exps = [torch.empty(geom.exponent_shape(), dtype=torch.int8, device=DEV) for _ in range(2)]
+        kw = dict(k_exponents=exps[0], v_exponents=exps[1])
+        swa.paged_append(whole, k, v, *pages, table, lens, **kw)
+        results.append([*swa.paged_gather(whole, *pages, table, lens, **kw), *swa.paged_forward(geom, q, *pages, table, lens, **kw)])
+        del pages, exps
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
 
 
 def test_special_values():
@@ -645,6 +698,41 @@ def test_another_stream():
     for a, b in zip(ref, got):
         assert torch.equal(a, b)
     assert torch.equal(k[-1].cpu().double(), p["ks"][1][-1])
+
+
+def test_two_threads_at_once():
+    """Calls of two threads, each with its stream and workspace, give the bits of calls one after the other."""
+    import threading
+    work = []
+    for seed, (q_lens, kv_lens, tree) in enumerate((([61, 1, 4], [900, 700, 300], True), ([150, 1], [400, 2000], False))):
+        geom = geometry(q_lens, kv_lens, 16, N=8, N_kv=2, D=128, pre_tokens=200, sink_tokens=4, cache_dtype="e4m3", **W)
+        p = make(geom, kv_lens, seed + 3, tree)
+        work.append((geom, p, run(geom, p)))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def many(i):
+        geom, p, _ = work[i]
+        dev = {n: t.to(DEV) for n, t in p["kw"].items()}
+        args = [t.to(DEV) for t in (p["q"], *p["pages"], p["table"], p["lens"])]
+        ws = swa.paged_forward_workspace(geom, DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                got[i].append(swa.paged_forward(geom, *args, workspace=ws, **dev))
+        side.synchronize()
+
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for res in got[i]:
+            for x, y in zip(work[i][2], res):
+                assert torch.equal(x, y)
 
 
 def test_python_refusals():
