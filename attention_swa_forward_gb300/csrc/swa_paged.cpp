@@ -18,9 +18,10 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is b
 // does not hold a batch up.  201 sequences of up to 2000 keys and one of 131072:
 // 358 us, 354 with 8192 (twice the CTAs, most with nothing to do), 408 with 4096.
 constexpr int64_t kRowsMostKeys = 16384;
-// The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 202 us, 206 with
-// 4096, 220 with 1024, 250 with 16384; one of 131072: 54 us (76 splits either way).
-constexpr int64_t kRows8MostKeys = 2048;
+// The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 196 us, 198 with
+// 2048, 206 with 4096, 204 with 1024, 250 with 16384; 24 of them 78, 84 with 2048; 64
+// of up to 4000 keys 68.5, 72.6; 64 of 8192 182, 179.
+constexpr int64_t kRows8MostKeys = 1536;
 constexpr int64_t kMostSplits = 65535;  // a grid's second dimension
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)
 constexpr int64_t kClusterSteps = 5;  // key steps a CTA of it takes where more CTAs could be had
@@ -643,6 +644,9 @@ swa_status_t forward_plan(const swa_paged_params_t* p, ForwardPlan& f) {
       const bool q8 = p->cache_dtype == SWA_CACHE_E4M3;
       part.par = std::min(ceil_div(int64_t(kSms) * (q8 ? 4 : 1), items), steps);
       part.cap = std::max((q8 ? kRows8MostKeys : kRowsMostKeys) / step + 2, ceil_div(steps, kMostSplits));
+      // (runs that a few more CTAs than the GPU holds would shorten by little: one
+      // sequence of 131072 keys, 76 splits 54 us, 79 68)
+      if (q8 && ceil_div(steps, part.cap) * 4 <= part.par * 5) part.cap = std::max(part.cap, ceil_div(steps, part.par));
       part.least = 1;
       // Up to 8 splits are one cluster, which joins them without a second
       // launch: a power of two of CTAs, all resident at once.  One token of

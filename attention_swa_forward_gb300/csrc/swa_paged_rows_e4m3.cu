@@ -25,11 +25,11 @@
 //    (the results move with it): 11 bits where that is at least 2^-14 (p <= 2^8),
 //    2^-25 below.  A lane makes the factor of one of the 32 exponents.
 // Bound by HBM where the keys are many: 64 tokens of 100 to 16384 keys, 32 / 8
-// heads of 128, 199 us (1.13 GB; a copy would take 166), of 8192 keys each 179.
+// heads of 128, 196 us (1.13 GB; a copy would take 166), of 8192 keys each 182.
 // (Measured on the first of those on the way here: codes as bf16, by moving bits
 // with integer instructions and multiplying each pair by its row's power of two,
 // 765 instructions a group, 448 us; as fp16 394; by TMA instead of copies by all
-// lanes 317; transposed, and in shorter runs of keys, 199.)
+// lanes 317; transposed, and in shorter runs of keys, 196.)
 #include "swa_paged_rows_end.cuh"
 
 namespace swa {

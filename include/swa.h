@@ -382,7 +382,7 @@ typedef struct {
                                   default): max_pages * page_size.  How the keys are split over the GPU
                                   follows from it, whatever the lengths are: without a window, up to 16
                                   query rows of a sequence and key/value head take a CTA, and up to 8 KB
-                                  of workspace, per 16384 keys of this bound (2048 with an 8-bit cache) */
+                                  of workspace, per 16384 keys of this bound (1536 with an 8-bit cache) */
   double scale;                /* score scale, default 1.0 */
   int64_t pre_tokens;          /* BAND, around each token's position; defaults 2147483647 */
   int64_t next_tokens;
