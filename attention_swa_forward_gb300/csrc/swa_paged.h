@@ -234,7 +234,8 @@ SWA_PAGED_HD PagedKeys paged_keys(const ArgsOf<X>& a, int kv_len, int q_len, int
   if (a.sparse_mode == 4) {
     const bool tree = tree_of<X>(a) != nullptr;
     const int p0 = kv_len - q_len + (tree ? 0 : tok0), p1 = p0 + n_tok - 1;
-    k.lo = p0 - a.pre > 0 ? p0 - a.pre : 0;
+    const int pre = tree && a.pre < 0 ? 0 : a.pre;  // (a window that begins ahead still leaves a tree its chunk)
+    k.lo = p0 - pre > 0 ? p0 - pre : 0;
     if (!tree) k.hi = p1 + a.next < k.hi ? p1 + a.next : k.hi;
     if (const int sinks = sinks_of<X>(a); sinks > 0) {
       const int n = sinks < k.hi + 1 ? sinks : k.hi + 1;
