@@ -73,10 +73,9 @@ __device__ __forceinline__ uint32_t exp_factor(int e) {
     return static_cast<uint32_t>(max(e, kExpLeastBf16) + 239) << 7;
   }
 }
-// 2^e in fp32: 0 below its normal range, NaN above kExpMost.
-__device__ __forceinline__ float exp_f32(int e, int shift) {
-  const int x = max(e, kExpLeastBf16) + shift + 127;
-  return e > kExpMost ? __int_as_float(0x7FC00000) : __int_as_float(max(x, 0) << 23);
+// 2^e in fp32, NaN above kExpMost.
+__device__ __forceinline__ float exp_f32(int e) {
+  return e > kExpMost ? __int_as_float(0x7FC00000) : __int_as_float((max(e, kExpLeastBf16) + 127) << 23);
 }
 // Elementwise product of two pairs.
 template <bool F16>

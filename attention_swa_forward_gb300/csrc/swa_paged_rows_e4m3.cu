@@ -21,15 +21,21 @@
 //  * Products are fp16 whatever the type of q, which is brought into range by a
 //    power of two per row (exactly, but for bits below 2^-39 of its largest).  The
 //    exponent of a key multiplies its scores in fp32; that of a value goes into
-//    its weight, rounded to fp16 as p 2^(e - E + 7), E the largest exponent so far
-//    (the results move with it): 11 bits where that is at least 2^-14 (p <= 2^8),
-//    2^-25 below.  A lane makes the factor of one of the 32 exponents.
+//    its weight, rounded to fp16 as w = p 2^e ref: 11 bits down to 2^-14, 2^-25
+//    below.  The power of two `ref` is a query row's own, and so what a row gets
+//    does not depend on values that it does not see or gives no weight: it is
+//    brought down, and the row's result with it, where a weight passes 2^15, to
+//    leave the largest at 2^6 or more (at first it is the most that some row may
+//    need: a weight of 1 on the least exponent).  The running maximum moves in
+//    whole powers of two, and the weights' scale against them, so that weights are
+//    as they were.  A lane makes the factor of one of the 32 exponents.
 // Bound by HBM where the keys are many: 64 tokens of 100 to 16384 keys, 32 / 8
-// heads of 128, 196 us (1.13 GB; a copy would take 166), of 8192 keys each 182.
+// heads of 128, 199 us (1.13 GB; a copy would take 166), of 8192 keys each 181.
 // (Measured on the first of those on the way here: codes as bf16, by moving bits
 // with integer instructions and multiplying each pair by its row's power of two,
 // 765 instructions a group, 448 us; as fp16 394; by TMA instead of copies by all
-// lanes 317; transposed, and in shorter runs of keys, 196.)
+// lanes 317; transposed, and in shorter runs of keys, 196; with `ref` a row's own instead of
+// one for all that the warp has seen, 199.)
 #include "swa_paged_rows_end.cuh"
 
 namespace swa {
@@ -76,6 +82,12 @@ template <int DP>
 __device__ __forceinline__ int place(int r, int c) {
   return r * DP + ((c ^ (DP == 128 ? r & 7 : (r >> 1) & 3)) << 4);
 }
+
+// A weight is p 2^e ref with p <= 2^8 and e <= kExpMost: at most 2^122.
+constexpr int kRefMost = 7 - kExpLeastBf16;
+constexpr float kWeightMost = 32768.f;  // (fp16 holds twice that)
+// The power of two that x > 0 begins with.
+__device__ __forceinline__ int pow2_exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements, a row's pair a thread.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -181,24 +193,27 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
     return;
   }
 
-  // keys that the thread's rows see, and that every row of the tile sees (swa_paged_rows.cuh)
+  // keys that the thread's rows see, and that every row of the tile sees (swa_paged_rows.cuh).  Those of 16 rows, whose
+  // registers are all taken, are formed where they are needed, at the ends of what is seen (draft of 4 tokens,
+  // 32 / 8 heads of 128: 285 us, 312 with them kept; one token of 1003 keys 7.7, 7.9 formed there).
   const int prefix = kv_len - w.q_len;
   int row_lo[NB][2], row_hi[NB][2], row_tok[NB][2], all_lo = 0, all_hi = kv_len - 1;
-#pragma unroll
-  for (int x = 0; x < NB; ++x)
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int r = 8 * x + 2 * quad + y;
-      row_tok[x][y] = tok0 + (r < n_rows ? row_token(r, a.gs_magic) : 0);
-      row_lo[x][y] = 0;
-      row_hi[x][y] = kv_len - 1;
-      if (a.sparse_mode == 4) {
-        const int p = token_position(a, w, kv_len, row_tok[x][y]);
-        row_lo[x][y] = max(0, p - a.pre);
-        row_hi[x][y] = min(kv_len - 1, p + a.next);
-      }
-      if (a.tree) row_hi[x][y] = prefix - 1;
+  auto row_keys = [&](int x, int y) {
+    const int r = 8 * x + 2 * quad + y;
+    row_tok[x][y] = tok0 + (r < n_rows ? row_token(r, a.gs_magic) : 0);
+    row_lo[x][y] = 0;
+    row_hi[x][y] = kv_len - 1;
+    if (a.sparse_mode == 4) {
+      const int p = token_position(a, w, kv_len, row_tok[x][y]);
+      row_lo[x][y] = max(0, p - a.pre);
+      row_hi[x][y] = min(kv_len - 1, p + a.next);
     }
+    if (a.tree) row_hi[x][y] = prefix - 1;
+  };
+  if constexpr (NB == 1) {
+    row_keys(0, 0);
+    row_keys(0, 1);
+  }
   if (a.sparse_mode == 4) {
     all_lo = max(0, (a.tree ? kv_len - 1 : prefix + tok0 + n_tok - 1) - a.pre);
     all_hi = min(kv_len - 1, prefix + tok0 + a.next);
@@ -286,7 +301,9 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
       m[x][y] = m_true[x][y] = -INFINITY;
       l[x][y] = 0.f;
     }
-  int v_ref = kExpLeastBf16 - 1;  // E of the weights
+  float ref[NB][2];  // of the weights
+#pragma unroll
+  for (int x = 0; x < NB; ++x) ref[x][0] = ref[x][1] = pow2(kRefMost);
   const bool fold = a.scale_log2 > 0.f;  // the scale folds into the exponent's multiply-add
 
 #pragma unroll 1
@@ -339,19 +356,8 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
         for (int x = 0; x < DP / 32; ++x) vw[t][x] = seen ? vw[t][x] : 0u;
       }
     }
-    const int top = __reduce_max_sync(0xFFFFFFFFu, lane < 16 || e > kExpMost ? kExpLeastBf16 : e);
-    if (top > v_ref) {
-      const float f = pow2(max(v_ref - top, -126));
-#pragma unroll
-      for (int x = 0; x < NB; ++x)
-#pragma unroll
-        for (int t = 0; t < DP / 16; ++t)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[x][t][y] *= f;
-      v_ref = top;
-    }
     // of the scores' keys lane / 4 and lane / 4 + 8
-    const float factor = exp_f32(e, lane < 16 ? 0 : 7 - v_ref);
+    const float factor = exp_f32(e);
     float kf[2], vf[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -382,6 +388,7 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
       for (int x = 0; x < NB; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
+          if constexpr (NB > 1) row_keys(x, y);
           // bit t: key j0 + t is a token of the chunk that the row sees
           const uint32_t drafted = a.tree && j0 - prefix > -16 ? tree_bits(a, w, row_tok[x][y], j0 - prefix) : 0u;
 #pragma unroll
@@ -409,30 +416,56 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
       for (int x = 0; x < NB; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          // (also when m is -inf: 0)
-          const float alpha = m_true[x][y] > m[x][y] ? ex2_approx(m[x][y] - m_true[x][y]) : 1.f;
-          m[x][y] = m_true[x][y];
-          l[x][y] *= alpha;
+          // to the next whole number (from -inf: all so far is 0)
+          const float d = m_true[x][y] > m[x][y] ? ceilf(m_true[x][y]) - m[x][y] : 0.f;
+          m[x][y] = d > 0.f ? ceilf(m_true[x][y]) : m[x][y];
+          l[x][y] *= ex2_approx(-d);
+          const int up = min(__float2int_rn(fminf(d, 256.f)), kRefMost - pow2_exponent(ref[x][y]));
+          ref[x][y] *= pow2(up);
+          const float f = ex2_approx(up - d);  // (1 but where ref is at its most)
 #pragma unroll
           for (int t = 0; t < DP / 16; ++t) {
-            o[x][t][y] *= alpha;
-            o[x][t][2 + y] *= alpha;
+            o[x][t][y] *= f;
+            o[x][t][2 + y] *= f;
+          }
+        }
+    }
+    float wt[NB][4], most = 0.f;  // weights of the values, as sc
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float ms = m[x][y] == -INFINITY ? 0.f : m[x][y], c = fold ? c_row[x][y] : 1.f;
+        const float p0 = ex2_approx(fmaf(sc[x][y], c, -ms)), p1 = ex2_approx(fmaf(sc[x][2 + y], c, -ms));
+        l[x][y] += p0 + p1;
+        wt[x][y] = p0 * (vf[0] * ref[x][y]);
+        wt[x][2 + y] = p1 * (vf[1] * ref[x][y]);
+        most = fmaxf(most, fmaxf(wt[x][y], wt[x][2 + y]));
+      }
+    if (__any_sync(0xFFFFFFFFu, most > kWeightMost)) {
+#pragma unroll
+      for (int x = 0; x < NB; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float top = fmaxf(wt[x][y], wt[x][2 + y]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          const float f = top > kWeightMost ? pow2(6 - pow2_exponent(top)) : 1.f;
+          ref[x][y] *= f;
+          wt[x][y] *= f;
+          wt[x][2 + y] *= f;
+#pragma unroll
+          for (int t = 0; t < DP / 16; ++t) {
+            o[x][t][y] *= f;
+            o[x][t][2 + y] *= f;
           }
         }
     }
     uint32_t p[NB][2];  // P^T as B fragments: keys 2 quad + {0, 1}, {8, 9} of row 8 x + lane / 4
 #pragma unroll
     for (int x = 0; x < NB; ++x) {
-      float pr[4];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const float ms = m[x][y] == -INFINITY ? 0.f : m[x][y], c = fold ? c_row[x][y] : 1.f;
-        pr[y] = ex2_approx(fmaf(sc[x][y], c, -ms));
-        pr[2 + y] = ex2_approx(fmaf(sc[x][2 + y], c, -ms));
-        l[x][y] += pr[y] + pr[2 + y];
-      }
-      p[x][0] = transpose8(pack2<true>(pr[0] * vf[0], pr[1] * vf[0]));
-      p[x][1] = transpose8(pack2<true>(pr[2] * vf[1], pr[3] * vf[1]));
+      p[x][0] = transpose8(pack2<true>(wt[x][0], wt[x][1]));
+      p[x][1] = transpose8(pack2<true>(wt[x][2], wt[x][3]));
     }
 #pragma unroll
     for (int t = 0; t < DP / 16; ++t) {
@@ -465,7 +498,7 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
         s.ml[warp][r][0] = m_true[x][y];
         s.ml[warp][r][1] = l[x][y] * f;
       }
-      const float fo = f * pow2(v_ref - 7);
+      const float fo = f * pow2(-pow2_exponent(ref[x][y]));
       float* dst = so + (warp * kRowsTile + r) * RowsEnd<DP>::kOPitch + row * (DP / 8);
 #pragma unroll
       for (int t = 0; t < DP / 8; t += 4)

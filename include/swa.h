@@ -415,10 +415,10 @@ typedef enum { SWA_CACHE_SAME = 0, SWA_CACHE_E4M3 = 1 } swa_cache_t;
  * is not defined (NaN or 480 * 2^e).
  * A slot that no query of a call sees is ignored, its exponent included.
  * Attention of up to 16 query rows per sequence and key/value head rounds the
- * weight of a value to fp16, relative to the largest exponent E among the
- * sequence's visible values: to 11 bits down to an exponent of E - 21, and to
- * 2^(E - 32) below; q (bf16) loses what is below 2^-39 of its row's largest.  With
- * more rows the keys and values are exact and the weights as without the cache. */
+ * weight of a value with its exponent, P * 2^exponent, to fp16 relative to the
+ * largest that the query row has: to 11 bits down to 2^-20 of it, and to 2^-31 of it
+ * below; q (bf16) loses what is below 2^-39 of its row's largest.  With more rows
+ * the keys and values are exact and the weights as without the cache. */
 
 SWA_API void swa_paged_params_default(swa_paged_params_t *p);
 
