@@ -73,9 +73,9 @@ __device__ __forceinline__ uint32_t exp_factor(int e) {
     return static_cast<uint32_t>(max(e, kExpLeastBf16) + 239) << 7;
   }
 }
-// 2^e in fp32, NaN above kExpMost.
+// 2^e in fp32, NaN above kExpMost (e not below the least).
 __device__ __forceinline__ float exp_f32(int e) {
-  return e > kExpMost ? __int_as_float(0x7FC00000) : __int_as_float((max(e, kExpLeastBf16) + 127) << 23);
+  return e > kExpMost ? __int_as_float(0x7FC00000) : __int_as_float((e + 127) << 23);
 }
 // Elementwise product of two pairs.
 template <bool F16>

@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
   float ref[NB][2];  // of the weights
 #pragma unroll
   for (int x = 0; x < NB; ++x) ref[x][0] = ref[x][1] = pow2(kRefMost);
+  const int least = a.f16 ? kExpLeastF16 : kExpLeastBf16;  // an exponent below it counts as it
   const bool fold = a.scale_log2 > 0.f;  // the scale folds into the exponent's multiply-add
 
 #pragma unroll 1
@@ -343,12 +344,13 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
         vw[t][1] = v.y;
       }
     }
-    int e = lds_s8(smem_u32(s.exps[warp][st][0]) + lane);  // lanes 0-15: of the keys; 16-31: of the values
+    // lanes 0-15: of the keys; 16-31: of the values
+    int e = max(lds_s8(smem_u32(s.exps[warp][st][0]) + lane), least);
     __syncwarp();
     issue(it + kStages);  // the stage is free
     // what slots that no row sees hold counts for nothing, a NaN's code and exponent neither
     if (j0 < keys.lo || j0 + 15 > keys.hi) {
-      if (!some_see(j0 + (lane & 15))) e = kExpLeastBf16;
+      if (!some_see(j0 + (lane & 15))) e = least;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const bool seen = some_see(j0 + 2 * quad + (t & 1) + 8 * (t >> 1));
