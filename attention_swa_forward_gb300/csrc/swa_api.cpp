@@ -677,8 +677,17 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
     return le;
   };
   e = run_tables(kv_descs, key_major, key_major);
-  if (t_ev[3]) cudaEventRecord(t_ev[3], s);
   if (e != cudaSuccess) return cuda_fail(e, "backward dK/dV launch");
+  a.part_base = 0;
+  auto join = [&](const auto& t) {
+    const int64_t n = piece_items(t.d, t.count);
+    const cudaError_t le = n > 0 ? launch_backward_join(a, t, static_cast<int>(n), s) : cudaSuccess;
+    a.part_base += n;
+    return le;
+  };
+  e = run_tables(kv_descs, join, join);
+  if (t_ev[3]) cudaEventRecord(t_ev[3], s);
+  if (e != cudaSuccess) return cuda_fail(e, "backward dK/dV join launch");
   // query-major pass: dQ (one work item per query tile)
   const std::vector<SeqDesc> q_descs = build_descs(plan, true);
   if (t_ev[4]) cudaEventRecord(t_ev[4], s);
@@ -689,16 +698,6 @@ swa_status_t swa_backward(const swa_params_t* p, const void* q, const void* k, c
   e = run_tables(q_descs, query_major, query_major);
   if (t_ev[5]) cudaEventRecord(t_ev[5], s);
   if (e != cudaSuccess) return cuda_fail(e, "backward dQ launch");
-  // (behind the query-major pass, which ends after the key-major one)
-  a.part_base = 0;
-  auto join = [&](const auto& t) {
-    const int64_t n = piece_items(t.d, t.count);
-    const cudaError_t le = n > 0 ? launch_backward_join(a, t, static_cast<int>(n), s) : cudaSuccess;
-    a.part_base += n;
-    return le;
-  };
-  e = run_tables(kv_descs, join, join);
-  if (e != cudaSuccess) return cuda_fail(e, "backward dK/dV join launch");
   return SWA_OK;
 }
 

@@ -581,8 +581,9 @@ SWA_API swa_status_t swa_workspace_status(const void *workspace, swa_stream_t st
  * stop, dK/dV start, dK/dV stop, dQ start, dQ stop, preprocess start,
  * preprocess stop}.  Later calls on this thread record each pair on their
  * stream immediately around the corresponding kernel launch (swa_forward's
- * forward kernel; swa_backward's key-major dK/dV kernel, query-major dQ
- * kernel and D / lse2 preprocess).  No other effect. */
+ * forward kernel; swa_backward's key-major dK/dV kernel, with sink_tokens and
+ * the sum of its pieces, query-major dQ kernel and D / lse2 preprocess).  No
+ * other effect. */
 SWA_API void swa_set_timing_events(void *const *events);
 
 /* Test and inspection support (additions of this library; the pages have no
