@@ -106,11 +106,11 @@ __device__ __forceinline__ uint2 values4(uint32_t x, uint32_t factor) {
   return make_uint2(mul2<F16>(lo, factor), mul2<F16>(hi, factor));
 }
 // The power of two that brings a row of magnitude `top` (bits of |x|) to [2^14, 2^15),
-// as far as 2^+-100 go: its fp16 values then lose nothing of a bf16's 8 bits
-// down to 2^-29 of the largest.
+// as far as 2^100 goes: its fp16 values then lose nothing of a bf16's 8 bits
+// down to 2^-29 of the largest.  A row of zeros stays.
 __device__ __forceinline__ int row_shift(uint32_t top) {
   const int e = static_cast<int>(top >> 23) - 127;
-  return min(max(14 - e, -100), 100);
+  return top == 0 ? 0 : min(14 - e, 100);
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
 

@@ -38,6 +38,8 @@
 // one for all that the warp has seen, 199.)
 #include "swa_paged_rows_end.cuh"
 
+#include <cfloat>
+
 namespace swa {
 namespace {
 
@@ -172,7 +174,12 @@ __global__ void __launch_bounds__(kRowsThreads, (rows8_ctas<DP, NB, WIDE, CL>())
           qf[x][kk][y] = pack2<true>(__uint_as_float(qf[x][kk][y] << 16) * up,
                                      __uint_as_float(qf[x][kk][y] & 0xFFFF0000u) * up);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) c_row[x][y] *= __shfl_sync(0xFFFFFFFFu, down, (2 * quad + y) * 4);
+      for (int y = 0; y < 2; ++y) {
+        // a positive scale stays one, and a number: 2^-126 of any score is nothing, and 0 or infinity would make NaN
+        // of a masked score or of one of 0
+        const float c = a.scale_log2 * __shfl_sync(0xFFFFFFFFu, down, (2 * quad + y) * 4);
+        c_row[x][y] = fminf(fmaxf(c, a.scale_log2 > 0.f ? FLT_MIN : -FLT_MAX), FLT_MAX);
+      }
     }
   }
 

@@ -491,8 +491,9 @@ SWA_API swa_status_t swa_paged_gather(const swa_paged_params_t *p, const void *k
  * p + next_tokens and 0 <= j < kv_lens[b] (mode 4; with sink_tokens also the
  * keys j < sink_tokens up to p + next_tokens), or every key (mode 0).  A
  * row that sees no key gets out = 0, softmax_max = -inf, softmax_sum = 0.
- * Scores, statistics and sums are fp32; exp(scale q.k - maximum) is rounded to
- * p->dtype before the product with V, as in swa_forward, and out once more.
+ * Scores (q.k before the scale too), statistics and sums are fp32; exp(scale q.k -
+ * maximum) is rounded to p->dtype before the product with V, as in swa_forward,
+ * and out once more.
  *   q             device, p->dtype, [T_q, N, D], may be strided, its rows and
  *                 heads apart (no stride 0)
  *   k_pages, v_pages, block_table, table_stride, kv_lens
