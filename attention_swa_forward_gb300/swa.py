@@ -566,11 +566,12 @@ class PagedParams:
         c.scale, c.sparse_mode = float(geom.scale), int(geom.sparse_mode)
         c.pre_tokens, c.next_tokens = int(geom.pre_tokens), int(geom.next_tokens)
         c.dtype = DTYPES[geom.dtype]
-        c.sink_tokens, c.cache_dtype = int(geom.sink_tokens), CACHE_DTYPES[geom.cache_dtype]
+        c.sink_tokens = int(getattr(geom, "sink_tokens", 0) or 0)
+        c.cache_dtype = CACHE_DTYPES[getattr(geom, "cache_dtype", "") or ""]
         self.torch_dtype = _TORCH_DTYPES[geom.dtype]
         self._ref = ctypes.byref(c)
         self.q_shape = (geom.T_q, geom.N, geom.D)
-        self.kv_shape = (geom.T_q, geom.n_kv, geom.D)
+        self.kv_shape = (geom.T_q, c.N_kv or geom.N, geom.D)
         self.stat_shape = (geom.T_q, geom.N)
         self.addr = ctypes.addressof(c)
 
