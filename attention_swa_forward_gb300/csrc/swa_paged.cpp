@@ -18,9 +18,11 @@ constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements; a TMA stride is b
 // does not hold a batch up.  201 sequences of up to 2000 keys and one of 131072:
 // 358 us, 354 with 8192 (twice the CTAs, most with nothing to do), 408 with 4096.
 constexpr int64_t kRowsMostKeys = 16384;
-// The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 196 us, 198 with
-// 2048, 206 with 4096, 204 with 1024, 250 with 16384; 24 of them 78, 84 with 2048; 64
-// of up to 4000 keys 68.5, 72.6; 64 of 8192 182, 179.
+// The same over an 8-bit cache.  64 sequences of 100 to 16384 keys: 199 us, 201 with
+// 2048, 206 with 4096, 207 with 1024, 250 with 16384; 24 of them 79, 85 with 2048; 64
+// of up to 4000 keys 69.5, 73.7; 64 of 8192 181, 178.  (A bound on the lengths far above
+// them costs more with short runs, whose CTAs start to find nothing: those 64 sequences
+// 294 us with a bound of 131072 keys, 1066 with 2^20; over a 16-bit cache 397, 401 and 412.)
 constexpr int64_t kRows8MostKeys = 1536;
 constexpr int64_t kMostSplits = 65535;  // a grid's second dimension
 constexpr int64_t kClusterMost = 8;   // CTAs of a cluster of the few-row kernel (any GPU schedules 8)

@@ -44,11 +44,10 @@ namespace swa {
 namespace {
 
 // CTAs an SM, as registers and shared memory allow.  64 tokens of 100 to 16384
-// keys, 8 key/value heads, 16 rows: heads of 128 284 us with 3, 308 with 2, 439
-// (spills) with 4; of 64 185 with 4, 252 with 2; 8 rows, heads of 64: 142 with 6
-// (and four stages), 151 with 4.  Clusters are few CTAs, and spills would cost
-// them time; copies by all lanes want more stages instead (heads of 40: 162 us, 186
-// with 6 CTAs).
+// keys, 8 key/value heads, 16 rows: heads of 128 285 us with 3, 312 with 2, 427
+// (spills) with 4; of 64 191 with 4, 250 with 2; 8 rows, heads of 64: 144 with 6,
+// 149 with 4.  Clusters are few CTAs, and spills would cost them time; copies by
+// all lanes want more stages instead (heads of 40: 162 us, 186 with 6 CTAs).
 template <int DP, int NB, bool WIDE, bool CL>
 constexpr int rows8_ctas() {
   if (!WIDE || CL) return NB == 1 ? 4 : 2;
