@@ -535,12 +535,13 @@ SWA_API swa_status_t swa_paged_forward(const swa_paged_params_t *p, const void *
  * those that swa_paged_forward's formula gives for position kv_lens[b] - q_len_b +
  * depth, depth[t] being its distance from the root (held within [0, q_len_b - 1]);
  * with next_tokens >= 0, as a tree needs, that is its window and the sinks (a
- * negative pre_tokens leaves the sinks).  The tree alone decides on the chunk's own keys.  The slots hold the chunk in its
- * order, whatever the depths: its tokens are appended as they come, rotated by
- * `positions` of kv_lens[b] - q_len_b + depth.  What is read: pages of keys from
- * the root's window on, the sinks' and the chunk's, every slot of the chunk
- * counting as seen.  Afterwards the accepted tokens are appended again in their
- * order, over the chunk.
+ * negative pre_tokens leaves the sinks).  The tree alone decides on the chunk's
+ * own keys.  The slots hold the chunk in its order, whatever the depths: its
+ * tokens are appended as they come, rotated by `positions` of
+ * kv_lens[b] - q_len_b + depth.  What is read: pages of keys from the root's window
+ * on, the sinks' and the chunk's, every slot of the chunk counting as seen.
+ * Afterwards the accepted tokens are appended again in their order, over the
+ * chunk.
  *   extra         NULL, or host; the pointers in it are device memory:
  *     k_exponents, v_exponents
  *                 as for swa_paged_append_ext; NULL iff the cache is not 8-bit.

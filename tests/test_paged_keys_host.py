@@ -8,7 +8,6 @@ import pytest
 
 from attention_swa_forward_gb300 import build as B
 
-CUDA = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
 SOURCE = """#include <cstdio>
 #include "swa_paged.h"
 using namespace swa;
@@ -32,9 +31,10 @@ int main() {
 
 @pytest.fixture(scope="module")
 def keys_of(tmp_path_factory):
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
     d = tmp_path_factory.mktemp("keys")
     (d / "keys.cpp").write_text(SOURCE)
-    subprocess.run(["g++", "-O1", "-std=c++17", "-I", B.CSRC, "-I", B.INCLUDE, "-I", CUDA, str(d / "keys.cpp"), "-o",
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I", B.CSRC, "-I", B.INCLUDE, "-I", cuda, str(d / "keys.cpp"), "-o",
                     str(d / "keys")], check=True)
 
     def call(cases):
